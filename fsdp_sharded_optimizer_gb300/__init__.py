@@ -7,6 +7,10 @@ weights (the all-gather).  ZeRO-3 adds the per-unit gather and the per-unit
 reduce-scatter, scheduled with next-unit prefetch on a side stream
 (``zero3_step``, natively or as a CUDA graph).
 
+``zero_embed_*``, ``zero_block_norm_*`` and ``zero_distill_*`` are operators of
+the model that is trained: the embedding, the norms around a block and the
+distillation loss, each with its gradient.
+
 The public calls carry the C ABI's names (include/zero.h) and live in
 ``_binding``.  They are loaded on first use, so that ``build`` can be imported
 before the library exists; using any of them without a built library raises
@@ -28,7 +32,12 @@ _PUBLIC = ("ZERO_DEFAULT_ALIGN", "ZERO_CHUNK_ELEMS", "ZERO_EALIGN", "ZERO_ECUDA"
            "zero3_update_unit_reduced", "zero3_step_f32grads", "zero3_accumulate_unit",
            "zero3_reduce_scatter_unit_accumulated", "zero_reshard_f32", "zero3_plan_microbatch",
            "zero3_step_microbatch", "zero_step_stage12_checked",
-           "zero3_reduce_scatter_unit_checked", "zero3_step_checked")
+           "zero3_reduce_scatter_unit_checked", "zero3_step_checked",
+           "zero_embed_forward", "zero_embed_backward", "zero_embed_scratch_bytes",
+           "zero_block_norm_forward", "zero_block_norm_backward",
+           "zero_block_norm_scratch_bytes", "zero_distill_forward",
+           "zero_distill_forward_backward", "zero_block_norm_t", "zero_block_norm_grads_t",
+           "zero_distill_t")
 
 __all__ = list(_PUBLIC)
 

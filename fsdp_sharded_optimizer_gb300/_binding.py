@@ -77,6 +77,31 @@ class zero_clip_t(C.Structure):
                 ("norm_coef", C.c_void_p), ("grad_shard", C.c_void_p)]
 
 
+ZERO_TYPE_BF16, ZERO_TYPE_F32, ZERO_TYPE_I32, ZERO_TYPE_I64 = 1, 2, 3, 4
+ZERO_NORM_RMS, ZERO_NORM_LAYER = 0, 1
+
+
+class zero_block_norm_t(C.Structure):
+    _fields_ = [("n_rows", C.c_int64), ("dim", C.c_int64), ("rows_per_gate", C.c_int64),
+                ("kind", C.c_int32), ("post_norm", C.c_int32), ("pre_norm", C.c_int32),
+                ("act_type", C.c_int32), ("res_type", C.c_int32), ("param_type", C.c_int32),
+                ("gate_type", C.c_int32), ("eps", C.c_double), ("residual_scale", C.c_double),
+                ("branch_scale", C.c_double)]
+
+
+class zero_block_norm_grads_t(C.Structure):
+    _fields_ = [("dgate", C.c_void_p), ("dpost_weight", C.c_void_p), ("dpost_bias", C.c_void_p),
+                ("dpre_weight", C.c_void_p), ("dpre_bias", C.c_void_p),
+                ("dgate_type", C.c_int32), ("grad_type", C.c_int32)]
+
+
+class zero_distill_t(C.Structure):
+    _fields_ = [("n_rows", C.c_int64), ("vocab", C.c_int64), ("logits_stride", C.c_int64),
+                ("top", C.c_int32), ("logits_type", C.c_int32), ("teacher_type", C.c_int32),
+                ("id_type", C.c_int32), ("label_type", C.c_int32), ("temperature", C.c_double),
+                ("ce_weight", C.c_double), ("kl_weight", C.c_double)]
+
+
 def clip_args(max_norm, scratch, norm_coef, grad_shard=None):
     """A zero_clip_t for zero3_step from device tensors (scratch of
     zero_clip_scratch_bytes(), norm_coef of 2 floats, and optionally the fp32
@@ -155,6 +180,23 @@ SIGNATURES = {
     "zero_gen_grads_unit": (C.c_int, [_U64, _I64, _F64, _I32, _P, _I32, _P, _P]),
     "zero_gen_master": (C.c_int, [_U64, _F64, _P, _I32, _I32, _P, _P]),
     "zero_cast_bf16": (C.c_int, [_P, _P, _I64, _P]),
+    # table, type, vocab, dim, ids, type, n_tokens, scale, out, type, stream
+    "zero_embed_forward": (C.c_int, [_P, _I32, _I64, _I64, _P, _I32, _I64, _F64, _P, _I32, _P]),
+    "zero_embed_scratch_bytes": (_I64, [_I64, _I64, _I64]),
+    # dout, type, ids, type, n_tokens, scale, dtable, type, vocab, dim, accumulate, scratch,
+    # scratch bytes, stream
+    "zero_embed_backward": (C.c_int, [_P, _I32, _P, _I32, _I64, _F64, _P, _I32, _I64, _I64, _I32,
+                                      _P, _I64, _P]),
+    # norm, x, branch, gate, post weight and bias, pre weight and bias, y, u, stream
+    "zero_block_norm_forward": (C.c_int, [_P] * 11),
+    "zero_block_norm_scratch_bytes": (_I64, [_I64, _I64, _I64]),
+    # norm, dy, du, y, branch, gate, post weight and bias, pre weight, dx, dbranch, grads,
+    # scratch, scratch bytes, stream
+    "zero_block_norm_backward": (C.c_int, [_P] * 13 + [_I64, _P]),
+    # distill, logits, teacher logits, teacher ids, labels, row weight, ce, kl, stream
+    "zero_distill_forward": (C.c_int, [_P] * 9),
+    # ..., ce, kl, dlogits, dlogits stride, stream
+    "zero_distill_forward_backward": (C.c_int, [_P] * 9 + [_I64, _P]),
     "zero_stream_wait": (C.c_int, [_P, _I64]),
     "zero_strerror": (C.c_char_p, [C.c_int]),
 }
@@ -700,3 +742,247 @@ def zero_gen_master(seed, sigma, units, master, stream=None):
 def zero_cast_bf16(src, dst, stream=None):
     _check("zero_cast_bf16", lib.zero_cast_bf16(
         _dev(src, 4, "src"), _dev(dst, 2, "dst"), src.numel(), _stream(stream)))
+
+
+# ------------------------------------------------- operators of the model
+def _shape(what, t, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, shape, tuple(t.shape)))
+
+
+def _float_type(t, what):
+    """ZERO_TYPE_BF16 (bfloat16, or its bits as int16/uint16) or ZERO_TYPE_F32."""
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return ZERO_TYPE_BF16
+    if t.dtype == torch.float32:
+        return ZERO_TYPE_F32
+    raise ValueError("%s must be bf16 or fp32, got %s" % (what, t.dtype))
+
+
+def _index_type(t, what):
+    if t.dtype == torch.int32:
+        return ZERO_TYPE_I32
+    if t.dtype == torch.int64:
+        return ZERO_TYPE_I64
+    raise ValueError("%s must be int32 or int64, got %s" % (what, t.dtype))
+
+
+def _ptr(t, what):
+    """The address of a contiguous device-addressable tensor, None for None."""
+    if t is None:
+        return None
+    if not _addressable(t) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA or pinned host tensor" % what)
+    return t.data_ptr()
+
+
+def _scratch(t):
+    return _ptr(t, "scratch"), t.numel() * t.element_size()
+
+
+def zero_embed_forward(table, ids, out, scale=1.0, stream=None):
+    """out[t, :] = scale * table[ids[t], :]; a row of +0 where the id lies outside the
+    table.  table (V x D) and out (tokens x D): bf16 or fp32; ids: int32 or int64."""
+    if table.dim() != 2:
+        raise ValueError("table must have two dimensions")
+    V, D = table.shape
+    _shape("out", out, *ids.shape, D)
+    _check("zero_embed_forward", lib.zero_embed_forward(
+        _ptr(table, "table"), _float_type(table, "table"), V, D, _ptr(ids, "ids"),
+        _index_type(ids, "ids"), ids.numel(), float(scale), _ptr(out, "out"),
+        _float_type(out, "out"), _stream(stream)))
+
+
+def _bytes(fn, n):
+    if n < 0:
+        raise ZeroError(fn, int(n))
+    return n
+
+
+def zero_embed_scratch_bytes(n_tokens, vocab, dim):
+    return _bytes("zero_embed_scratch_bytes",
+                  lib.zero_embed_scratch_bytes(int(n_tokens), int(vocab), int(dim)))
+
+
+def zero_embed_backward(dout, ids, dtable, scratch, scale=1.0, accumulate=False, stream=None):
+    """dtable[v, :] = (dtable[v, :] if accumulate else 0) + scale * the sum of dout's
+    rows whose id is v, by sorted tokens.  scratch: a device tensor of
+    zero_embed_scratch_bytes(tokens, V, D) bytes."""
+    if dtable.dim() != 2:
+        raise ValueError("dtable must have two dimensions")
+    V, D = dtable.shape
+    _shape("dout", dout, *ids.shape, D)
+    _check("zero_embed_backward", lib.zero_embed_backward(
+        _ptr(dout, "dout"), _float_type(dout, "dout"), _ptr(ids, "ids"), _index_type(ids, "ids"),
+        ids.numel(), float(scale), _ptr(dtable, "dtable"), _float_type(dtable, "dtable"), V, D,
+        1 if accumulate else 0, *_scratch(scratch), _stream(stream)))
+
+
+def _norm_spec(stream_rows, act, gate, params, kind, rows_per_gate, post_norm, pre_norm, eps,
+               residual_scale, branch_scale):
+    """The zero_block_norm_t of a call, with its tensors' shapes and types checked."""
+    if stream_rows.dim() != 2:
+        raise ValueError("the residual stream must have two dimensions")
+    R, D = stream_rows.shape
+    res = _float_type(stream_rows, "the residual stream")
+    for name, t in act.items():
+        if t is not None:
+            _shape(name, t, R, D)
+    types = {_float_type(t, name) for name, t in act.items() if t is not None}
+    if len(types) > 1:
+        raise ValueError("activations must have one type")
+    span = int(rows_per_gate) if rows_per_gate else max(1, R)
+    if gate is not None:
+        _shape("gate", gate, max(1, -(-R // span)), D)
+    for name, t in params.items():
+        if t is not None:
+            _shape(name, t, D)
+    ptypes = {_float_type(t, name) for name, t in params.items() if t is not None}
+    if len(ptypes) > 1:
+        raise ValueError("norm weights and biases must have one type")
+    kinds = {"rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
+    if kind not in kinds:
+        raise ValueError("kind must be 'rms' or 'layer'")
+    return zero_block_norm_t(R, D, span, kinds[kind], int(bool(post_norm)), int(bool(pre_norm)),
+                             types.pop() if types else res, res,
+                             ptypes.pop() if ptypes else ZERO_TYPE_BF16,
+                             _float_type(gate, "gate") if gate is not None else ZERO_TYPE_BF16,
+                             float(eps), float(residual_scale), float(branch_scale))
+
+
+def zero_block_norm_forward(x, branch=None, gate=None, post_weight=None, post_bias=None,
+                            pre_weight=None, pre_bias=None, y=None, u=None, kind="rms",
+                            rows_per_gate=None, post_norm=True, pre_norm=True, eps=1e-6,
+                            residual_scale=1.0, branch_scale=1.0, stream=None):
+    """y = residual_scale * x + branch_scale * gate * norm(branch), u = norm(y).
+
+    x, y (rows x D) of the residual type, branch, u (rows x D) of the activations'
+    type, gate (gate rows x D; row i uses gate row i // rows_per_gate, all rows the
+    one gate row by default), weights and biases (D).  post_norm / pre_norm False
+    leaves out the branch's norm / the norm of y (u is then None).  Without a
+    branch (before the first block) u = norm(x), and y is None."""
+    if branch is None:
+        post_norm = False
+    if y is not None:
+        _shape("y", y, *x.shape)
+        if _float_type(y, "y") != _float_type(x, "x"):
+            raise ValueError("x and y must have one type")
+    spec = _norm_spec(x, {"branch": branch, "u": u}, gate,
+                      {"post_weight": post_weight, "post_bias": post_bias,
+                       "pre_weight": pre_weight, "pre_bias": pre_bias}, kind, rows_per_gate,
+                      post_norm, pre_norm, eps, residual_scale, branch_scale)
+    _check("zero_block_norm_forward", lib.zero_block_norm_forward(
+        C.byref(spec), _ptr(x, "x"), _ptr(branch, "branch"), _ptr(gate, "gate"),
+        _ptr(post_weight, "post_weight"), _ptr(post_bias, "post_bias"),
+        _ptr(pre_weight, "pre_weight"), _ptr(pre_bias, "pre_bias"), _ptr(y, "y"), _ptr(u, "u"),
+        _stream(stream)))
+
+
+def zero_block_norm_scratch_bytes(n_rows, dim, rows_per_gate=None):
+    span = int(rows_per_gate) if rows_per_gate else max(1, int(n_rows))
+    return _bytes("zero_block_norm_scratch_bytes",
+                  lib.zero_block_norm_scratch_bytes(int(n_rows), int(dim), span))
+
+
+def zero_block_norm_backward(y, scratch, dy=None, du=None, branch=None, gate=None,
+                             post_weight=None, post_bias=None, pre_weight=None, dx=None,
+                             dbranch=None, dgate=None, dpost_weight=None, dpost_bias=None,
+                             dpre_weight=None, dpre_bias=None, kind="rms", rows_per_gate=None,
+                             post_norm=True, pre_norm=True, eps=1e-6, residual_scale=1.0,
+                             branch_scale=1.0, stream=None):
+    """The gradient of zero_block_norm_forward, given dy and du (either may be None: 0;
+    du exactly when pre_norm is False).  y: the stream the forward call wrote (x
+    where it had no branch).  Writes the gradients that are given: dx, dbranch
+    (with a branch), dgate, and the weights' and biases' sums over the rows, which
+    may lie in a rank's gradient buffer.  scratch: a device tensor of
+    zero_block_norm_scratch_bytes(rows, D, rows_per_gate) bytes."""
+    if branch is None:
+        post_norm = False
+    for name, t in (("dy", dy), ("dx", dx)):
+        if t is not None:
+            _shape(name, t, *y.shape)
+            if _float_type(t, name) != _float_type(y, "y"):
+                raise ValueError("y and %s must have one type" % name)
+    spec = _norm_spec(y, {"branch": branch, "du": du, "dbranch": dbranch}, gate,
+                      {"post_weight": post_weight, "post_bias": post_bias,
+                       "pre_weight": pre_weight}, kind, rows_per_gate, post_norm, pre_norm, eps,
+                      residual_scale, branch_scale)
+    grads = {"dpost_weight": dpost_weight, "dpost_bias": dpost_bias, "dpre_weight": dpre_weight,
+             "dpre_bias": dpre_bias}
+    for name, t in grads.items():
+        if t is not None:
+            _shape(name, t, spec.dim)
+    types = {_float_type(t, name) for name, t in grads.items() if t is not None}
+    if len(types) > 1:
+        raise ValueError("the gradients of weights and biases must have one type")
+    if dgate is not None:
+        _shape("dgate", dgate, max(1, -(-spec.n_rows // spec.rows_per_gate)), spec.dim)
+    out = zero_block_norm_grads_t(
+        _ptr(dgate, "dgate"), *[_ptr(t, name) for name, t in grads.items()],
+        _float_type(dgate, "dgate") if dgate is not None else ZERO_TYPE_BF16,
+        types.pop() if types else ZERO_TYPE_BF16)
+    _check("zero_block_norm_backward", lib.zero_block_norm_backward(
+        C.byref(spec), _ptr(dy, "dy"), _ptr(du, "du"), _ptr(y, "y"), _ptr(branch, "branch"),
+        _ptr(gate, "gate"), _ptr(post_weight, "post_weight"), _ptr(post_bias, "post_bias"),
+        _ptr(pre_weight, "pre_weight"), _ptr(dx, "dx"), _ptr(dbranch, "dbranch"), C.byref(out),
+        *_scratch(scratch), _stream(stream)))
+
+
+def _matrix(t, what):
+    """Address and row stride of a matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % what)
+    if not _addressable(t) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be CUDA or pinned host memory with contiguous rows" % what)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight, temperature,
+                  ce_weight, kl_weight):
+    ptr, stride = _matrix(logits, "logits")
+    R, V = logits.shape
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must have two dimensions")
+    K = teacher_ids.shape[1]
+    _shape("teacher_ids", teacher_ids, R, K)
+    _shape("teacher_logits", teacher_logits, R, K)
+    for name, t in (("ce", ce), ("kl", kl), ("labels", labels), ("row_weight", row_weight)):
+        if t is not None:
+            _shape(name, t, R)
+            if name != "labels" and t.dtype != torch.float32:
+                raise ValueError("%s must be fp32" % name)
+    spec = zero_distill_t(R, V, stride, K, _float_type(logits, "logits"),
+                          _float_type(teacher_logits, "teacher_logits"),
+                          _index_type(teacher_ids, "teacher_ids"),
+                          _index_type(labels, "labels") if labels is not None else ZERO_TYPE_I64,
+                          float(temperature), float(ce_weight), float(kl_weight))
+    return spec, (C.byref(spec), ptr, _ptr(teacher_logits, "teacher_logits"),
+                  _ptr(teacher_ids, "teacher_ids"), _ptr(labels, "labels"),
+                  _ptr(row_weight, "row_weight"), _ptr(ce, "ce"), _ptr(kl, "kl"))
+
+
+def zero_distill_forward(logits, teacher_logits, teacher_ids, ce, kl, labels=None,
+                         row_weight=None, temperature=1.0, stream=None):
+    """Each row's distillation loss kl (temperature^2 * KL(teacher || student), the
+    teacher given by its top logits and their ids, -1 for no entry) and cross
+    entropy ce (0 without a label in [0, V)).  logits (rows x V): bf16 or fp32,
+    rows contiguous, any row stride; teacher_logits, teacher_ids (rows x K); ce,
+    kl, row_weight (rows): fp32; rows of weight 0 are not read."""
+    _, args = _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight,
+                            temperature, 0.0, 1.0)
+    _check("zero_distill_forward", lib.zero_distill_forward(*args, _stream(stream)))
+
+
+def zero_distill_forward_backward(logits, teacher_logits, teacher_ids, ce, kl, dlogits,
+                                  labels=None, row_weight=None, temperature=1.0, ce_weight=0.0,
+                                  kl_weight=1.0, stream=None):
+    """zero_distill_forward, and dlogits = the gradient of the sum over the rows of
+    row_weight * (ce_weight * ce + kl_weight * kl).  dlogits may be logits."""
+    spec, args = _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight,
+                               temperature, ce_weight, kl_weight)
+    ptr, stride = _matrix(dlogits, "dlogits")
+    _shape("dlogits", dlogits, spec.n_rows, spec.vocab)
+    if _float_type(dlogits, "dlogits") != spec.logits_type:
+        raise ValueError("logits and dlogits must have one type")
+    _check("zero_distill_forward_backward", lib.zero_distill_forward_backward(
+        *args, ptr, stride, _stream(stream)))

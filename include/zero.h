@@ -786,6 +786,184 @@ int zero_stream_wait(cudaStream_t stream, int64_t timeout_ms);
  * it). */
 const char* zero_strerror(int code);
 
+/* ---------------------------------------------------------------------
+ * Operators of the model around the step: what a training loop computes with
+ * the weights that the all-gather or the unit gather delivers, and whose
+ * gradients the reduce-scatter takes, besides its matrix products.  No page
+ * defines them; each states its formula.
+ *
+ * Conventions beyond those above:
+ *  - Tensors are row-major.  A weight or a gradient may lie anywhere inside a
+ *    flat unit or rank buffer, so pointers need the alignment of their element
+ *    only (ZERO_EALIGN otherwise); wide loads are used where addresses allow.
+ *  - All arithmetic and all sums are fp32; an output of bf16 is rounded once,
+ *    to nearest even.  Sums have a fixed order: the same call on the same
+ *    inputs gives the same bits.
+ *  - Scratch is the caller's, 16-byte aligned, of the size the *_scratch_bytes
+ *    call gives; calls that share it must be ordered.  Its contents need not
+ *    be kept from one call to the next.
+ *  - Outputs must not overlap inputs unless the call says so.
+ * ------------------------------------------------------------------- */
+
+#define ZERO_TYPE_BF16 1
+#define ZERO_TYPE_F32 2
+#define ZERO_TYPE_I32 3
+#define ZERO_TYPE_I64 4
+
+/* zero_embed_forward -- embedding lookup with scaling:
+ *   out[t, :] = scale * table[ids[t], :]        t < n_tokens
+ * A token whose id lies outside [0, vocab) (padding) gets a row of +0.
+ *   table   [vocab, dim], table_type ZERO_TYPE_BF16 or ZERO_TYPE_F32
+ *   ids     [n_tokens], id_type ZERO_TYPE_I32 or ZERO_TYPE_I64
+ *   out     [n_tokens, dim], out_type ZERO_TYPE_BF16 or ZERO_TYPE_F32
+ * vocab and n_tokens up to 2^30, dim up to 2^22; n_tokens = 0 does nothing.
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_embed_forward(const void* table, int32_t table_type, int64_t vocab, int64_t dim,
+                       const void* ids, int32_t id_type, int64_t n_tokens, double scale,
+                       void* out, int32_t out_type, cudaStream_t stream);
+
+/* Bytes of scratch of zero_embed_backward; ZERO_EINVAL for sizes it refuses. */
+int64_t zero_embed_scratch_bytes(int64_t n_tokens, int64_t vocab, int64_t dim);
+
+/* zero_embed_backward -- the gradient of zero_embed_forward in its table:
+ *   dtable[v, :] = (accumulate ? dtable[v, :] : 0)
+ *                  + scale * sum over { t : ids[t] = v } of dout[t, :]
+ * The tokens are sorted by id; sums run in the order of the tokens, cut at
+ * fixed places of the sorted list.  Tokens whose id lies outside [0, vocab)
+ * are not read.
+ *   dout        [n_tokens, dim], ZERO_TYPE_BF16 or ZERO_TYPE_F32
+ *   dtable      [vocab, dim], ZERO_TYPE_BF16 or ZERO_TYPE_F32, e.g. the
+ *               table's place in a rank's gradient buffer
+ *   accumulate  0: every row is written, +0 where no token has the id;
+ *               1: added to what is there (a table tied to the output head,
+ *               whose gradient the head has written); other rows are not
+ *               touched
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_embed_backward(const void* dout, int32_t dout_type, const void* ids, int32_t id_type,
+                        int64_t n_tokens, double scale, void* dtable, int32_t dtable_type,
+                        int64_t vocab, int64_t dim, int32_t accumulate, void* scratch,
+                        int64_t scratch_bytes, cudaStream_t stream);
+
+#define ZERO_NORM_RMS 0
+#define ZERO_NORM_LAYER 1
+
+/* The norms around a block.  kind: ZERO_NORM_RMS, norm(v) = v * r * w + c with
+ * r = 1/sqrt(mean(v^2) + eps), or ZERO_NORM_LAYER, the same of v - mean(v).
+ * An absent (null) weight is 1, an absent bias 0. */
+typedef struct {
+    int64_t n_rows, dim;     /* dim up to 16384 */
+    int64_t rows_per_gate;   /* >= 1: row i uses row i / rows_per_gate of the gate */
+    int32_t kind;
+    int32_t post_norm;       /* 1: the branch is normed before it is added */
+    int32_t pre_norm;        /* 1: the sum is normed for the next block */
+    int32_t act_type;        /* branch, u, du, dbranch */
+    int32_t res_type;        /* x, y, dy, dx (fp32 activations need an fp32 residual) */
+    int32_t param_type;      /* weights and biases */
+    int32_t gate_type;
+    double eps;              /* > 0 */
+    double residual_scale, branch_scale;
+} zero_block_norm_t;
+
+/* zero_block_norm_forward -- between two blocks of a residual stream x:
+ *   n = post_norm ? norm(branch; post_weight, post_bias) : branch
+ *   y = residual_scale * x + branch_scale * gate[row / rows_per_gate] * n
+ *   u = norm(y; pre_weight, pre_bias)
+ * (u from y before y is rounded).  Without a branch (null; before the first
+ * block) u = norm(x; ...) and y has to be null.
+ *   x, y        [n_rows, dim] of res_type; y may be x
+ *   branch, u   [n_rows, dim] of act_type; u is null exactly when !pre_norm
+ *   gate        [max(1, ceil(n_rows / rows_per_gate)), dim] of gate_type, or
+ *               null (1): per channel with rows_per_gate >= n_rows, per
+ *               sequence with its length, per token with 1
+ *   weights     [dim] of param_type, or null
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_block_norm_forward(const zero_block_norm_t* norm, const void* x, const void* branch,
+                            const void* gate, const void* post_weight, const void* post_bias,
+                            const void* pre_weight, const void* pre_bias, void* y, void* u,
+                            cudaStream_t stream);
+
+/* Gradients of the parameters, each or none wanted (null). */
+typedef struct {
+    void *dgate;                                 /* as the gate, of dgate_type */
+    void *dpost_weight, *dpost_bias, *dpre_weight, *dpre_bias; /* [dim] of grad_type */
+    int32_t dgate_type, grad_type;               /* ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+} zero_block_norm_grads_t;
+
+/* Bytes of scratch of zero_block_norm_backward; ZERO_EINVAL for sizes it refuses. */
+int64_t zero_block_norm_scratch_bytes(int64_t n_rows, int64_t dim, int64_t rows_per_gate);
+
+/* zero_block_norm_backward -- the gradient of zero_block_norm_forward:
+ *   g = dy + (the transposed Jacobian of the norm at y) du
+ *   dx = residual_scale * g
+ *   dbranch = the transposed Jacobian of the branch's norm applied to
+ *             branch_scale * gate * g
+ *   dgate, dpost_*, dpre_* = their sums over the rows (written, not added;
+ *             +0 with no rows)
+ *   dy          [n_rows, dim] of res_type, or null (0)
+ *   du          of act_type, null exactly when !pre_norm
+ *   y           the stream that the forward call wrote (x where it had no
+ *               branch); not read when !pre_norm
+ *   dx          of res_type, may be dy; null: not wanted
+ *   dbranch     of act_type, null exactly when branch is; may be du
+ * The statistics are formed again from y and branch.
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_block_norm_backward(const zero_block_norm_t* norm, const void* dy, const void* du,
+                             const void* y, const void* branch, const void* gate,
+                             const void* post_weight, const void* post_bias,
+                             const void* pre_weight, void* dx, void* dbranch,
+                             const zero_block_norm_grads_t* grads, void* scratch,
+                             int64_t scratch_bytes, cudaStream_t stream);
+
+/* Distillation of a student from a teacher's top logits. */
+typedef struct {
+    int64_t n_rows, vocab;
+    int64_t logits_stride;  /* elements between rows of the logits, >= vocab */
+    int32_t top;            /* teacher entries per row, 1 .. 1024 */
+    int32_t logits_type;    /* logits and dlogits: ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+    int32_t teacher_type;   /* teacher_logits: ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+    int32_t id_type;        /* teacher_ids: ZERO_TYPE_I32 or ZERO_TYPE_I64 */
+    int32_t label_type;     /* labels: ZERO_TYPE_I32 or ZERO_TYPE_I64 */
+    double temperature;     /* 1e-3 .. 1e3 */
+    double ce_weight, kl_weight;
+} zero_distill_t;
+
+/* zero_distill_forward -- the losses of each row, with q = softmax(logits /
+ * temperature) and p = softmax(teacher_logits / temperature) over the row's
+ * counted entries:
+ *   kl[row] = temperature^2 * sum_k p_k (log p_k - log q[teacher_ids_k])
+ *   ce[row] = -log softmax(logits)[label]
+ * An entry whose id lies outside [0, vocab) is not counted (shorter lists);
+ * an id that occurs twice counts with both probabilities.  kl is 0 where no
+ * entry counts (or all that count are -inf), ce where the label lies outside
+ * [0, vocab) or labels is null, both where every logit is -inf or row_weight
+ * is 0 (such rows are not read).
+ *   logits          [n_rows, vocab], rows logits_stride apart
+ *   teacher_logits  [n_rows, top]
+ *   teacher_ids     [n_rows, top]
+ *   labels          [n_rows] or null
+ *   row_weight      [n_rows] fp32 or null (1)
+ *   ce, kl          [n_rows] fp32, written; not multiplied by any weight
+ * ce_weight and kl_weight are not used.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_distill_forward(const zero_distill_t* d, const void* logits, const void* teacher_logits,
+                         const void* teacher_ids, const void* labels, const float* row_weight,
+                         float* ce, float* kl, cudaStream_t stream);
+
+/* zero_distill_forward_backward -- the losses, and the gradient of
+ *   sum over the rows of row_weight * (ce_weight * ce + kl_weight * kl)
+ * in the logits, with the row on chip between the two:
+ *   dlogits[j] = row_weight * ( kl_weight * temperature * (q_j - sum of p_k
+ *                over the entries with id j) + ce_weight * (q1_j - [j = label]) )
+ * each part only where its loss is defined (+0 elsewhere).
+ *   dlogits     [n_rows, vocab] of logits_type, rows dlogits_stride apart; may
+ *               be logits itself (then with the same stride).  Columns from
+ *               vocab to the stride are not touched.
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_distill_forward_backward(const zero_distill_t* d, const void* logits,
+                                  const void* teacher_logits, const void* teacher_ids,
+                                  const void* labels, const float* row_weight, float* ce,
+                                  float* kl, void* dlogits, int64_t dlogits_stride,
+                                  cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
