@@ -38,7 +38,8 @@ namespace {
 using dev::Bf16;
 
 constexpr int kThreads = 512;        // threads of a block, at most
-constexpr int kMaxBlocks = 304;      // backward: two blocks for each of 152 SMs
+constexpr int kMaxBlocks = 304;      // forward: two blocks for each of 152 SMs
+constexpr int kMaxBackBlocks = 152;  // backward: its registers fill an SM with one block
 constexpr int64_t kMaxDim = 16384;   // 512 threads, 4 vectors of 8 columns each
 constexpr int kVectors = 4;          // parameter gradients: dw and dc of both norms
 
@@ -47,6 +48,7 @@ struct Geometry {
     int32_t threads;         // of a group
     int32_t groups;          // in a block
     int32_t classes;         // rows are dealt by row mod classes (1: aligned, or taken as they are)
+    int32_t wide;            // rows start (with their class) at 16-byte boundaries
     int32_t blocks;
     int64_t run;             // backward: consecutive rows of a worker (of `classes` workers together)
 };
@@ -75,166 +77,286 @@ __device__ __forceinline__ Group make_group(int threads)
     return g;
 }
 
-// Sums of kN values over the group's threads, valid in all of them.  Two
-// buffers in turn: one is written again only after the barrier of the other's
-// use, which every thread reaches after it has read the first.
+// Sums of kN (1, 2 or 4) values over the group's threads, valid in all of
+// them.  In a warp, kN values are halved along the first steps: a lane keeps
+// half of them and gives the other half away, so that the 4 sums cost 6
+// shuffles, not 20.  Across warps: one word per warp and value.  Two buffers in
+// turn: one is written again only after the barrier of the other's use, which
+// every thread reaches after it has read the first.
+constexpr int kMaxWarps = kThreads / 32;
+
 template <int kN>
 __device__ __forceinline__ void group_sum(Group& g, float (&v)[kN])
 {
-    __shared__ float red[2][kThreads / 32][4];
-#pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], off);
-    if (g.warps == 1) return;
+    static_assert(kN == 1 || kN == 2 || kN == 4, "");
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    __shared__ __align__(16) float red[2][kMaxWarps * kN];
     const int lane = threadIdx.x & 31;
-    if (lane == 0) {
-#pragma unroll
-        for (int n = 0; n < kN; ++n) red[g.buffer][threadIdx.x >> 5][n] = v[n];
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.threads) : "memory");
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        v[n] = lane < g.warps ? red[g.buffer][g.first_warp + lane][n] : 0.0f;
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], off);
-        v[n] = __shfl_sync(0xFFFFFFFFu, v[n], 0);
-    }
-    g.buffer ^= 1;
-}
-
-// The 8 columns from col of the row that starts at p: columns outside [0, dim)
-// are read as 0 and not written.
-template <typename T>
-__device__ __forceinline__ void load_cols(const T* p, int64_t col, int64_t dim, float (&x)[8])
-{
-    const T* q = p + col;
-    if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-        dev::load_vec<8>(q, x);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = col + e >= 0 && col + e < dim ? dev::load1(q + e) : 0.0f;
-}
-template <typename T>
-__device__ __forceinline__ void store_cols(T* p, int64_t col, int64_t dim, const float (&x)[8])
-{
-    T* q = p + col;
-    if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-        dev::store8(q, x);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (col + e >= 0 && col + e < dim) dev::store1(q + e, x[e]);
-}
-__device__ __forceinline__ void load_cols_any(const void* p, int32_t type, int64_t row,
-                                              int64_t col, int64_t dim, float absent,
-                                              float (&x)[8])
-{
-    if (!p) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = absent;
-    } else if (type == ZERO_TYPE_BF16) {
-        load_cols(static_cast<const Bf16*>(p) + row * dim, col, dim, x);
+    float mine; // the sum of value (lane >> 3) & 3, lane >> 4 or 0 over this lane's part
+    if constexpr (kN == 1) {
+        mine = v[0];
+        mine += __shfl_xor_sync(kAll, mine, 16);
+        mine += __shfl_xor_sync(kAll, mine, 8);
+    } else if constexpr (kN == 2) {
+        const bool up = lane & 16;
+        mine = (up ? v[1] : v[0]) + __shfl_xor_sync(kAll, up ? v[0] : v[1], 16);
+        mine += __shfl_xor_sync(kAll, mine, 8);
     } else {
-        load_cols(static_cast<const float*>(p) + row * dim, col, dim, x);
+        const bool up = lane & 16, odd = lane & 8;
+        const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(kAll, up ? v[0] : v[2], 16);
+        const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(kAll, up ? v[1] : v[3], 16);
+        mine = (odd ? b : a) + __shfl_xor_sync(kAll, odd ? a : b, 8);
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) mine += __shfl_xor_sync(kAll, mine, off);
+    constexpr int kLanes = 32 / kN; // lanes that hold a value's sum
+    if (g.warps > 1) {
+        float* buf = red[g.buffer] + g.first_warp * kN;
+        if (lane % kLanes == 0) buf[(lane / kLanes) * g.warps + (threadIdx.x >> 5) - g.first_warp] = mine;
+        asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.threads) : "memory");
+        // value n's warps by its kLanes lanes
+        const float* of = buf + (lane / kLanes) * g.warps;
+        mine = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; w += kLanes) {
+            const int at = w + lane % kLanes;
+            if (at < g.warps) mine += of[at];
+        }
+#pragma unroll
+        for (int off = (kLanes < kMaxWarps ? kLanes : kMaxWarps) / 2; off > 0; off >>= 1)
+            mine += __shfl_xor_sync(kAll, mine, off);
+        g.buffer ^= 1;
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) v[n] = __shfl_sync(kAll, mine, n * kLanes);
+}
+
+// The 8 columns from col of the row that starts at p, as loaded.  full: they
+// all lie in the row, at a multiple of 16 bytes; else those inside are read
+// one by one and the others are 0.
+__device__ __forceinline__ void edge_cols(const Bf16* p, int col, int dim, dev::Raw8<Bf16>& r)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int c = col + 2 * e;
+        const uint32_t lo = c >= 0 && c < dim ? p[c].bits : 0u;
+        const uint32_t hi = c + 1 >= 0 && c + 1 < dim ? p[c + 1].bits : 0u;
+        w[e] = lo | (hi << 16);
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void edge_cols(const float* p, int col, int dim, dev::Raw8<float>& r)
+{
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = col + e >= 0 && col + e < dim ? p[col + e] : 0.0f;
+    r.a = make_float4(x[0], x[1], x[2], x[3]);
+    r.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void load_cols(const T* p, int col, int dim, bool full, dev::Raw8<T>& r)
+{
+    if (full)
+        dev::stream_raw8(p + col, r);
+    else
+        edge_cols(p, col, dim, r);
+}
+template <typename T>
+__device__ __forceinline__ void store_cols(T* p, int col, int dim, bool full, const float (&x)[8])
+{
+    if (full) {
+        dev::store8_stream(p + col, x);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (col + e >= 0 && col + e < dim) dev::store1(p + col + e, x[e]);
+}
+// Weights, biases and gate rows: read seldom, at any alignment.
+__device__ __forceinline__ void load_vector(const void* p, int32_t type, int64_t row, int col,
+                                            int dim, float absent, float (&x)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = absent;
+    if (!p) return;
+    const int64_t at = row * dim + col;
+    if (type == ZERO_TYPE_BF16) {
+        const Bf16* q = static_cast<const Bf16*>(p) + at;
+        if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0)
+            dev::load_vec<8>(q, x);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = col + e >= 0 && col + e < dim ? dev::load1(q + e) : 0.0f;
+    } else {
+        const float* q = static_cast<const float*>(p) + at;
+        if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0)
+            dev::load_vec<8>(q, x);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = col + e >= 0 && col + e < dim ? q[e] : 0.0f;
     }
 }
 
-// Mean (0 for RMSNorm) and 1/sqrt(variance + eps) of a row.  LayerNorm's
-// variance is taken about the mean in a second sum: the one-pass form
-// mean(v^2) - mean^2 loses the digits that a large mean takes.
+// The thread's columns: kNV pieces of 8.
 template <int kNV>
-__device__ __forceinline__ void row_stats(Group& g, const float (&v)[kNV][8],
-                                          const bool (&in)[kNV][8], int64_t dim, bool layer,
-                                          float eps, float& mean, float& rstd)
+struct Columns {
+    int col[kNV];
+    bool full[kNV];
+    uint32_t inside[kNV]; // bit e: column col + e lies in the row
+};
+template <int kNV>
+__device__ __forceinline__ Columns<kNV> make_columns(const Geometry& G, const Group& g, int shift)
 {
-    const float inv = 1.0f / static_cast<float>(dim);
-    mean = 0.0f;
-    if (layer) {
-        float s[1] = {0.0f};
+    Columns<kNV> c;
+    const int dim = static_cast<int>(G.dim);
 #pragma unroll
-        for (int i = 0; i < kNV; ++i)
+    for (int i = 0; i < kNV; ++i) {
+        c.col[i] = (g.thread + i * g.threads) * 8 - shift;
+        c.full[i] = G.wide && c.col[i] >= 0 && c.col[i] + 8 <= dim;
+        c.inside[i] = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += v[i][e];
-        group_sum(g, s);
-        mean = s[0] * inv;
+        for (int e = 0; e < 8; ++e)
+            if (c.col[i] + e >= 0 && c.col[i] + e < dim) c.inside[i] |= 1u << e;
     }
-    float s[1] = {0.0f};
+    return c;
+}
+
+// x - mean inside the row, 0 outside.
+template <int kNV>
+__device__ __forceinline__ void centre(const Columns<kNV>& c, float mean, float (&x)[kNV][8])
+{
 #pragma unroll
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = in[i][e] ? v[i][e] - mean : 0.0f;
-            s[0] = fmaf(d, d, s[0]);
-        }
-    group_sum(g, s);
-    rstd = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+        for (int e = 0; e < 8; ++e) x[i][e] = c.inside[i] >> e & 1 ? x[i][e] - mean : 0.0f;
+}
+template <int kNV>
+__device__ __forceinline__ float total(const float (&x)[kNV][8])
+{
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += x[i][e];
+    return s;
+}
+template <int kNV>
+__device__ __forceinline__ float dot(const float (&x)[kNV][8], const float (&y)[kNV][8])
+{
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[i][e], y[i][e], s);
+    return s;
 }
 
 // ------------------------------------------------------------------ forward
-template <int kNV, typename Act, typename Res>
-__global__ void __launch_bounds__(kThreads)
+// The row's centred values and 1/sqrt(variance + eps).  LayerNorm's variance
+// is taken about the mean in a second sum: the one-pass form
+// mean(v^2) - mean^2 loses the digits that a large mean takes.
+template <int kNV, bool kFull>
+__device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, const Params& P,
+                                             float inv, float (&v)[kNV][8])
+{
+    if (kFull && P.layer) {
+        float s[1] = {total(v)};
+        group_sum(g, s);
+        centre(c, s[0] * inv, v);
+    }
+    float s[1] = {dot(v, v)};
+    group_sum(g, s);
+    return 1.0f / sqrtf(fmaf(s[0], inv, P.eps));
+}
+
+// kFull: LayerNorm, or biases; else neither.  Rows are dealt to the groups in
+// turn; the next row's loads are issued before this row is computed, and the
+// weights stay in registers: branch_scale * gate * w of the branch's norm as one
+// factor, formed again only where the gate's row changes.
+template <int kNV, bool kFull, typename Act, typename Res>
+__global__ void __launch_bounds__(kThreads, kNV == 1 && !kFull ? 2 : 1)
 forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
                const Act* __restrict__ h, Res* __restrict__ y, Act* __restrict__ u)
 {
     Group g = make_group(G.threads);
     const int64_t worker = static_cast<int64_t>(blockIdx.x) * G.groups + g.id;
     const int64_t workers = static_cast<int64_t>(G.blocks) * G.groups / G.classes * G.classes;
-    if (worker >= workers) return;
-    const int64_t shift = G.classes == 1 ? 0 : worker % G.classes * G.dim % 8;
-    int64_t col[kNV];
-    bool in[kNV][8];
+    if (worker >= workers || worker >= G.rows) return;
+    const int dim = static_cast<int>(G.dim);
+    const float inv = 1.0f / static_cast<float>(dim);
+    const Columns<kNV> c = make_columns<kNV>(
+        G, g, G.classes == 1 ? 0 : static_cast<int>(worker % G.classes * G.dim % 8));
+    float pw[kNV][8], pb[kNV][8], qw[kNV][8], qb[kNV][8];
+    auto factors = [&](int64_t gate_row) {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            float t[8];
+            load_vector(P.gate, P.gate_type, gate_row, c.col[i], dim, 1.0f, t);
+            load_vector(P.post_w, P.param_type, 0, c.col[i], dim, 1.0f, pw[i]);
+            if (kFull) load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, pb[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[e] *= P.branch_scale;
+                pw[i][e] *= t[e];
+                if (kFull) pb[i][e] *= t[e];
+            }
+        }
+    };
+    int64_t gate_row = P.gate ? worker / G.span : 0;
+    int64_t gate_end = P.gate ? (gate_row + 1) * G.span : G.rows; // first row of the next gate row
+    factors(gate_row);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-        col[i] = (g.thread + static_cast<int64_t>(i) * g.threads) * 8 - shift;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) in[i][e] = col[i] + e >= 0 && col[i] + e < G.dim;
+        load_vector(P.pre_w, P.param_type, 0, c.col[i], dim, 1.0f, qw[i]);
+        if (kFull) load_vector(P.pre_b, P.param_type, 0, c.col[i], dim, 0.0f, qb[i]);
     }
+    dev::Raw8<Res> rx[kNV];
+    dev::Raw8<Act> rh[kNV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            load_cols(x + row * G.dim, c.col[i], dim, c.full[i], rx[i]);
+            if (h) load_cols(h + row * G.dim, c.col[i], dim, c.full[i], rh[i]);
+        }
+    };
+    fetch(worker);
     for (int64_t row = worker; row < G.rows; row += workers) {
-        float v[kNV][8];
+        float v[kNV][8], n[kNV][8];
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) load_cols(x + row * G.dim, col[i], G.dim, v[i]);
+        for (int i = 0; i < kNV; ++i) {
+            dev::unpack8(rx[i], v[i]);
+            if (h) dev::unpack8(rh[i], n[i]);
+        }
+        if (row + workers < G.rows) fetch(row + workers);
         if (h) {
-            float n[kNV][8];
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) load_cols(h + row * G.dim, col[i], G.dim, n[i]);
-            if (P.post) {
-                float mean, rstd;
-                row_stats(g, n, in, G.dim, P.layer, P.eps, mean, rstd);
-#pragma unroll
-                for (int i = 0; i < kNV; ++i) {
-                    float w[8], c[8];
-                    load_cols_any(P.post_w, P.param_type, 0, col[i], G.dim, 1.0f, w);
-                    load_cols_any(P.post_b, P.param_type, 0, col[i], G.dim, 0.0f, c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) n[i][e] = fmaf((n[i][e] - mean) * rstd, w[e], c[e]);
-                }
+            const float rstd = P.post ? standardise<kNV, kFull>(g, c, P, inv, n) : 1.0f;
+            if (row >= gate_end) {
+                gate_row = row / G.span;
+                gate_end = (gate_row + 1) * G.span;
+                factors(gate_row);
             }
-            const int64_t gate_row = P.gate ? row / G.span : 0;
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
-                float t[8];
-                load_cols_any(P.gate, P.gate_type, gate_row, col[i], G.dim, 1.0f, t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[i][e] = fmaf(P.res_scale, v[i][e], P.branch_scale * t[e] * n[i][e]);
-                if (y) store_cols(y + row * G.dim, col[i], G.dim, v[i]);
+                for (int e = 0; e < 8; ++e) {
+                    float t = P.res_scale * v[i][e];
+                    if (kFull) t += pb[i][e];
+                    v[i][e] = fmaf(n[i][e] * rstd, pw[i][e], t);
+                }
+                store_cols(y + row * G.dim, c.col[i], dim, c.full[i], v[i]);
             }
         }
         if (P.pre) {
-            float mean, rstd;
-            row_stats(g, v, in, G.dim, P.layer, P.eps, mean, rstd);
+            const float rstd = standardise<kNV, kFull>(g, c, P, inv, v);
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
-                float w[8], c[8];
-                load_cols_any(P.pre_w, P.param_type, 0, col[i], G.dim, 1.0f, w);
-                load_cols_any(P.pre_b, P.param_type, 0, col[i], G.dim, 0.0f, c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = fmaf((v[i][e] - mean) * rstd, w[e], c[e]);
-                store_cols(u + row * G.dim, col[i], G.dim, v[i]);
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] = kFull ? fmaf(v[i][e] * rstd, qw[i][e], qb[i][e])
+                                    : v[i][e] * rstd * qw[i][e];
+                store_cols(u + row * G.dim, c.col[i], dim, c.full[i], v[i]);
             }
         }
     }
@@ -253,7 +375,10 @@ struct Grads {
     float* gate_partial;
 };
 
-template <int kNV, typename Act, typename Res>
+// The sums of a row come together as far as the formulas allow: RMSNorm takes
+// { y^2, du w y, h^2 } and then { d w h }, two exchanges a row; LayerNorm
+// { y, du w, h }, the centred { y^2, du w y, h^2 }, then { d w, d w h }.
+template <int kNV, bool kFull, typename Act, typename Res>
 __global__ void __launch_bounds__(kThreads)
 backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __restrict__ dy,
                 const Act* __restrict__ du, const Res* __restrict__ y, const Act* __restrict__ h,
@@ -267,19 +392,15 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
     const int64_t lo = strip * G.run + cls;
     int64_t hi = strip * G.run + G.run;
     if (hi > G.rows) hi = G.rows;
-    const int64_t shift = G.classes == 1 ? 0 : cls * G.dim % 8;
-    const float inv = 1.0f / static_cast<float>(G.dim);
-    int64_t col[kNV];
-    bool in[kNV][8];
+    const int dim = static_cast<int>(G.dim);
+    const float inv = 1.0f / static_cast<float>(dim);
+    const Columns<kNV> c =
+        make_columns<kNV>(G, g, G.classes == 1 ? 0 : static_cast<int>(cls * G.dim % 8));
+    constexpr int kSums = kFull ? kVectors + 1 : 3;
+    // dw post, dw pre, dgate / branch_scale; dc post, dc pre
+    float sums[kSums][kNV][8];
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        col[i] = (g.thread + static_cast<int64_t>(i) * g.threads) * 8 - shift;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) in[i][e] = col[i] + e >= 0 && col[i] + e < G.dim;
-    }
-    float sums[kVectors + 1][kNV][8]; // dw, dc of post, dw, dc of pre, dgate
-#pragma unroll
-    for (int a = 0; a <= kVectors; ++a)
+    for (int a = 0; a < kSums; ++a)
 #pragma unroll
         for (int i = 0; i < kNV; ++i)
 #pragma unroll
@@ -287,7 +408,17 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
 
     const bool by_rows = D.gate_rows > 1;
     int64_t gate_row = P.gate && lo < hi ? lo / G.span : 0;
+    int64_t gate_end = P.gate ? (gate_row + 1) * G.span : G.rows;
     const int64_t first_gate = gate_row;
+    float pw[kNV][8], qw[kNV][8], gate[kNV][8]; // gate: branch_scale * gate
+    auto load_gate = [&] {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            load_vector(P.gate, P.gate_type, gate_row, c.col[i], dim, 1.0f, gate[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) gate[i][e] *= P.branch_scale;
+        }
+    };
     // The sum of one gate row: final where this worker has all its rows.
     auto leave_gate = [&] {
         const int64_t from = gate_row * G.span;
@@ -295,67 +426,93 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         const bool whole = G.classes == 1 ? from >= lo && to <= hi : to - from == 1;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            if (whole) {
-                if (D.dgate_type == ZERO_TYPE_BF16)
-                    store_cols(static_cast<Bf16*>(D.dgate) + gate_row * G.dim, col[i], G.dim,
-                               sums[kVectors][i]);
-                else
-                    store_cols(static_cast<float*>(D.dgate) + gate_row * G.dim, col[i], G.dim,
-                               sums[kVectors][i]);
-            } else {
-                const int slot = gate_row == first_gate ? 0 : 1;
-                store_cols(D.gate_partial + (2 * worker + slot) * G.dim, col[i], G.dim,
-                           sums[kVectors][i]);
-            }
+            float t[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[kVectors][i][e] = 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                t[e] = P.branch_scale * sums[2][i][e];
+                sums[2][i][e] = 0.0f;
+            }
+            if (!whole) {
+                const int slot = gate_row == first_gate ? 0 : 1;
+                store_cols(D.gate_partial + (2 * worker + slot) * G.dim, c.col[i], dim, false, t);
+            } else if (D.dgate_type == ZERO_TYPE_BF16) {
+                store_cols(static_cast<Bf16*>(D.dgate) + gate_row * G.dim, c.col[i], dim, false, t);
+            } else {
+                store_cols(static_cast<float*>(D.dgate) + gate_row * G.dim, c.col[i], dim, false, t);
+            }
         }
     };
-
-    for (int64_t row = lo; row < hi; row += G.classes) {
-        if (P.gate && row / G.span != gate_row) {
-            if (by_rows) leave_gate();
-            gate_row = row / G.span;
-        }
-        float t[kNV][8]; // the gradient that arrives at y
+    dev::Raw8<Res> rdy[kNV], ry[kNV];
+    dev::Raw8<Act> rdu[kNV], rh[kNV];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            if (dy)
-                load_cols(dy + row * G.dim, col[i], G.dim, t[i]);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[i][e] = 0.0f;
+            if (dy) load_cols(dy + row * G.dim, c.col[i], dim, c.full[i], rdy[i]);
+            if (P.pre) {
+                load_cols(y + row * G.dim, c.col[i], dim, c.full[i], ry[i]);
+                load_cols(du + row * G.dim, c.col[i], dim, c.full[i], rdu[i]);
+            }
+            if (h) load_cols(h + row * G.dim, c.col[i], dim, c.full[i], rh[i]);
         }
+    };
+    if (lo < hi) {
+        fetch(lo);
+        load_gate();
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            load_vector(P.post_w, P.param_type, 0, c.col[i], dim, 1.0f, pw[i]);
+            load_vector(P.pre_w, P.param_type, 0, c.col[i], dim, 1.0f, qw[i]);
+        }
+    }
+
+    for (int64_t row = lo; row < hi; row += G.classes) {
+        float t[kNV][8], v[kNV][8], d[kNV][8], n[kNV][8]; // dy, then g; y; du; branch
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[i][e] = v[i][e] = d[i][e] = n[i][e] = 0.0f;
+            if (dy) dev::unpack8(rdy[i], t[i]);
+            if (P.pre) {
+                dev::unpack8(ry[i], v[i]);
+                dev::unpack8(rdu[i], d[i]);
+            }
+            if (h) dev::unpack8(rh[i], n[i]);
+        }
+        if (row + G.classes < hi) fetch(row + G.classes);
+        if (row >= gate_end) {
+            if (by_rows) leave_gate();
+            gate_row = row / G.span;
+            gate_end = (gate_row + 1) * G.span;
+            load_gate();
+        }
+        float m0 = 0.0f;
+        if (kFull && P.layer) {
+            float s[4] = {total(v), dot(d, qw), total(n), 0.0f};
+            group_sum(g, s);
+            centre(c, s[0] * inv, v);
+            m0 = s[1] * inv;
+            if (P.post) centre(c, s[2] * inv, n);
+        }
+        float s[4] = {dot(v, v), 0.0f, dot(n, n), 0.0f};
+#pragma unroll
+        for (int i = 0; i < kNV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[1] = fmaf(d[i][e] * qw[i][e], v[i][e], s[1]);
+        group_sum(g, s);
         if (P.pre) {
-            float v[kNV][8], d[kNV][8];
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) {
-                load_cols(y + row * G.dim, col[i], G.dim, v[i]);
-                load_cols(du + row * G.dim, col[i], G.dim, d[i]);
-            }
-            float mean, rstd, m[2] = {0.0f, 0.0f};
-            row_stats(g, v, in, G.dim, P.layer, P.eps, mean, rstd);
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) {
-                float w[8];
-                load_cols_any(P.pre_w, P.param_type, 0, col[i], G.dim, 1.0f, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[i][e] = in[i][e] ? (v[i][e] - mean) * rstd : 0.0f;
-                    sums[2][i][e] = fmaf(d[i][e], v[i][e], sums[2][i][e]);
-                    sums[3][i][e] += d[i][e];
-                    d[i][e] *= w[e];
-                    m[0] += d[i][e];
-                    m[1] = fmaf(d[i][e], v[i][e], m[1]);
-                }
-            }
-            group_sum(g, m);
-            const float m0 = P.layer ? m[0] * inv : 0.0f, m1 = m[1] * inv;
+            const float rstd = 1.0f / sqrtf(fmaf(s[0], inv, P.eps));
+            const float m1 = s[1] * rstd * inv; // mean(du w y^)
+            const float k = rstd * rstd * m1;
 #pragma unroll
             for (int i = 0; i < kNV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[i][e] = fmaf(rstd, d[i][e] - m0 - v[i][e] * m1, t[i][e]);
+                for (int e = 0; e < 8; ++e) {
+                    if (kFull) sums[4][i][e] += d[i][e];
+                    const float dr = d[i][e] * rstd;
+                    sums[1][i][e] = fmaf(dr, v[i][e], sums[1][i][e]);
+                    t[i][e] = fmaf(-k, v[i][e], fmaf(dr, qw[i][e], t[i][e]));
+                    if (kFull) t[i][e] = fmaf(-rstd, m0, t[i][e]);
+                }
         }
         if (dx) {
 #pragma unroll
@@ -363,70 +520,79 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
                 float o[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = P.res_scale * t[i][e];
-                store_cols(dx + row * G.dim, col[i], G.dim, o);
+                store_cols(dx + row * G.dim, c.col[i], dim, c.full[i], o);
             }
         }
         if (!h) continue;
-        float n[kNV][8];
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) load_cols(h + row * G.dim, col[i], G.dim, n[i]);
-        float mean = 0.0f, rstd = 1.0f, m[2] = {0.0f, 0.0f};
-        if (P.post) row_stats(g, n, in, G.dim, P.layer, P.eps, mean, rstd);
+        const float rstd = P.post ? 1.0f / sqrtf(fmaf(s[2], inv, P.eps)) : 1.0f;
+        float m[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            float w[8], c[8], s[8];
-            load_cols_any(P.post_w, P.param_type, 0, col[i], G.dim, 1.0f, w);
-            load_cols_any(P.post_b, P.param_type, 0, col[i], G.dim, 0.0f, c);
-            load_cols_any(P.gate, P.gate_type, gate_row, col[i], G.dim, 1.0f, s);
+            float pb[8];
+            if (kFull) load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, pb);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float d = P.branch_scale * t[i][e];
-                n[i][e] = in[i][e] ? (n[i][e] - mean) * rstd : 0.0f;
-                sums[kVectors][i][e] = fmaf(d, fmaf(n[i][e], w[e], c[e]), sums[kVectors][i][e]);
-                const float dn = d * s[e];
-                sums[0][i][e] = fmaf(dn, n[i][e], sums[0][i][e]);
-                sums[1][i][e] += dn;
-                t[i][e] = dn * w[e];
-                m[0] += t[i][e];
+                n[i][e] *= rstd;
+                float a = n[i][e] * pw[i][e];
+                if (kFull) a += pb[e];
+                sums[2][i][e] = fmaf(t[i][e], a, sums[2][i][e]);
+                t[i][e] *= gate[i][e];
+                // outside the row t is not 0 where LayerNorm's mean was taken off
+                if (kFull && !(c.inside[i] >> e & 1)) t[i][e] = 0.0f;
+                sums[0][i][e] = fmaf(t[i][e], n[i][e], sums[0][i][e]);
+                if (kFull) sums[3][i][e] += t[i][e];
+                t[i][e] *= pw[i][e];
+                if (kFull) m[0] += t[i][e];
                 m[1] = fmaf(t[i][e], n[i][e], m[1]);
             }
         }
-        float m0 = 0.0f, m1 = 0.0f;
         if (P.post) {
-            group_sum(g, m);
-            m0 = P.layer ? m[0] * inv : 0.0f;
-            m1 = m[1] * inv;
+            if (kFull) {
+                group_sum(g, m);
+            } else {
+                float one[1] = {m[1]};
+                group_sum(g, one);
+                m[1] = one[0];
+            }
         }
+        const float k0 = kFull && P.post && P.layer ? m[0] * inv : 0.0f;
+        const float k1 = P.post ? m[1] * inv : 0.0f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[i][e] = rstd * (t[i][e] - m0 - n[i][e] * m1);
-            store_cols(dh + row * G.dim, col[i], G.dim, t[i]);
+            for (int e = 0; e < 8; ++e) t[i][e] = rstd * fmaf(-k1, n[i][e], t[i][e] - k0);
+            store_cols(dh + row * G.dim, c.col[i], dim, c.full[i], t[i]);
         }
     }
     if (by_rows && lo < hi) leave_gate();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The block's sums, its groups added in order.
 #pragma unroll
-    for (int a = 0; a <= kVectors; ++a) {
-        if (a >= D.vectors) break;
-        float* out = D.partial + (static_cast<int64_t>(blockIdx.x) * D.vectors + a) * G.dim;
+    for (int a = 0; a < kSums; ++a) {
+        constexpr int kPlace[kVectors + 1] = {0, 2, kVectors, 1, 3}; // in Finals' order
+        if (kPlace[a] >= D.vectors) continue;
+        if (a == 2) {
+#pragma unroll
+            for (int i = 0; i < kNV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[a][i][e] *= P.branch_scale;
+        }
+        float* out = D.partial + (static_cast<int64_t>(blockIdx.x) * D.vectors + kPlace[a]) * G.dim;
         if (G.groups == 1) {
 #pragma unroll
-            for (int i = 0; i < kNV; ++i) store_cols(out, col[i], G.dim, sums[a][i]);
+            for (int i = 0; i < kNV; ++i) store_cols(out, c.col[i], dim, false, sums[a][i]);
             continue;
         }
         __syncthreads();
-        if (g.id < G.groups) {
 #pragma unroll
-            for (int i = 0; i < kNV; ++i)
-                store_cols(combine + g.id * G.dim, col[i], G.dim, sums[a][i]);
-        }
+        for (int i = 0; i < kNV; ++i)
+            store_cols(combine + g.id * dim, c.col[i], dim, false, sums[a][i]);
         __syncthreads();
-        for (int64_t c = threadIdx.x; c < G.dim; c += blockDim.x) {
-            float total = 0.0f;
-            for (int k = 0; k < G.groups; ++k) total += combine[k * G.dim + c];
-            out[c] = total;
+        for (int j = threadIdx.x; j < dim; j += blockDim.x) {
+            float sum = 0.0f;
+            for (int k = 0; k < G.groups; ++k) sum += combine[k * dim + j];
+            out[j] = sum;
         }
     }
 }
@@ -434,7 +600,7 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
 // Sums the blocks' partials (blockIdx.y < vectors) and the shared gate rows'.
 // 32 columns x kSlices threads; a slice adds a run of the partials in order,
 // the slices are added in order.
-constexpr int kSlices = 8;
+constexpr int kSlices = 32;
 
 struct Finals {
     void* out[kVectors + 1];
@@ -444,9 +610,11 @@ struct Finals {
 __global__ void __launch_bounds__(32 * kSlices)
 reduce_kernel(const Geometry G, const Grads D, const Finals F)
 {
+    // launched while the blocks of backward_kernel drain; waits for all of them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    __shared__ float sums[kSlices][32];
+    __shared__ float sums[kSlices][33];
     const int64_t tasks = D.vectors + (D.gate_rows > 1 ? D.gate_rows : 0);
     for (int64_t task = blockIdx.y; task < tasks; task += gridDim.y) {
         const float* src;
@@ -488,18 +656,18 @@ reduce_kernel(const Geometry G, const Grads D, const Finals F)
         const int64_t per = (count + kSlices - 1) / kSlices;
         const int64_t lo = slice * per, hi = lo + per < count ? lo + per : count;
         if (col < G.dim) {
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t k = lo; k < hi; ++k) acc += src[(first + k) * step + col];
         }
         __syncthreads();
         sums[slice][lane] = acc;
         __syncthreads();
-        if (slice == 0 && col < G.dim) {
-            float total[1] = {0.0f};
+        // warp w sums column w of the 32 over the slices (lanes), in a fixed tree
+        float all[1] = {sums[lane][slice]};
 #pragma unroll
-            for (int s = 0; s < kSlices; ++s) total[0] += sums[s][lane];
-            dev::store_any<1>(out, type, col, total);
-        }
+        for (int off = 16; off > 0; off >>= 1) all[0] += __shfl_xor_sync(0xFFFFFFFFu, all[0], off);
+        const int64_t mine = static_cast<int64_t>(blockIdx.x) * 32 + slice;
+        if (lane == 0 && mine < G.dim) dev::store_any<1>(out, type, mine, all);
     }
 }
 
@@ -509,7 +677,14 @@ bool sizes_ok(int64_t rows, int64_t dim, int64_t span)
     return rows >= 0 && rows <= (int64_t(1) << 40) && dim >= 1 && dim <= kMaxDim && span >= 1;
 }
 
-// aligned: every row tensor starts at a multiple of 16 bytes.
+int vectors_per_thread(int64_t dim, int32_t classes)
+{
+    const int64_t vecs = (dim + (classes > 1 ? 7 : 0) + 7) / 8;
+    return vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+}
+
+// aligned: every row tensor starts at a multiple of 16 bytes.  Depends on the
+// sizes alone, so that the order of the sums does too.
 Geometry geometry(int64_t rows, int64_t dim, int64_t span, bool aligned, bool backward)
 {
     Geometry G = {};
@@ -520,31 +695,25 @@ Geometry geometry(int64_t rows, int64_t dim, int64_t span, bool aligned, bool ba
     if (dim % 8 != 0 && aligned && dim + 7 <= kMaxDim &&
         (!backward || G.span == 1 || G.span >= rows))
         G.classes = dim % 4 == 0 ? 2 : dim % 2 == 0 ? 4 : 8;
+    G.wide = aligned && (dim % 8 == 0 || G.classes > 1);
     const int64_t vecs = (dim + (G.classes > 1 ? 7 : 0) + 7) / 8;
-    const int64_t per_thread = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+    const int64_t per_thread = vectors_per_thread(dim, G.classes);
     const int64_t lanes = (vecs + per_thread - 1) / per_thread;
     G.threads = static_cast<int32_t>((lanes + 31) / 32 * 32);
     G.groups = kThreads / G.threads;
     if (G.groups > 15 && G.threads > 32) G.groups = 15;
-    while (G.groups > 1 && (rows + G.groups - 1) / G.groups < kMaxBlocks) G.groups /= 2;
+    const int64_t most = backward ? kMaxBackBlocks : kMaxBlocks;
+    while (G.groups > 1 && (rows + G.groups - 1) / G.groups < most) G.groups /= 2;
     int64_t blocks = (rows + G.groups - 1) / G.groups;
-    if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+    if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
-    if (G.classes > 1) { // at least one worker of each class
-        while (blocks * G.groups < G.classes) ++blocks;
-    }
+    while (blocks * G.groups < G.classes) ++blocks; // a worker of each class
     G.blocks = static_cast<int32_t>(blocks);
     const int64_t strips = blocks * G.groups / G.classes;
     const int64_t run = (rows + strips - 1) / strips;
     G.run = (run + G.classes - 1) / G.classes * G.classes;
     if (G.run < 1) G.run = G.classes;
     return G;
-}
-
-int vectors_per_thread(const Geometry& G)
-{
-    const int64_t vecs = (G.dim + (G.classes > 1 ? 7 : 0) + 7) / 8;
-    return vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
 }
 
 // Scratch of the larger of the two shapes that the pointers' alignment may give.
@@ -603,6 +772,18 @@ Params make_params(const zero_block_norm_t* n, const void* gate, const void* pos
     return P;
 }
 
+template <int kNV, typename Act, typename Res>
+void start_forward(const Geometry& G, const Params& P, const Res* x, const Act* h, Res* y, Act* u,
+                   cudaStream_t stream)
+{
+    const unsigned grid = static_cast<unsigned>(G.blocks);
+    const unsigned block = static_cast<unsigned>(G.threads * G.groups);
+    if (P.layer || P.post_b || P.pre_b)
+        forward_kernel<kNV, true, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+    else
+        forward_kernel<kNV, false, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+}
+
 template <typename Act, typename Res>
 int launch_forward(const Geometry& G, const Params& P, const void* x, const void* h, void* y,
                    void* u, cudaStream_t stream)
@@ -611,17 +792,32 @@ int launch_forward(const Geometry& G, const Params& P, const void* x, const void
     const auto* hp = static_cast<const Act*>(h);
     auto* yp = static_cast<Res*>(y);
     auto* up = static_cast<Act*>(u);
-    const dim3 grid(static_cast<unsigned>(G.blocks)), block(static_cast<unsigned>(G.threads * G.groups));
-    switch (vectors_per_thread(G)) {
-    case 1: forward_kernel<1, Act, Res><<<grid, block, 0, stream>>>(G, P, xp, hp, yp, up); break;
-    case 2: forward_kernel<2, Act, Res><<<grid, block, 0, stream>>>(G, P, xp, hp, yp, up); break;
-    default: forward_kernel<4, Act, Res><<<grid, block, 0, stream>>>(G, P, xp, hp, yp, up);
+    switch (vectors_per_thread(G.dim, G.classes)) {
+    case 1: start_forward<1>(G, P, xp, hp, yp, up, stream); break;
+    case 2: start_forward<2>(G, P, xp, hp, yp, up, stream); break;
+    default: start_forward<4>(G, P, xp, hp, yp, up, stream);
     }
     return cuda_status(cudaGetLastError());
 }
 
+template <int kNV, typename Act, typename Res>
+void start_backward(const Geometry& G, const Params& P, const Grads& D, bool full, const Res* dy,
+                    const Act* du, const Res* y, const Act* h, Res* dx, Act* dh,
+                    cudaStream_t stream)
+{
+    const unsigned grid = static_cast<unsigned>(G.blocks);
+    const unsigned block = static_cast<unsigned>(G.threads * G.groups);
+    const size_t smem = G.groups > 1 ? static_cast<size_t>(G.groups) * G.dim * sizeof(float) : 0;
+    if (full)
+        backward_kernel<kNV, true, Act, Res>
+            <<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
+    else
+        backward_kernel<kNV, false, Act, Res>
+            <<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
+}
+
 template <typename Act, typename Res>
-int launch_backward(const Geometry& G, const Params& P, const Grads& D, const void* dy,
+int launch_backward(const Geometry& G, const Params& P, const Grads& D, bool full, const void* dy,
                     const void* du, const void* y, const void* h, void* dx, void* dh,
                     cudaStream_t stream)
 {
@@ -631,17 +827,10 @@ int launch_backward(const Geometry& G, const Params& P, const Grads& D, const vo
     const auto* hp = static_cast<const Act*>(h);
     auto* dxp = static_cast<Res*>(dx);
     auto* dhp = static_cast<Act*>(dh);
-    const dim3 grid(static_cast<unsigned>(G.blocks)), block(static_cast<unsigned>(G.threads * G.groups));
-    const size_t smem = G.groups > 1 ? static_cast<size_t>(G.groups) * G.dim * sizeof(float) : 0;
-    switch (vectors_per_thread(G)) {
-    case 1:
-        backward_kernel<1, Act, Res><<<grid, block, smem, stream>>>(G, P, D, dyp, dup, yp, hp, dxp, dhp);
-        break;
-    case 2:
-        backward_kernel<2, Act, Res><<<grid, block, smem, stream>>>(G, P, D, dyp, dup, yp, hp, dxp, dhp);
-        break;
-    default:
-        backward_kernel<4, Act, Res><<<grid, block, smem, stream>>>(G, P, D, dyp, dup, yp, hp, dxp, dhp);
+    switch (vectors_per_thread(G.dim, G.classes)) {
+    case 1: start_backward<1>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream); break;
+    case 2: start_backward<2>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream); break;
+    default: start_backward<4>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream);
     }
     return cuda_status(cudaGetLastError());
 }
@@ -727,13 +916,14 @@ extern "C" int zero_block_norm_backward(const zero_block_norm_t* norm, const voi
     D.vectors = D.gate_rows == 1 ? kVectors + 1 : kVectors;
     D.partial = static_cast<float*>(scratch);
     D.gate_partial = D.partial + static_cast<int64_t>(G.blocks) * (kVectors + 1) * G.dim;
+    const bool full = P.layer || post_bias || grads->dpost_bias || grads->dpre_bias;
     int status;
     if (norm->act_type == ZERO_TYPE_F32)
-        status = launch_backward<float, float>(G, P, D, dy, du, y, branch, dx, dbranch, stream);
+        status = launch_backward<float, float>(G, P, D, full, dy, du, y, branch, dx, dbranch, stream);
     else if (norm->res_type == ZERO_TYPE_F32)
-        status = launch_backward<Bf16, float>(G, P, D, dy, du, y, branch, dx, dbranch, stream);
+        status = launch_backward<Bf16, float>(G, P, D, full, dy, du, y, branch, dx, dbranch, stream);
     else
-        status = launch_backward<Bf16, Bf16>(G, P, D, dy, du, y, branch, dx, dbranch, stream);
+        status = launch_backward<Bf16, Bf16>(G, P, D, full, dy, du, y, branch, dx, dbranch, stream);
     if (status != ZERO_OK) return status;
     Finals F = {};
     F.out[0] = grads->dpost_weight;
@@ -746,6 +936,14 @@ extern "C" int zero_block_norm_backward(const zero_block_norm_t* norm, const voi
     const int64_t tasks = D.vectors + (D.gate_rows > 1 ? D.gate_rows : 0);
     const dim3 grid(static_cast<unsigned>((G.dim + 31) / 32),
                     static_cast<unsigned>(tasks < 1024 ? tasks : 1024));
-    reduce_kernel<<<grid, 32 * kSlices, 0, stream>>>(G, D, F);
-    return cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * kSlices);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, reduce_kernel, G, D, F));
 }
