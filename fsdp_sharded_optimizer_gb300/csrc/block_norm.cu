@@ -162,8 +162,12 @@ __device__ __forceinline__ void load_cols(const T* p, int col, int dim, bool ful
     else
         edge_cols(p, col, dim, r);
 }
+__device__ __forceinline__ float part(const float2 (&x)[4], int e)
+{
+    return e & 1 ? x[e >> 1].y : x[e >> 1].x;
+}
 template <typename T>
-__device__ __forceinline__ void store_cols(T* p, int col, int dim, bool full, const float (&x)[8])
+__device__ __forceinline__ void store_cols(T* p, int col, int dim, bool full, const float2 (&x)[4])
 {
     if (full) {
         dev::store8_stream(p + col, x);
@@ -171,31 +175,32 @@ __device__ __forceinline__ void store_cols(T* p, int col, int dim, bool full, co
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (col + e >= 0 && col + e < dim) dev::store1(p + col + e, x[e]);
+        if (col + e >= 0 && col + e < dim) dev::store1(p + col + e, part(x, e));
 }
 // Weights, biases and gate rows: read seldom, at any alignment.
 __device__ __forceinline__ void load_vector(const void* p, int32_t type, int64_t row, int col,
-                                            int dim, float absent, float (&x)[8])
+                                            int dim, float absent, float2 (&x)[4])
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = absent;
+    for (int i = 0; i < 4; ++i) x[i] = dev::pair(absent);
     if (!p) return;
     const int64_t at = row * dim + col;
     if (type == ZERO_TYPE_BF16) {
         const Bf16* q = static_cast<const Bf16*>(p) + at;
+        dev::Raw8<Bf16> r;
         if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0)
-            dev::load_vec<8>(q, x);
+            dev::load_raw8(q, r);
         else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = col + e >= 0 && col + e < dim ? dev::load1(q + e) : 0.0f;
+            edge_cols(q - col, col, dim, r);
+        dev::unpack8(r, x);
     } else {
         const float* q = static_cast<const float*>(p) + at;
+        dev::Raw8<float> r;
         if (col >= 0 && col + 8 <= dim && (reinterpret_cast<uintptr_t>(q) & 15) == 0)
-            dev::load_vec<8>(q, x);
+            dev::load_raw8(q, r);
         else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = col + e >= 0 && col + e < dim ? q[e] : 0.0f;
+            edge_cols(q - col, col, dim, r);
+        dev::unpack8(r, x);
     }
 }
 
@@ -225,32 +230,39 @@ __device__ __forceinline__ Columns<kNV> make_columns(const Geometry& G, const Gr
 
 // x - mean inside the row, 0 outside.
 template <int kNV>
-__device__ __forceinline__ void centre(const Columns<kNV>& c, float mean, float (&x)[kNV][8])
+__device__ __forceinline__ void centre(const Columns<kNV>& c, float mean, float2 (&x)[kNV][4])
 {
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
+    for (int i = 0; i < kNV; ++i) {
+        if (c.inside[i] == 0xFFu) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = c.inside[i] >> e & 1 ? x[i][e] - mean : 0.0f;
+            for (int e = 0; e < 4; ++e) x[i][e] = dev::add2(x[i][e], dev::pair(-mean));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[i][e].x = c.inside[i] >> (2 * e) & 1 ? x[i][e].x - mean : 0.0f;
+                x[i][e].y = c.inside[i] >> (2 * e + 1) & 1 ? x[i][e].y - mean : 0.0f;
+            }
+        }
+    }
 }
 template <int kNV>
-__device__ __forceinline__ float total(const float (&x)[kNV][8])
+__device__ __forceinline__ float total(const float2 (&x)[kNV][4])
 {
-    float s = 0.0f;
+    float2 s = x[0][0];
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[i][e];
-    return s;
+    for (int i = 0; i < 4 * kNV; ++i)
+        if (i) s = dev::add2(s, x[i / 4][i % 4]);
+    return s.x + s.y;
 }
 template <int kNV>
-__device__ __forceinline__ float dot(const float (&x)[kNV][8], const float (&y)[kNV][8])
+__device__ __forceinline__ float dot(const float2 (&x)[kNV][4], const float2 (&y)[kNV][4])
 {
-    float s = 0.0f;
+    float2 s = dev::mul2(x[0][0], y[0][0]);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(x[i][e], y[i][e], s);
-    return s;
+    for (int i = 0; i < 4 * kNV; ++i)
+        if (i) s = dev::fma2(x[i / 4][i % 4], y[i / 4][i % 4], s);
+    return s.x + s.y;
 }
 
 // ------------------------------------------------------------------ forward
@@ -259,7 +271,7 @@ __device__ __forceinline__ float dot(const float (&x)[kNV][8], const float (&y)[
 // mean(v^2) - mean^2 loses the digits that a large mean takes.
 template <int kNV, bool kFull>
 __device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, const Params& P,
-                                             float inv, float (&v)[kNV][8])
+                                             float inv, float2 (&v)[kNV][4])
 {
     if (kFull && P.layer) {
         float s[1] = {total(v)};
@@ -268,7 +280,7 @@ __device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, co
     }
     float s[1] = {dot(v, v)};
     group_sum(g, s);
-    return 1.0f / sqrtf(fmaf(s[0], inv, P.eps));
+    return rsqrtf(fmaf(s[0], inv, P.eps));
 }
 
 // kFull: LayerNorm, or biases; else neither.  Rows are dealt to the groups in
@@ -276,7 +288,7 @@ __device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, co
 // weights stay in registers: branch_scale * gate * w of the branch's norm as one
 // factor, formed again only where the gate's row changes.
 template <int kNV, bool kFull, typename Act, typename Res>
-__global__ void __launch_bounds__(kThreads, kNV == 1 && !kFull ? 2 : 1)
+__global__ void __launch_bounds__(kThreads)
 forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
                const Act* __restrict__ h, Res* __restrict__ y, Act* __restrict__ u)
 {
@@ -288,19 +300,19 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
     const float inv = 1.0f / static_cast<float>(dim);
     const Columns<kNV> c = make_columns<kNV>(
         G, g, G.classes == 1 ? 0 : static_cast<int>(worker % G.classes * G.dim % 8));
-    float pw[kNV][8], pb[kNV][8], qw[kNV][8], qb[kNV][8];
+    float2 pw[kNV][4], pb[kNV][4], qw[kNV][4], qb[kNV][4];
     auto factors = [&](int64_t gate_row) {
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            float t[8];
+            float2 t[4];
             load_vector(P.gate, P.gate_type, gate_row, c.col[i], dim, 1.0f, t);
             load_vector(P.post_w, P.param_type, 0, c.col[i], dim, 1.0f, pw[i]);
             if (kFull) load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, pb[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[e] *= P.branch_scale;
-                pw[i][e] *= t[e];
-                if (kFull) pb[i][e] *= t[e];
+            for (int e = 0; e < 4; ++e) {
+                t[e] = dev::mul2(t[e], dev::pair(P.branch_scale));
+                pw[i][e] = dev::mul2(pw[i][e], t[e]);
+                if (kFull) pb[i][e] = dev::mul2(pb[i][e], t[e]);
             }
         }
     };
@@ -323,7 +335,7 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
     };
     fetch(worker);
     for (int64_t row = worker; row < G.rows; row += workers) {
-        float v[kNV][8], n[kNV][8];
+        float2 v[kNV][4], n[kNV][4];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             dev::unpack8(rx[i], v[i]);
@@ -331,31 +343,33 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
         }
         if (row + workers < G.rows) fetch(row + workers);
         if (h) {
-            const float rstd = P.post ? standardise<kNV, kFull>(g, c, P, inv, n) : 1.0f;
+            const float2 r = dev::pair(P.post ? standardise<kNV, kFull>(g, c, P, inv, n) : 1.0f);
             if (row >= gate_end) {
                 gate_row = row / G.span;
                 gate_end = (gate_row + 1) * G.span;
                 factors(gate_row);
             }
+            const float2 a = dev::pair(P.res_scale);
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float t = P.res_scale * v[i][e];
-                    if (kFull) t += pb[i][e];
-                    v[i][e] = fmaf(n[i][e] * rstd, pw[i][e], t);
+                for (int e = 0; e < 4; ++e) {
+                    v[i][e] = kFull ? dev::fma2(a, v[i][e], pb[i][e]) : dev::mul2(a, v[i][e]);
+                    v[i][e] = dev::fma2(dev::mul2(n[i][e], r), pw[i][e], v[i][e]);
                 }
                 store_cols(y + row * G.dim, c.col[i], dim, c.full[i], v[i]);
             }
         }
         if (P.pre) {
-            const float rstd = standardise<kNV, kFull>(g, c, P, inv, v);
+            const float2 r = dev::pair(standardise<kNV, kFull>(g, c, P, inv, v));
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[i][e] = kFull ? fmaf(v[i][e] * rstd, qw[i][e], qb[i][e])
-                                    : v[i][e] * rstd * qw[i][e];
+                for (int e = 0; e < 4; ++e) {
+                    v[i][e] = dev::mul2(v[i][e], r);
+                    v[i][e] = kFull ? dev::fma2(v[i][e], qw[i][e], qb[i][e])
+                                    : dev::mul2(v[i][e], qw[i][e]);
+                }
                 store_cols(u + row * G.dim, c.col[i], dim, c.full[i], v[i]);
             }
         }
@@ -363,6 +377,33 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
 }
 
 // ----------------------------------------------------------------- backward
+// Per-column factors that a thread keeps in shared memory, where the sums take
+// its registers: its own 8 columns of vector k, piece i, as two 16-byte words;
+// consecutive threads have consecutive words.  No other thread reads them.
+template <int kNV>
+struct Slots {
+    float4* base;
+    __device__ __forceinline__ float4* at(int k, int i) const
+    {
+        return base + (k * kNV + i) * 2 * blockDim.x + threadIdx.x;
+    }
+    __device__ __forceinline__ void put(int k, int i, const float2 (&x)[4]) const
+    {
+        at(k, i)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        at(k, i)[blockDim.x] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+    }
+    __device__ __forceinline__ void get(int k, int i, float2 (&x)[4]) const
+    {
+        const float4 a = at(k, i)[0], b = at(k, i)[blockDim.x];
+        x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
+    }
+};
+constexpr int kSlotPost = 0, kSlotPre = 1, kSlotGate = 2, kSlotBias = 3;
+// With 4 pieces a thread four vectors do not fit; the bias is then read anew.
+template <int kNV>
+constexpr bool kBiasSlot = kNV < 4;
+
 // Partial sums in the scratch: [blocks][vectors in use][dim] of the sums over
 // all rows, then, with several gate rows, [workers][2][dim] of the gate rows
 // that a worker shares with others: its first one, and its last one.
@@ -384,7 +425,10 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
                 const Act* __restrict__ du, const Res* __restrict__ y, const Act* __restrict__ h,
                 Res* __restrict__ dx, Act* __restrict__ dh)
 {
-    extern __shared__ float combine[]; // groups x dim, where a block has several groups
+    extern __shared__ float4 shared[];
+    const Slots<kNV> slots = {shared};
+    // after the rows: groups x dim, where a block has several groups
+    float* combine = reinterpret_cast<float*>(shared);
     Group g = make_group(G.threads);
     const int64_t worker = static_cast<int64_t>(blockIdx.x) * G.groups + g.id;
     const int64_t strip = worker / G.classes; // workers of a strip share its rows by class
@@ -398,25 +442,26 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         make_columns<kNV>(G, g, G.classes == 1 ? 0 : static_cast<int>(cls * G.dim % 8));
     constexpr int kSums = kFull ? kVectors + 1 : 3;
     // dw post, dw pre, dgate / branch_scale; dc post, dc pre
-    float sums[kSums][kNV][8];
+    float2 sums[kSums][kNV][4];
 #pragma unroll
     for (int a = 0; a < kSums; ++a)
 #pragma unroll
         for (int i = 0; i < kNV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[a][i][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) sums[a][i][e] = dev::pair(0.0f);
 
     const bool by_rows = D.gate_rows > 1;
     int64_t gate_row = P.gate && lo < hi ? lo / G.span : 0;
     int64_t gate_end = P.gate ? (gate_row + 1) * G.span : G.rows;
     const int64_t first_gate = gate_row;
-    float pw[kNV][8], qw[kNV][8], gate[kNV][8]; // gate: branch_scale * gate
-    auto load_gate = [&] {
+    auto load_gate = [&] { // branch_scale * gate
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            load_vector(P.gate, P.gate_type, gate_row, c.col[i], dim, 1.0f, gate[i]);
+            float2 w[4];
+            load_vector(P.gate, P.gate_type, gate_row, c.col[i], dim, 1.0f, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) gate[i][e] *= P.branch_scale;
+            for (int e = 0; e < 4; ++e) w[e] = dev::mul2(w[e], dev::pair(P.branch_scale));
+            slots.put(kSlotGate, i, w);
         }
     };
     // The sum of one gate row: final where this worker has all its rows.
@@ -426,11 +471,11 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         const bool whole = G.classes == 1 ? from >= lo && to <= hi : to - from == 1;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            float t[8];
+            float2 t[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[e] = P.branch_scale * sums[2][i][e];
-                sums[2][i][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                t[e] = dev::mul2(dev::pair(P.branch_scale), sums[2][i][e]);
+                sums[2][i][e] = dev::pair(0.0f);
             }
             if (!whole) {
                 const int slot = gate_row == first_gate ? 0 : 1;
@@ -460,17 +505,24 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         load_gate();
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            load_vector(P.post_w, P.param_type, 0, c.col[i], dim, 1.0f, pw[i]);
-            load_vector(P.pre_w, P.param_type, 0, c.col[i], dim, 1.0f, qw[i]);
+            float2 w[4];
+            load_vector(P.post_w, P.param_type, 0, c.col[i], dim, 1.0f, w);
+            slots.put(kSlotPost, i, w);
+            load_vector(P.pre_w, P.param_type, 0, c.col[i], dim, 1.0f, w);
+            slots.put(kSlotPre, i, w);
+            if (kFull && kBiasSlot<kNV>) {
+                load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, w);
+                slots.put(kSlotBias, i, w);
+            }
         }
     }
 
     for (int64_t row = lo; row < hi; row += G.classes) {
-        float t[kNV][8], v[kNV][8], d[kNV][8], n[kNV][8]; // dy, then g; y; du; branch
+        float2 t[kNV][4], v[kNV][4], d[kNV][4], n[kNV][4]; // dy, then g; y; du; branch
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[i][e] = v[i][e] = d[i][e] = n[i][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) t[i][e] = v[i][e] = d[i][e] = n[i][e] = dev::pair(0.0f);
             if (dy) dev::unpack8(rdy[i], t[i]);
             if (P.pre) {
                 dev::unpack8(ry[i], v[i]);
@@ -487,80 +539,110 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         }
         float m0 = 0.0f;
         if (kFull && P.layer) {
-            float s[4] = {total(v), dot(d, qw), total(n), 0.0f};
+            float2 dw = dev::pair(0.0f);
+#pragma unroll
+            for (int i = 0; i < kNV; ++i) {
+                float2 w[4];
+                slots.get(kSlotPre, i, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dw = dev::fma2(d[i][e], w[e], dw);
+            }
+            float s[4] = {total(v), dw.x + dw.y, total(n), 0.0f};
             group_sum(g, s);
             centre(c, s[0] * inv, v);
             m0 = s[1] * inv;
             if (P.post) centre(c, s[2] * inv, n);
         }
-        float s[4] = {dot(v, v), 0.0f, dot(n, n), 0.0f};
+        float2 dwv = dev::pair(0.0f);
 #pragma unroll
-        for (int i = 0; i < kNV; ++i)
+        for (int i = 0; i < kNV; ++i) {
+            float2 w[4];
+            slots.get(kSlotPre, i, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[1] = fmaf(d[i][e] * qw[i][e], v[i][e], s[1]);
+            for (int e = 0; e < 4; ++e) dwv = dev::fma2(dev::mul2(d[i][e], w[e]), v[i][e], dwv);
+        }
+        float s[4] = {dot(v, v), dwv.x + dwv.y, dot(n, n), 0.0f};
         group_sum(g, s);
         if (P.pre) {
-            const float rstd = 1.0f / sqrtf(fmaf(s[0], inv, P.eps));
-            const float m1 = s[1] * rstd * inv; // mean(du w y^)
-            const float k = rstd * rstd * m1;
+            const float rstd = rsqrtf(fmaf(s[0], inv, P.eps));
+            const float2 r = dev::pair(rstd);
+            const float2 k = dev::pair(-rstd * rstd * rstd * s[1] * inv); // -r^2 mean(du w y^)
+            const float2 k0 = dev::pair(-rstd * m0);
 #pragma unroll
-            for (int i = 0; i < kNV; ++i)
+            for (int i = 0; i < kNV; ++i) {
+                float2 w[4];
+                slots.get(kSlotPre, i, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (kFull) sums[4][i][e] += d[i][e];
-                    const float dr = d[i][e] * rstd;
-                    sums[1][i][e] = fmaf(dr, v[i][e], sums[1][i][e]);
-                    t[i][e] = fmaf(-k, v[i][e], fmaf(dr, qw[i][e], t[i][e]));
-                    if (kFull) t[i][e] = fmaf(-rstd, m0, t[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    if (kFull) sums[4][i][e] = dev::add2(sums[4][i][e], d[i][e]);
+                    d[i][e] = dev::mul2(d[i][e], r);
+                    sums[1][i][e] = dev::fma2(d[i][e], v[i][e], sums[1][i][e]);
+                    t[i][e] = dev::fma2(k, v[i][e], dev::fma2(d[i][e], w[e], t[i][e]));
+                    if (kFull) t[i][e] = dev::add2(t[i][e], k0);
                 }
+            }
         }
         if (dx) {
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
-                float o[8];
+                float2 o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = P.res_scale * t[i][e];
+                for (int e = 0; e < 4; ++e) o[e] = dev::mul2(dev::pair(P.res_scale), t[i][e]);
                 store_cols(dx + row * G.dim, c.col[i], dim, c.full[i], o);
             }
         }
         if (!h) continue;
-        const float rstd = P.post ? 1.0f / sqrtf(fmaf(s[2], inv, P.eps)) : 1.0f;
-        float m[2] = {0.0f, 0.0f};
+        const float rstd = P.post ? rsqrtf(fmaf(s[2], inv, P.eps)) : 1.0f;
+        const float2 r = dev::pair(rstd);
+        float2 m0s = dev::pair(0.0f), m1s = m0s;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-            float pb[8];
-            if (kFull) load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, pb);
+            float2 pb[4], pw[4], gate[4];
+            slots.get(kSlotPost, i, pw);
+            slots.get(kSlotGate, i, gate);
+            if (kFull && kBiasSlot<kNV>)
+                slots.get(kSlotBias, i, pb);
+            else if (kFull)
+                load_vector(P.post_b, P.param_type, 0, c.col[i], dim, 0.0f, pb);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                n[i][e] *= rstd;
-                float a = n[i][e] * pw[i][e];
-                if (kFull) a += pb[e];
-                sums[2][i][e] = fmaf(t[i][e], a, sums[2][i][e]);
-                t[i][e] *= gate[i][e];
-                // outside the row t is not 0 where LayerNorm's mean was taken off
-                if (kFull && !(c.inside[i] >> e & 1)) t[i][e] = 0.0f;
-                sums[0][i][e] = fmaf(t[i][e], n[i][e], sums[0][i][e]);
-                if (kFull) sums[3][i][e] += t[i][e];
-                t[i][e] *= pw[i][e];
-                if (kFull) m[0] += t[i][e];
-                m[1] = fmaf(t[i][e], n[i][e], m[1]);
+            for (int e = 0; e < 4; ++e) {
+                n[i][e] = dev::mul2(n[i][e], r);
+                const float2 a =
+                    kFull ? dev::fma2(n[i][e], pw[e], pb[e]) : dev::mul2(n[i][e], pw[e]);
+                sums[2][i][e] = dev::fma2(t[i][e], a, sums[2][i][e]);
+                t[i][e] = dev::mul2(t[i][e], gate[e]);
+                if (kFull) { // outside the row t is not 0 where LayerNorm's mean was taken off
+                    if (!(c.inside[i] >> (2 * e) & 1)) t[i][e].x = 0.0f;
+                    if (!(c.inside[i] >> (2 * e + 1) & 1)) t[i][e].y = 0.0f;
+                    sums[3][i][e] = dev::add2(sums[3][i][e], t[i][e]);
+                }
+                sums[0][i][e] = dev::fma2(t[i][e], n[i][e], sums[0][i][e]);
+                t[i][e] = dev::mul2(t[i][e], pw[e]);
+                if (kFull) m0s = dev::add2(m0s, t[i][e]);
+                m1s = dev::fma2(t[i][e], n[i][e], m1s);
             }
         }
+        float k0 = 0.0f, k1 = 0.0f;
         if (P.post) {
             if (kFull) {
+                float m[2] = {m0s.x + m0s.y, m1s.x + m1s.y};
                 group_sum(g, m);
+                if (P.layer) k0 = m[0] * inv;
+                k1 = m[1] * inv;
             } else {
-                float one[1] = {m[1]};
-                group_sum(g, one);
-                m[1] = one[0];
+                float m[1] = {m1s.x + m1s.y};
+                group_sum(g, m);
+                k1 = m[0] * inv;
             }
         }
-        const float k0 = kFull && P.post && P.layer ? m[0] * inv : 0.0f;
-        const float k1 = P.post ? m[1] * inv : 0.0f;
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[i][e] = rstd * fmaf(-k1, n[i][e], t[i][e] - k0);
+            for (int e = 0; e < 4; ++e) {
+                float2 o = t[i][e];
+                if (kFull) o = dev::add2(o, dev::pair(-k0));
+                t[i][e] = dev::mul2(r, dev::fma2(dev::pair(-k1), n[i][e], o));
+            }
             store_cols(dh + row * G.dim, c.col[i], dim, c.full[i], t[i]);
         }
     }
@@ -576,7 +658,8 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
 #pragma unroll
             for (int i = 0; i < kNV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sums[a][i][e] *= P.branch_scale;
+                for (int e = 0; e < 4; ++e)
+                    sums[a][i][e] = dev::mul2(sums[a][i][e], dev::pair(P.branch_scale));
         }
         float* out = D.partial + (static_cast<int64_t>(blockIdx.x) * D.vectors + kPlace[a]) * G.dim;
         if (G.groups == 1) {
@@ -600,7 +683,7 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
 // Sums the blocks' partials (blockIdx.y < vectors) and the shared gate rows'.
 // 32 columns x kSlices threads; a slice adds a run of the partials in order,
 // the slices are added in order.
-constexpr int kSlices = 32;
+constexpr int kSlices = 8;
 
 struct Finals {
     void* out[kVectors + 1];
@@ -614,7 +697,7 @@ reduce_kernel(const Geometry G, const Grads D, const Finals F)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    __shared__ float sums[kSlices][33];
+    __shared__ float sums[kSlices][32];
     const int64_t tasks = D.vectors + (D.gate_rows > 1 ? D.gate_rows : 0);
     for (int64_t task = blockIdx.y; task < tasks; task += gridDim.y) {
         const float* src;
@@ -662,12 +745,12 @@ reduce_kernel(const Geometry G, const Grads D, const Finals F)
         __syncthreads();
         sums[slice][lane] = acc;
         __syncthreads();
-        // warp w sums column w of the 32 over the slices (lanes), in a fixed tree
-        float all[1] = {sums[lane][slice]};
+        if (slice == 0 && col < G.dim) {
+            float all[1] = {0.0f};
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) all[0] += __shfl_xor_sync(0xFFFFFFFFu, all[0], off);
-        const int64_t mine = static_cast<int64_t>(blockIdx.x) * 32 + slice;
-        if (lane == 0 && mine < G.dim) dev::store_any<1>(out, type, mine, all);
+            for (int w = 0; w < kSlices; ++w) all[0] += sums[w][lane];
+            dev::store_any<1>(out, type, col, all);
+        }
     }
 }
 
@@ -677,10 +760,15 @@ bool sizes_ok(int64_t rows, int64_t dim, int64_t span)
     return rows >= 0 && rows <= (int64_t(1) << 40) && dim >= 1 && dim <= kMaxDim && span >= 1;
 }
 
-int vectors_per_thread(int64_t dim, int32_t classes)
+// Two vectors a thread halve the exchanges' share of the work, where that
+// leaves no more threads idle (forward; the backward kernel's sums take the
+// registers).
+int vectors_per_thread(int64_t dim, int32_t classes, bool backward)
 {
     const int64_t vecs = (dim + (classes > 1 ? 7 : 0) + 7) / 8;
-    return vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+    if (vecs > 2 * kThreads) return 4;
+    if (vecs > kThreads) return 2;
+    return !backward && vecs % 64 == 0 ? 2 : 1;
 }
 
 // aligned: every row tensor starts at a multiple of 16 bytes.  Depends on the
@@ -697,7 +785,7 @@ Geometry geometry(int64_t rows, int64_t dim, int64_t span, bool aligned, bool ba
         G.classes = dim % 4 == 0 ? 2 : dim % 2 == 0 ? 4 : 8;
     G.wide = aligned && (dim % 8 == 0 || G.classes > 1);
     const int64_t vecs = (dim + (G.classes > 1 ? 7 : 0) + 7) / 8;
-    const int64_t per_thread = vectors_per_thread(dim, G.classes);
+    const int64_t per_thread = vectors_per_thread(dim, G.classes, backward);
     const int64_t lanes = (vecs + per_thread - 1) / per_thread;
     G.threads = static_cast<int32_t>((lanes + 31) / 32 * 32);
     G.groups = kThreads / G.threads;
@@ -792,7 +880,7 @@ int launch_forward(const Geometry& G, const Params& P, const void* x, const void
     const auto* hp = static_cast<const Act*>(h);
     auto* yp = static_cast<Res*>(y);
     auto* up = static_cast<Act*>(u);
-    switch (vectors_per_thread(G.dim, G.classes)) {
+    switch (vectors_per_thread(G.dim, G.classes, false)) {
     case 1: start_forward<1>(G, P, xp, hp, yp, up, stream); break;
     case 2: start_forward<2>(G, P, xp, hp, yp, up, stream); break;
     default: start_forward<4>(G, P, xp, hp, yp, up, stream);
@@ -801,19 +889,23 @@ int launch_forward(const Geometry& G, const Params& P, const void* x, const void
 }
 
 template <int kNV, typename Act, typename Res>
-void start_backward(const Geometry& G, const Params& P, const Grads& D, bool full, const Res* dy,
+int start_backward(const Geometry& G, const Params& P, const Grads& D, bool full, const Res* dy,
                     const Act* du, const Res* y, const Act* h, Res* dx, Act* dh,
                     cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>(G.blocks);
     const unsigned block = static_cast<unsigned>(G.threads * G.groups);
-    const size_t smem = G.groups > 1 ? static_cast<size_t>(G.groups) * G.dim * sizeof(float) : 0;
-    if (full)
-        backward_kernel<kNV, true, Act, Res>
-            <<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
-    else
-        backward_kernel<kNV, false, Act, Res>
-            <<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
+    size_t smem = static_cast<size_t>(full && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * block;
+    const size_t combine = static_cast<size_t>(G.groups) * G.dim * sizeof(float);
+    if (G.groups > 1 && combine > smem) smem = combine;
+    auto* kernel = full ? backward_kernel<kNV, true, Act, Res> : backward_kernel<kNV, false, Act, Res>;
+    if (smem > 32 * 1024 && // beside the static words
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+        return ZERO_ECUDA;
+    kernel<<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
+    return cuda_status(cudaGetLastError());
 }
 
 template <typename Act, typename Res>
@@ -827,12 +919,11 @@ int launch_backward(const Geometry& G, const Params& P, const Grads& D, bool ful
     const auto* hp = static_cast<const Act*>(h);
     auto* dxp = static_cast<Res*>(dx);
     auto* dhp = static_cast<Act*>(dh);
-    switch (vectors_per_thread(G.dim, G.classes)) {
-    case 1: start_backward<1>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream); break;
-    case 2: start_backward<2>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream); break;
-    default: start_backward<4>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream);
+    switch (vectors_per_thread(G.dim, G.classes, true)) {
+    case 1: return start_backward<1>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream);
+    case 2: return start_backward<2>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream);
+    default: return start_backward<4>(G, P, D, full, dyp, dup, yp, hp, dxp, dhp, stream);
     }
-    return cuda_status(cudaGetLastError());
 }
 
 } // namespace

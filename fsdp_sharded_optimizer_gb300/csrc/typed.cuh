@@ -122,6 +122,59 @@ __device__ __forceinline__ void store8_stream(float* p, const float (&x)[8])
     __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
 
+// Two fp32 values in one register pair: one instruction works on both.
+__device__ __forceinline__ unsigned long long as_pair(float2 a)
+{
+    return (static_cast<unsigned long long>(__float_as_uint(a.y)) << 32) | __float_as_uint(a.x);
+}
+__device__ __forceinline__ float2 from_pair(unsigned long long a)
+{
+    return make_float2(__uint_as_float(static_cast<uint32_t>(a)),
+                       __uint_as_float(static_cast<uint32_t>(a >> 32)));
+}
+__device__ __forceinline__ float2 pair(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_pair(a)), "l"(as_pair(b)), "l"(as_pair(c)));
+    return from_pair(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_pair(a)), "l"(as_pair(b)));
+    return from_pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_pair(a)), "l"(as_pair(b)));
+    return from_pair(d);
+}
+__device__ __forceinline__ void unpack8(const Raw8<Bf16>& r, float2 (&x)[4])
+{
+    x[0] = make_float2(bf16_lo(r.a.x), bf16_hi(r.a.x));
+    x[1] = make_float2(bf16_lo(r.a.y), bf16_hi(r.a.y));
+    x[2] = make_float2(bf16_lo(r.a.z), bf16_hi(r.a.z));
+    x[3] = make_float2(bf16_lo(r.a.w), bf16_hi(r.a.w));
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float2 (&x)[4])
+{
+    x[0] = make_float2(r.a.x, r.a.y), x[1] = make_float2(r.a.z, r.a.w);
+    x[2] = make_float2(r.b.x, r.b.y), x[3] = make_float2(r.b.z, r.b.w);
+}
+__device__ __forceinline__ void store8_stream(Bf16* p, const float2 (&x)[4])
+{
+    __stcs(reinterpret_cast<uint4*>(p),
+           make_uint4(cvt_bf16x2(x[0].x, x[0].y), cvt_bf16x2(x[1].x, x[1].y),
+                      cvt_bf16x2(x[2].x, x[2].y), cvt_bf16x2(x[3].x, x[3].y)));
+}
+__device__ __forceinline__ void store8_stream(float* p, const float2 (&x)[4])
+{
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
+}
+
 // kVec (8 or 1) elements at once.
 template <int kVec, typename T>
 __device__ __forceinline__ void load_vec(const T* p, float (&x)[kVec])

@@ -112,7 +112,8 @@ CASES = [
     dict(rows=400, dim=1002, span=1), dict(rows=333, dim=520, span=100),
     dict(rows=333, dim=515, span=100), dict(rows=2048, dim=256, span=7),
     dict(rows=1300, dim=256, span=1), dict(rows=90, dim=4096, span=2, kind="layer", bias=True),
-    dict(rows=61, dim=2048, gate=False), dict(rows=61, dim=2048, post=False),
+    dict(rows=2500, dim=256), dict(rows=2500, dim=256, kind="layer", bias=True),
+    dict(rows=400, dim=4096), dict(rows=61, dim=2048, gate=False), dict(rows=61, dim=2048, post=False),
     dict(rows=61, dim=2048, pre=False), dict(rows=61, dim=264, branch=False),
     dict(rows=40, dim=5000), dict(rows=9, dim=16384, kind="layer", bias=True),
     dict(rows=9, dim=16383), dict(rows=40, dim=256, offset=1), dict(rows=40, dim=131, offset=3),
