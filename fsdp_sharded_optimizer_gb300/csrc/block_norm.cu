@@ -154,25 +154,18 @@ __device__ __forceinline__ void edge_cols(const float* p, int col, int dim, dev:
     r.a = make_float4(x[0], x[1], x[2], x[3]);
     r.b = make_float4(x[4], x[5], x[6], x[7]);
 }
-template <typename T>
-__device__ __forceinline__ void load_cols(const T* p, int col, int dim, bool full, dev::Raw8<T>& r)
+__device__ __forceinline__ void clear(dev::Raw8<Bf16>& r) { r.a = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void clear(dev::Raw8<float>& r)
 {
-    if (full)
-        dev::stream_raw8(p + col, r);
-    else
-        edge_cols(p, col, dim, r);
+    r.a = r.b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 __device__ __forceinline__ float part(const float2 (&x)[4], int e)
 {
     return e & 1 ? x[e >> 1].y : x[e >> 1].x;
 }
 template <typename T>
-__device__ __forceinline__ void store_cols(T* p, int col, int dim, bool full, const float2 (&x)[4])
+__device__ __forceinline__ void store_edge(T* p, int col, int dim, const float2 (&x)[4])
 {
-    if (full) {
-        dev::store8_stream(p + col, x);
-        return;
-    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (col + e >= 0 && col + e < dim) dev::store1(p + col + e, part(x, e));
@@ -204,44 +197,73 @@ __device__ __forceinline__ void load_vector(const void* p, int32_t type, int64_t
     }
 }
 
-// The thread's columns: kNV pieces of 8.
-template <int kNV>
+// What a kernel is compiled for.
+//   kPlain  RMSNorm without biases, rows at 16-byte boundaries, whole pieces
+//   kWhole  LayerNorm or biases too, the same rows
+//   kEdges  everything: pieces that reach over the row's ends, any alignment
+// The tests for ends in kEdges' loads and stores cost it about a third of the
+// other two's rate.
+enum Mode { kPlain = 0, kWhole = 1, kEdges = 2 };
+
+// The thread's columns: kNV pieces of 8.  A piece of kPlain and kWhole lies in
+// the row as a whole, or outside.
+template <int kNV, int kMode>
 struct Columns {
-    int col[kNV];
-    bool full[kNV];
-    uint32_t inside[kNV]; // bit e: column col + e lies in the row
-};
-template <int kNV>
-__device__ __forceinline__ Columns<kNV> make_columns(const Geometry& G, const Group& g, int shift)
-{
-    Columns<kNV> c;
-    const int dim = static_cast<int>(G.dim);
+    int col[kNV], dim;
+    bool full[kNV]; // inside the row, at a multiple of 16 bytes
+
+    __device__ __forceinline__ Columns(const Geometry& G, const Group& g, int shift)
+    {
+        dim = static_cast<int>(G.dim);
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-        c.col[i] = (g.thread + i * g.threads) * 8 - shift;
-        c.full[i] = G.wide && c.col[i] >= 0 && c.col[i] + 8 <= dim;
-        c.inside[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c.col[i] + e >= 0 && c.col[i] + e < dim) c.inside[i] |= 1u << e;
+        for (int i = 0; i < kNV; ++i) {
+            col[i] = (g.thread + i * g.threads) * 8 - shift;
+            full[i] = col[i] + 8 <= dim;
+            if (kMode == kEdges) full[i] = G.wide && full[i] && col[i] >= 0;
+        }
     }
-    return c;
-}
+    __device__ __forceinline__ bool inside(int i, int e) const
+    {
+        return kMode != kEdges ? full[i] : col[i] + e >= 0 && col[i] + e < dim;
+    }
+    // The pieces' values at p, the row's start; 0 outside the row.
+    template <typename T>
+    __device__ __forceinline__ void load(const T* p, dev::Raw8<T> (&r)[kNV]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kNV; ++i) {
+            if (full[i])
+                dev::stream_raw8(p + col[i], r[i]);
+            else if (kMode == kEdges)
+                edge_cols(p, col[i], dim, r[i]);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* p, int i, const float2 (&x)[4]) const
+    {
+        if (full[i])
+            dev::store8_stream(p + col[i], x);
+        else if (kMode == kEdges)
+            store_edge(p, col[i], dim, x);
+    }
+};
 
 // x - mean inside the row, 0 outside.
-template <int kNV>
-__device__ __forceinline__ void centre(const Columns<kNV>& c, float mean, float2 (&x)[kNV][4])
+template <int kNV, int kMode>
+__device__ __forceinline__ void centre(const Columns<kNV, kMode>& c, float mean,
+                                       float2 (&x)[kNV][4])
 {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-        if (c.inside[i] == 0xFFu) {
+        if (kMode != kEdges) {
+            const float2 m = dev::pair(c.full[i] ? -mean : 0.0f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = dev::add2(x[i][e], dev::pair(-mean));
+            for (int e = 0; e < 4; ++e) x[i][e] = dev::add2(x[i][e], m);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[i][e].x = c.inside[i] >> (2 * e) & 1 ? x[i][e].x - mean : 0.0f;
-                x[i][e].y = c.inside[i] >> (2 * e + 1) & 1 ? x[i][e].y - mean : 0.0f;
+                x[i][e].x = c.inside(i, 2 * e) ? x[i][e].x - mean : 0.0f;
+                x[i][e].y = c.inside(i, 2 * e + 1) ? x[i][e].y - mean : 0.0f;
             }
         }
     }
@@ -269,11 +291,11 @@ __device__ __forceinline__ float dot(const float2 (&x)[kNV][4], const float2 (&y
 // The row's centred values and 1/sqrt(variance + eps).  LayerNorm's variance
 // is taken about the mean in a second sum: the one-pass form
 // mean(v^2) - mean^2 loses the digits that a large mean takes.
-template <int kNV, bool kFull>
-__device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, const Params& P,
+template <int kNV, int kMode>
+__device__ __forceinline__ float standardise(Group& g, const Columns<kNV, kMode>& c, const Params& P,
                                              float inv, float2 (&v)[kNV][4])
 {
-    if (kFull && P.layer) {
+    if (kMode != kPlain && P.layer) {
         float s[1] = {total(v)};
         group_sum(g, s);
         centre(c, s[0] * inv, v);
@@ -283,11 +305,10 @@ __device__ __forceinline__ float standardise(Group& g, const Columns<kNV>& c, co
     return rsqrtf(fmaf(s[0], inv, P.eps));
 }
 
-// kFull: LayerNorm, or biases; else neither.  Rows are dealt to the groups in
-// turn; the next row's loads are issued before this row is computed, and the
+// Rows are dealt to the groups in turn; the next row's loads are issued before this row is computed, and the
 // weights stay in registers: branch_scale * gate * w of the branch's norm as one
 // factor, formed again only where the gate's row changes.
-template <int kNV, bool kFull, typename Act, typename Res>
+template <int kNV, int kMode, typename Act, typename Res>
 __global__ void __launch_bounds__(kThreads)
 forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
                const Act* __restrict__ h, Res* __restrict__ y, Act* __restrict__ u)
@@ -298,8 +319,9 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
     if (worker >= workers || worker >= G.rows) return;
     const int dim = static_cast<int>(G.dim);
     const float inv = 1.0f / static_cast<float>(dim);
-    const Columns<kNV> c = make_columns<kNV>(
-        G, g, G.classes == 1 ? 0 : static_cast<int>(worker % G.classes * G.dim % 8));
+    constexpr bool kFull = kMode != kPlain;
+    const Columns<kNV, kMode> c(
+        G, g, kMode == kEdges ? static_cast<int>(worker % G.classes * G.dim % 8) : 0);
     float2 pw[kNV][4], pb[kNV][4], qw[kNV][4], qb[kNV][4];
     auto factors = [&](int64_t gate_row) {
 #pragma unroll
@@ -326,24 +348,28 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
     }
     dev::Raw8<Res> rx[kNV];
     dev::Raw8<Act> rh[kNV];
-    auto fetch = [&](int64_t row) {
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            load_cols(x + row * G.dim, c.col[i], dim, c.full[i], rx[i]);
-            if (h) load_cols(h + row * G.dim, c.col[i], dim, c.full[i], rh[i]);
-        }
-    };
-    fetch(worker);
-    for (int64_t row = worker; row < G.rows; row += workers) {
+    for (int i = 0; i < kNV; ++i) {
+        clear(rx[i]);
+        clear(rh[i]);
+    }
+    const int64_t step = workers * G.dim;
+    int64_t at = worker * G.dim; // the row's first element
+    c.load(x + at, rx);
+    if (h) c.load(h + at, rh);
+    for (int64_t row = worker; row < G.rows; row += workers, at += step) {
         float2 v[kNV][4], n[kNV][4];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
             dev::unpack8(rx[i], v[i]);
-            if (h) dev::unpack8(rh[i], n[i]);
+            dev::unpack8(rh[i], n[i]);
         }
-        if (row + workers < G.rows) fetch(row + workers);
+        if (row + workers < G.rows) {
+            c.load(x + at + step, rx);
+            if (h) c.load(h + at + step, rh);
+        }
         if (h) {
-            const float2 r = dev::pair(P.post ? standardise<kNV, kFull>(g, c, P, inv, n) : 1.0f);
+            const float2 r = dev::pair(P.post ? standardise(g, c, P, inv, n) : 1.0f);
             if (row >= gate_end) {
                 gate_row = row / G.span;
                 gate_end = (gate_row + 1) * G.span;
@@ -357,11 +383,11 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
                     v[i][e] = kFull ? dev::fma2(a, v[i][e], pb[i][e]) : dev::mul2(a, v[i][e]);
                     v[i][e] = dev::fma2(dev::mul2(n[i][e], r), pw[i][e], v[i][e]);
                 }
-                store_cols(y + row * G.dim, c.col[i], dim, c.full[i], v[i]);
+                c.store(y + at, i, v[i]);
             }
         }
         if (P.pre) {
-            const float2 r = dev::pair(standardise<kNV, kFull>(g, c, P, inv, v));
+            const float2 r = dev::pair(standardise(g, c, P, inv, v));
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
 #pragma unroll
@@ -370,7 +396,7 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
                     v[i][e] = kFull ? dev::fma2(v[i][e], qw[i][e], qb[i][e])
                                     : dev::mul2(v[i][e], qw[i][e]);
                 }
-                store_cols(u + row * G.dim, c.col[i], dim, c.full[i], v[i]);
+                c.store(u + at, i, v[i]);
             }
         }
     }
@@ -419,7 +445,7 @@ struct Grads {
 // The sums of a row come together as far as the formulas allow: RMSNorm takes
 // { y^2, du w y, h^2 } and then { d w h }, two exchanges a row; LayerNorm
 // { y, du w, h }, the centred { y^2, du w y, h^2 }, then { d w, d w h }.
-template <int kNV, bool kFull, typename Act, typename Res>
+template <int kNV, int kMode, typename Act, typename Res>
 __global__ void __launch_bounds__(kThreads)
 backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __restrict__ dy,
                 const Act* __restrict__ du, const Res* __restrict__ y, const Act* __restrict__ h,
@@ -438,8 +464,8 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
     if (hi > G.rows) hi = G.rows;
     const int dim = static_cast<int>(G.dim);
     const float inv = 1.0f / static_cast<float>(dim);
-    const Columns<kNV> c =
-        make_columns<kNV>(G, g, G.classes == 1 ? 0 : static_cast<int>(cls * G.dim % 8));
+    constexpr bool kFull = kMode != kPlain;
+    const Columns<kNV, kMode> c(G, g, kMode == kEdges ? static_cast<int>(cls * G.dim % 8) : 0);
     constexpr int kSums = kFull ? kVectors + 1 : 3;
     // dw post, dw pre, dgate / branch_scale; dc post, dc pre
     float2 sums[kSums][kNV][4];
@@ -479,29 +505,35 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
             }
             if (!whole) {
                 const int slot = gate_row == first_gate ? 0 : 1;
-                store_cols(D.gate_partial + (2 * worker + slot) * G.dim, c.col[i], dim, false, t);
+                store_edge(D.gate_partial + (2 * worker + slot) * G.dim, c.col[i], dim, t);
             } else if (D.dgate_type == ZERO_TYPE_BF16) {
-                store_cols(static_cast<Bf16*>(D.dgate) + gate_row * G.dim, c.col[i], dim, false, t);
+                store_edge(static_cast<Bf16*>(D.dgate) + gate_row * G.dim, c.col[i], dim, t);
             } else {
-                store_cols(static_cast<float*>(D.dgate) + gate_row * G.dim, c.col[i], dim, false, t);
+                store_edge(static_cast<float*>(D.dgate) + gate_row * G.dim, c.col[i], dim, t);
             }
         }
     };
     dev::Raw8<Res> rdy[kNV], ry[kNV];
     dev::Raw8<Act> rdu[kNV], rh[kNV];
-    auto fetch = [&](int64_t row) {
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            if (dy) load_cols(dy + row * G.dim, c.col[i], dim, c.full[i], rdy[i]);
-            if (P.pre) {
-                load_cols(y + row * G.dim, c.col[i], dim, c.full[i], ry[i]);
-                load_cols(du + row * G.dim, c.col[i], dim, c.full[i], rdu[i]);
-            }
-            if (h) load_cols(h + row * G.dim, c.col[i], dim, c.full[i], rh[i]);
+    for (int i = 0; i < kNV; ++i) { // what is absent, or outside the row, is 0
+        clear(rdy[i]);
+        clear(ry[i]);
+        clear(rdu[i]);
+        clear(rh[i]);
+    }
+    auto fetch = [&](int64_t from) {
+        if (dy) c.load(dy + from, rdy);
+        if (P.pre) {
+            c.load(y + from, ry);
+            c.load(du + from, rdu);
         }
+        if (h) c.load(h + from, rh);
     };
+    const int64_t step = G.classes * G.dim;
+    int64_t at = lo * G.dim; // the row's first element
     if (lo < hi) {
-        fetch(lo);
+        fetch(at);
         load_gate();
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
@@ -517,20 +549,16 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         }
     }
 
-    for (int64_t row = lo; row < hi; row += G.classes) {
+    for (int64_t row = lo; row < hi; row += G.classes, at += step) {
         float2 t[kNV][4], v[kNV][4], d[kNV][4], n[kNV][4]; // dy, then g; y; du; branch
 #pragma unroll
         for (int i = 0; i < kNV; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[i][e] = v[i][e] = d[i][e] = n[i][e] = dev::pair(0.0f);
-            if (dy) dev::unpack8(rdy[i], t[i]);
-            if (P.pre) {
-                dev::unpack8(ry[i], v[i]);
-                dev::unpack8(rdu[i], d[i]);
-            }
-            if (h) dev::unpack8(rh[i], n[i]);
+            dev::unpack8(rdy[i], t[i]);
+            dev::unpack8(ry[i], v[i]);
+            dev::unpack8(rdu[i], d[i]);
+            dev::unpack8(rh[i], n[i]);
         }
-        if (row + G.classes < hi) fetch(row + G.classes);
+        if (row + G.classes < hi) fetch(at + step);
         if (row >= gate_end) {
             if (by_rows) leave_gate();
             gate_row = row / G.span;
@@ -567,9 +595,9 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
             const float rstd = rsqrtf(fmaf(s[0], inv, P.eps));
             const float2 r = dev::pair(rstd);
             const float2 k = dev::pair(-rstd * rstd * rstd * s[1] * inv); // -r^2 mean(du w y^)
-            const float2 k0 = dev::pair(-rstd * m0);
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
+                const float2 k0 = dev::pair(kMode == kEdges || c.full[i] ? -rstd * m0 : 0.0f);
                 float2 w[4];
                 slots.get(kSlotPre, i, w);
 #pragma unroll
@@ -588,7 +616,7 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
                 float2 o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = dev::mul2(dev::pair(P.res_scale), t[i][e]);
-                store_cols(dx + row * G.dim, c.col[i], dim, c.full[i], o);
+                c.store(dx + at, i, o);
             }
         }
         if (!h) continue;
@@ -611,9 +639,11 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
                     kFull ? dev::fma2(n[i][e], pw[e], pb[e]) : dev::mul2(n[i][e], pw[e]);
                 sums[2][i][e] = dev::fma2(t[i][e], a, sums[2][i][e]);
                 t[i][e] = dev::mul2(t[i][e], gate[e]);
-                if (kFull) { // outside the row t is not 0 where LayerNorm's mean was taken off
-                    if (!(c.inside[i] >> (2 * e) & 1)) t[i][e].x = 0.0f;
-                    if (!(c.inside[i] >> (2 * e + 1) & 1)) t[i][e].y = 0.0f;
+                if (kMode == kEdges) { // LayerNorm's mean was taken off outside the row too
+                    if (!c.inside(i, 2 * e)) t[i][e].x = 0.0f;
+                    if (!c.inside(i, 2 * e + 1)) t[i][e].y = 0.0f;
+                }
+                if (kFull) {
                     sums[3][i][e] = dev::add2(sums[3][i][e], t[i][e]);
                 }
                 sums[0][i][e] = dev::fma2(t[i][e], n[i][e], sums[0][i][e]);
@@ -643,7 +673,7 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
                 if (kFull) o = dev::add2(o, dev::pair(-k0));
                 t[i][e] = dev::mul2(r, dev::fma2(dev::pair(-k1), n[i][e], o));
             }
-            store_cols(dh + row * G.dim, c.col[i], dim, c.full[i], t[i]);
+            c.store(dh + at, i, t[i]);
         }
     }
     if (by_rows && lo < hi) leave_gate();
@@ -664,13 +694,13 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         float* out = D.partial + (static_cast<int64_t>(blockIdx.x) * D.vectors + kPlace[a]) * G.dim;
         if (G.groups == 1) {
 #pragma unroll
-            for (int i = 0; i < kNV; ++i) store_cols(out, c.col[i], dim, false, sums[a][i]);
+            for (int i = 0; i < kNV; ++i) store_edge(out, c.col[i], dim, sums[a][i]);
             continue;
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kNV; ++i)
-            store_cols(combine + g.id * dim, c.col[i], dim, false, sums[a][i]);
+            store_edge(combine + g.id * dim, c.col[i], dim, sums[a][i]);
         __syncthreads();
         for (int j = threadIdx.x; j < dim; j += blockDim.x) {
             float sum = 0.0f;
@@ -860,16 +890,24 @@ Params make_params(const zero_block_norm_t* n, const void* gate, const void* pos
     return P;
 }
 
+Mode mode_of(const Geometry& G, bool full)
+{
+    return !G.wide || G.classes > 1 ? kEdges : full ? kWhole : kPlain;
+}
+
 template <int kNV, typename Act, typename Res>
 void start_forward(const Geometry& G, const Params& P, const Res* x, const Act* h, Res* y, Act* u,
                    cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>(G.blocks);
     const unsigned block = static_cast<unsigned>(G.threads * G.groups);
-    if (P.layer || P.post_b || P.pre_b)
-        forward_kernel<kNV, true, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+    const Mode mode = mode_of(G, P.layer || P.post_b || P.pre_b);
+    if (mode == kPlain)
+        forward_kernel<kNV, kPlain, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+    else if (mode == kWhole)
+        forward_kernel<kNV, kWhole, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
     else
-        forward_kernel<kNV, false, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+        forward_kernel<kNV, kEdges, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
 }
 
 template <typename Act, typename Res>
@@ -895,10 +933,13 @@ int start_backward(const Geometry& G, const Params& P, const Grads& D, bool full
 {
     const unsigned grid = static_cast<unsigned>(G.blocks);
     const unsigned block = static_cast<unsigned>(G.threads * G.groups);
-    size_t smem = static_cast<size_t>(full && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * block;
+    const Mode mode = mode_of(G, full);
+    size_t smem = static_cast<size_t>(mode != kPlain && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * block;
     const size_t combine = static_cast<size_t>(G.groups) * G.dim * sizeof(float);
     if (G.groups > 1 && combine > smem) smem = combine;
-    auto* kernel = full ? backward_kernel<kNV, true, Act, Res> : backward_kernel<kNV, false, Act, Res>;
+    auto* kernel = mode == kPlain   ? backward_kernel<kNV, kPlain, Act, Res>
+                   : mode == kWhole ? backward_kernel<kNV, kWhole, Act, Res>
+                                    : backward_kernel<kNV, kEdges, Act, Res>;
     if (smem > 32 * 1024 && // beside the static words
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
