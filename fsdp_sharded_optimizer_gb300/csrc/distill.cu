@@ -28,7 +28,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -231,18 +230,447 @@ distill_kernel(const Args A)
     }
 }
 
+// ------------------------------------------------ the row stays on the chip
+// One cluster of `ranks` blocks per row; rank r holds the row's r-th part in
+// shared memory, as the 16-byte pieces of memory that it lies in (a row may
+// start at any element: the first and the last piece are then partly outside,
+// read element by element, and hold -inf there).  A thread owns the same slots
+// for all rows and is the only one that reads or fills them, so it asks for
+// the next row's piece (cp.async) as soon as it has used this row's for the
+// last time, and no barrier stands between a row's loads and the one before.
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kMaxRanks = 8;
+
+// How many exponentials a logit takes.
+//   kOne     one: temperature 1, or no labels
+//   kSquare  temperature 2: e^(x/2), and its square
+//   kTwo     two
+enum Exps { kOne = 0, kSquare = 1, kTwo = 2 };
+
 template <typename T>
-int launch(const Args& A, bool grad, cudaStream_t stream)
+struct Piece { // 16 bytes of a row
+    static constexpr int kElems = 16 / sizeof(T), kPairs = kElems / 2;
+};
+__device__ __forceinline__ void unpack_piece(const uint4& w, float2 (&x)[4], Bf16)
 {
-    const void* kernel = grad ? reinterpret_cast<const void*>(distill_kernel<T, true>)
-                              : reinterpret_cast<const void*>(distill_kernel<T, false>);
-    const int resident = persistent_blocks(kernel, kThreads, 0);
+    x[0] = make_float2(dev::bf16_lo(w.x), dev::bf16_hi(w.x));
+    x[1] = make_float2(dev::bf16_lo(w.y), dev::bf16_hi(w.y));
+    x[2] = make_float2(dev::bf16_lo(w.z), dev::bf16_hi(w.z));
+    x[3] = make_float2(dev::bf16_lo(w.w), dev::bf16_hi(w.w));
+}
+__device__ __forceinline__ void unpack_piece(const uint4& w, float2 (&x)[2], float)
+{
+    x[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+}
+__device__ __forceinline__ uint4 pack_piece(const float2 (&x)[4], Bf16)
+{
+    return make_uint4(dev::cvt_bf16x2(x[0].x, x[0].y), dev::cvt_bf16x2(x[1].x, x[1].y),
+                      dev::cvt_bf16x2(x[2].x, x[2].y), dev::cvt_bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ uint4 pack_piece(const float2 (&x)[2], float)
+{
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
+}
+// The largest element (a NaN is passed over).
+__device__ __forceinline__ float piece_max(const uint4& w, Bf16)
+{
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(dev::bf16_lo(a), dev::bf16_hi(a));
+}
+__device__ __forceinline__ float piece_max(const uint4& w, float)
+{
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                 fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ uint4 lowest_piece(Bf16)
+{
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+}
+__device__ __forceinline__ uint4 lowest_piece(float)
+{
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+}
+__device__ __forceinline__ float2 exp2_pair(float2 a)
+{
+    return make_float2(exp2_approx(a.x), exp2_approx(a.y));
+}
+
+// Fills slot j of a row that starts at p and has n elements.
+template <typename T>
+__device__ __forceinline__ void fetch_piece(uint4* slot, const T* p, int64_t n, int64_t piece)
+{
+    constexpr int kE = Piece<T>::kElems;
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    const int64_t first = piece * kE - mis; // its first element
+    if (first >= 0 && first + kE <= n) {
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + first)
+                     : "memory");
+        return;
+    }
+    *slot = lowest_piece(T());
+    T* e = reinterpret_cast<T*>(slot);
+    for (int i = 0; i < kE; ++i)
+        if (first + i >= 0 && first + i < n) e[i] = p[first + i];
+}
+
+struct RowShared {
+    float red[2][4][kRowWarps];      // maxima, sums; of the block's warps
+    float ranks[2][kMaxRanks][3];    // by row parity: every rank's maximum and sums
+};
+
+template <typename T, bool kGrad, int kExps>
+__global__ void __launch_bounds__(kRowThreads)
+row_kernel(const Args A, int ranks, int slots)
+{
+    constexpr int kE = Piece<T>::kElems, kP = Piece<T>::kPairs;
+    constexpr int kBatch = 4; // pieces a thread has in registers at once
+    extern __shared__ uint4 part[]; // [slots], then top_p, top_s, top_id
+    __shared__ RowShared sh;
+    float* top_p = reinterpret_cast<float*>(part + slots);
+    float* top_s = top_p + A.top;
+    int32_t* top_id = reinterpret_cast<int32_t*>(top_s + A.top);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = ranks > 1 ? static_cast<int>(blockIdx.x % ranks) : 0;
+    const int64_t clusters = gridDim.x / ranks;
+    const float inv_tau = 1.0f / A.tau;
+    const float c2 = kLog2e * inv_tau; // kOne: the only one
+    const int64_t vocab = A.vocab;
+    const int64_t first_piece = static_cast<int64_t>(rank) * slots;
+
+    auto row_of = [&](int64_t row) { return static_cast<const T*>(A.logits) + row * A.stride; };
+    // This rank's pieces of a row (the number depends on where the row starts).
+    auto pieces = [&](const T* p) {
+        const int64_t mis = (reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T);
+        const int64_t n = (mis + vocab + kE - 1) / kE - first_piece;
+        return static_cast<int>(n < 0 ? 0 : n < slots ? n : slots);
+    };
+    auto weight = [&](int64_t row) { return A.row_weight ? A.row_weight[row] : 1.0f; };
+
+    if (ranks > 1) // every block has begun before another writes to its shared memory
+        asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                     "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    int64_t row = blockIdx.x / ranks;
+    float w = 0.0f;
+    if (row < A.rows) {
+        w = weight(row);
+        if (w != 0.0f) {
+            const T* p = row_of(row);
+            const int n = pieces(p);
+            for (int j = tid; j < n; j += kRowThreads) fetch_piece(part + j, p, vocab, first_piece + j);
+        }
+    }
+    int parity = 0;
+    for (; row < A.rows; row += clusters) {
+        const int64_t next = row + clusters;
+        const float w_next = next < A.rows ? weight(next) : 0.0f; // 0: nothing to fetch
+        const T* s = row_of(row);
+        T* ds = kGrad ? static_cast<T*>(A.dlogits) + row * A.dstride : nullptr;
+        const T* s_next = row_of(next);
+        const int n_next = w_next != 0.0f ? pieces(s_next) : 0;
+        const int n = pieces(s);
+        const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(s) & 15) / sizeof(T));
+        // element range of this rank
+        const int64_t lo = first_piece * kE - mis;
+        const int64_t hi = lo + static_cast<int64_t>(n) * kE;
+        if (w == 0.0f) { // a masked row: not read
+            if (rank == 0 && tid == 0) {
+                A.ce[row] = 0.0f;
+                A.kl[row] = 0.0f;
+            }
+            if (kGrad)
+                for (int64_t j = lo + tid; j < hi; j += kRowThreads)
+                    if (j >= 0 && j < vocab) dev::store1(ds + j, 0.0f);
+            for (int j = tid; j < n_next; j += kRowThreads)
+                fetch_piece(part + j, s_next, vocab, first_piece + j);
+            w = w_next;
+            continue; // the whole cluster does
+        }
+        // the teacher's entries; the student's logits there
+        float tm = -INFINITY;
+        for (int k = tid; k < A.top; k += kRowThreads) {
+            const int64_t id = dev::load_index(A.ids, A.id_type, row * A.top + k);
+            const bool counted = id >= 0 && id < vocab;
+            float t[1] = {-INFINITY};
+            if (counted) dev::load_any<1>(A.teacher, A.teacher_type, row * A.top + k, t);
+            tm = fmaxf(tm, t[0]);
+            top_id[k] = counted ? static_cast<int32_t>(id) : -1;
+            top_p[k] = t[0];
+            top_s[k] = counted ? dev::load1(s + id) : 0.0f;
+        }
+        const int64_t label = A.labels ? dev::load_index(A.labels, A.label_type, row) : -1;
+        const bool labelled = label >= 0 && label < vocab;
+        const float s_label = labelled ? dev::load1(s + label) : 0.0f;
+
+        // pass 1: the maximum, and the sums relative to it
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        float m = -INFINITY;
+        float2 z1 = dev::pair(0.0f), z2 = z1;
+        for (int j0 = tid; j0 < n; j0 += kRowThreads * kBatch) {
+            uint4 raw[kBatch];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int j = j0 + u * kRowThreads;
+                raw[u] = j < n ? part[j] : lowest_piece(T());
+                mx = fmaxf(mx, piece_max(raw[u], T()));
+            }
+            if (mx > m) {
+                const float f2 = exp2_approx((m - mx) * c2);
+                z2 = dev::mul2(z2, dev::pair(f2));
+                if (kExps == kSquare) z1 = dev::mul2(z1, dev::pair(f2 * f2));
+                if (kExps == kTwo)
+                    z1 = dev::mul2(z1, dev::pair(exp2_approx((m - mx) * kLog2e)));
+                m = mx;
+            }
+            const float2 base = dev::pair(m == -INFINITY ? 0.0f : -m);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                float2 x[kP];
+                unpack_piece(raw[u], x, T());
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    const float2 d = dev::add2(x[e], base);
+                    const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
+                    z2 = dev::add2(z2, e2);
+                    if (kExps == kSquare) z1 = dev::fma2(e2, e2, z1);
+                    if (kExps == kTwo)
+                        z1 = dev::add2(z1, exp2_pair(dev::mul2(d, dev::pair(kLog2e))));
+                }
+                if (!kGrad) {
+                    const int j = j0 + u * kRowThreads;
+                    if (j < n_next) fetch_piece(part + j, s_next, vocab, first_piece + j);
+                }
+            }
+        }
+        if (!kGrad) { // slots that this row did not use, and the next does
+            for (int j = (n - tid + kRowThreads * kBatch - 1) / (kRowThreads * kBatch) *
+                             (kRowThreads * kBatch) + tid;
+                 j < n_next; j += kRowThreads)
+                fetch_piece(part + j, s_next, vocab, first_piece + j);
+        }
+
+        // the block's maxima
+        float block_m = m;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            block_m = fmaxf(block_m, __shfl_xor_sync(0xFFFFFFFFu, block_m, off));
+            tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, off));
+        }
+        if (lane == 0) {
+            sh.red[0][0][warp] = block_m;
+            sh.red[0][1][warp] = tm;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRowWarps; ++i) {
+            block_m = fmaxf(block_m, sh.red[0][0][i]);
+            tm = fmaxf(tm, sh.red[0][1][i]);
+        }
+        const float base = block_m == -INFINITY ? 0.0f : block_m;
+        const float tbase = tm == -INFINITY ? 0.0f : tm;
+        // its sums
+        float v[4] = {z1.x + z1.y, z2.x + z2.y, 0.0f, 0.0f};
+        if (m > -INFINITY) {
+            const float f2 = exp2_approx((m - base) * c2);
+            v[1] *= f2;
+            v[0] *= kExps == kSquare ? f2 * f2 : kExps == kTwo ? exp2_approx((m - base) * kLog2e) : 0.0f;
+        }
+        for (int k = tid; k < A.top; k += kRowThreads) {
+            const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
+            v[2] += e;
+            if (e != 0.0f)
+                v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - base)) * inv_tau, v[3]);
+            top_p[k] = e;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], off);
+            if (lane == 0) sh.red[1][i][warp] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kRowWarps; ++k) v[i] += sh.red[1][i][k];
+        }
+        float row_m = base, zs1 = v[0], zs2 = v[1], cross = v[3];
+        const float zt = v[2];
+        if (ranks > 1) { // the cluster's
+            if (tid < ranks) {
+                const uint32_t here =
+                    static_cast<uint32_t>(__cvta_generic_to_shared(&sh.ranks[parity][rank][0]));
+                uint32_t there;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(tid));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(block_m) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4), "f"(v[0]) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 8), "f"(v[1]) : "memory");
+            }
+            asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            float most = -INFINITY;
+            for (int r = 0; r < ranks; ++r) most = fmaxf(most, sh.ranks[parity][r][0]);
+            row_m = most == -INFINITY ? 0.0f : most;
+            zs1 = zs2 = 0.0f;
+            for (int r = 0; r < ranks; ++r) {
+                const float rm = sh.ranks[parity][r][0];
+                // a part without anything above -inf holds 0, or NaN
+                const float f2 = rm == -INFINITY ? 1.0f : exp2_approx((rm - row_m) * c2);
+                const float f1 = kExps == kSquare ? f2 * f2
+                                 : kExps == kTwo && rm != -INFINITY
+                                     ? exp2_approx((rm - row_m) * kLog2e)
+                                     : 1.0f;
+                zs1 = fmaf(sh.ranks[parity][r][1], f1, zs1);
+                zs2 = fmaf(sh.ranks[parity][r][2], f2, zs2);
+            }
+            cross = fmaf(zt, (row_m - base) * inv_tau, cross);
+            parity ^= 1;
+        }
+        if (kExps == kOne) zs1 = zs2;
+        // a row whose logits are all -inf has no distribution, a teacher whose
+        // counted entries are all -inf (or none) has none either; a NaN is neither
+        const bool empty = zs2 == 0.0f;
+        const bool has_top = zt != 0.0f && !empty;
+        const bool has_label = labelled && !empty;
+        if (rank == 0 && tid == 0) {
+            A.ce[row] = has_label ? logf(zs1) - (s_label - row_m) : 0.0f;
+            A.kl[row] = has_top ? A.tau * A.tau * (cross / zt + (logf(zs2) - logf(zt))) : 0.0f;
+        }
+        if constexpr (kGrad) {
+            const float hit = has_label ? w * A.ce_weight : 0.0f;
+            const float pull = has_top ? w * A.kl_weight * A.tau : 0.0f;
+            const float share = has_top ? pull / zt : 0.0f;
+            // an empty row is all 0: its exponentials are of -inf, and taken from 0
+            float a1 = has_label ? hit / zs1 : 0.0f, a2 = has_top ? pull / zs2 : 0.0f;
+            if (kExps == kOne) a2 += a1;
+            auto dense = [&](float2 x) {
+                const float2 d = dev::add2(x, dev::pair(-row_m));
+                const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
+                float2 g = dev::mul2(e2, dev::pair(a2));
+                if (kExps == kSquare) g = dev::fma2(dev::mul2(e2, e2), dev::pair(a1), g);
+                if (kExps == kTwo)
+                    g = dev::fma2(exp2_pair(dev::mul2(d, dev::pair(kLog2e))), dev::pair(a1), g);
+                return g;
+            };
+            const bool has_any = has_top || has_label; // else +0, whatever the logits are
+            const bool alike = ((reinterpret_cast<uintptr_t>(ds) ^ reinterpret_cast<uintptr_t>(s)) & 15) == 0;
+#pragma unroll 4
+            for (int j = tid; j < n; j += kRowThreads) {
+                const uint4 raw = part[j];
+                float2 x[kP];
+                unpack_piece(raw, x, T());
+#pragma unroll
+                for (int e = 0; e < kP; ++e) x[e] = has_any ? dense(x[e]) : dev::pair(0.0f);
+                const int64_t at = lo + static_cast<int64_t>(j) * kE;
+                if (alike && at >= 0 && at + kE <= vocab) {
+                    __stcs(reinterpret_cast<uint4*>(ds + at), pack_piece(x, T()));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kE; ++e)
+                        if (at + e >= 0 && at + e < vocab)
+                            dev::store1(ds + at + e, e & 1 ? x[e / 2].y : x[e / 2].x);
+                }
+                if (j < n_next) fetch_piece(part + j, s_next, vocab, first_piece + j);
+            }
+            for (int j = (n - tid + kRowThreads - 1) / kRowThreads * kRowThreads + tid; j < n_next;
+                 j += kRowThreads)
+                fetch_piece(part + j, s_next, vocab, first_piece + j);
+            __syncthreads(); // before the teacher's entries are written over
+            bool label_in_top = false;
+            for (int k = tid; k < A.top; k += kRowThreads) {
+                const int32_t id = top_id[k];
+                if (id < 0) continue;
+                if (labelled && id == label) label_in_top = true;
+                if (id < lo || id >= hi) continue; // another rank's
+                bool first = true; // the first entry of an id writes for all of them
+                float p = 0.0f;
+                for (int q = 0; q < A.top; ++q) {
+                    if (top_id[q] != id) continue;
+                    if (q < k) first = false;
+                    p += top_p[q];
+                }
+                if (!first) continue;
+                float g = dense(dev::pair(top_s[k])).x;
+                g = fmaf(-share, p, g);
+                if (id == label) g -= hit;
+                dev::store1(ds + id, g);
+            }
+            // also orders this row's use of top_* before the next row's
+            if (!__syncthreads_or(label_in_top) && has_label && tid == 0 && label >= lo && label < hi)
+                dev::store1(ds + label, dense(dev::pair(s_label)).x - hit);
+        } else {
+            __syncthreads(); // this row's use of top_* before the next row's
+        }
+        w = w_next;
+    }
+    // no block ends while another may still write to its shared memory
+    if (ranks > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                     "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Bytes of a row that a block should hold, and may hold.
+constexpr int64_t kPartBytes = 56 * 1024, kMostPartBytes = 196 * 1024;
+
+template <typename T, bool kGrad, int kExps>
+int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
+{
+    const int64_t pieces = (A.vocab + 2 * (Piece<T>::kElems - 1)) / Piece<T>::kElems + 1;
+    int ranks = 1;
+    while (ranks < kMaxRanks &&
+           ((pieces + ranks - 1) / ranks * 16 > kPartBytes || A.rows * ranks * 2 <= 152))
+        ranks *= 2;
+    const int64_t slots = (pieces + ranks - 1) / ranks;
+    const size_t smem = static_cast<size_t>(slots) * 16 + static_cast<size_t>(A.top) * 12;
+    fits = slots * 16 <= kMostPartBytes;
+    if (!fits) return ZERO_OK;
+    auto* kernel = row_kernel<T, kGrad, kExps>;
+    const void* k = reinterpret_cast<const void*>(kernel);
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+        return ZERO_ECUDA;
+    const int resident = persistent_blocks(k, kRowThreads, smem);
+    if (resident < 1) return ZERO_ECUDA;
+    int64_t clusters = resident / ranks;
+    if (clusters < 1) clusters = 1;
+    if (clusters > A.rows) clusters = A.rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A, ranks, static_cast<int>(slots)));
+}
+
+template <typename T, bool kGrad>
+int launch(const Args& A, cudaStream_t stream)
+{
+    bool fits = false;
+    const int rc = !A.labels || A.tau == 1.0f ? launch_rows<T, kGrad, kOne>(A, stream, fits)
+                   : A.tau == 2.0f            ? launch_rows<T, kGrad, kSquare>(A, stream, fits)
+                                              : launch_rows<T, kGrad, kTwo>(A, stream, fits);
+    if (rc != ZERO_OK || fits) return rc;
+    // a row that not even 8 blocks can hold is read twice
+    const int resident =
+        persistent_blocks(reinterpret_cast<const void*>(distill_kernel<T, kGrad>), kThreads, 0);
     if (resident < 1) return ZERO_ECUDA;
     const unsigned blocks = static_cast<unsigned>(A.rows < resident ? A.rows : resident);
-    if (grad)
-        distill_kernel<T, true><<<blocks, kThreads, 0, stream>>>(A);
-    else
-        distill_kernel<T, false><<<blocks, kThreads, 0, stream>>>(A);
+    distill_kernel<T, kGrad><<<blocks, kThreads, 0, stream>>>(A);
     return cuda_status(cudaGetLastError());
 }
 
@@ -290,8 +718,9 @@ int distill(const zero_distill_t* d, const void* logits, const void* teacher_log
     A.tau = static_cast<float>(d->temperature);
     A.ce_weight = static_cast<float>(d->ce_weight);
     A.kl_weight = static_cast<float>(d->kl_weight);
-    return d->logits_type == ZERO_TYPE_BF16 ? launch<Bf16>(A, grad, stream)
-                                            : launch<float>(A, grad, stream);
+    if (d->logits_type == ZERO_TYPE_BF16)
+        return grad ? launch<Bf16, true>(A, stream) : launch<Bf16, false>(A, stream);
+    return grad ? launch<float, true>(A, stream) : launch<float, false>(A, stream);
 }
 
 } // namespace
