@@ -301,28 +301,78 @@ __device__ __forceinline__ float2 exp2_pair(float2 a)
     return make_float2(exp2_approx(a.x), exp2_approx(a.y));
 }
 
-// Fills slot j of a row that starts at p and has n elements.
+__device__ __forceinline__ float warp_max(float x) // a NaN is passed over
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Sums of 4 values over the warp: lane 8 i (and the 7 that follow) get value
+// i's.  A lane keeps half of the values at each of the first two steps.
+__device__ __forceinline__ float warp_sum4(const float (&v)[4], int lane)
+{
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const bool up = lane & 16, odd = lane & 8;
+    const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(kAll, up ? v[0] : v[2], 16);
+    const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(kAll, up ? v[1] : v[3], 16);
+    float x = (odd ? b : a) + __shfl_xor_sync(kAll, odd ? a : b, 8);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+    return x;
+}
+
+// A rank's part of a row: slots [0, n), of which [from, to) lie wholly inside
+// the row; element i of slot j is column lo + j * kElems + i.
 template <typename T>
-__device__ __forceinline__ void fetch_piece(uint4* slot, const T* p, int64_t n, int64_t piece)
+struct Part {
+    const T* row;
+    int64_t lo;
+    int n, from, to;
+
+    __device__ __forceinline__ Part(const T* p, int64_t vocab, int64_t first_piece, int slots)
+    {
+        constexpr int kE = Piece<T>::kElems;
+        const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+        row = p;
+        lo = first_piece * kE - mis;
+        const int64_t left = vocab - lo; // elements from slot 0 to the row's end
+        const int64_t all = left <= 0 ? 0 : (left + kE - 1) / kE;
+        n = static_cast<int>(all < slots ? all : slots);
+        from = lo < 0 ? 1 : 0;
+        const int64_t whole = left <= 0 ? 0 : left / kE;
+        to = static_cast<int>(whole < n ? whole : n);
+    }
+};
+// Asks for slot j where it lies inside the row.
+template <typename T>
+__device__ __forceinline__ void fetch_whole(uint32_t part, const Part<T>& p, int j)
+{
+    if (j >= p.from && j < p.to)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(part + 16u * j),
+                     "l"(p.row + p.lo + static_cast<int64_t>(j) * Piece<T>::kElems)
+                     : "memory");
+}
+// Fills the slots at the row's ends: at most one before `from`, one from `to`.
+template <typename T>
+__device__ __forceinline__ void fetch_ends(uint4* part, const Part<T>& p, int64_t vocab)
 {
     constexpr int kE = Piece<T>::kElems;
-    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-    const int64_t first = piece * kE - mis; // its first element
-    if (first >= 0 && first + kE <= n) {
-        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + first)
-                     : "memory");
-        return;
-    }
-    *slot = lowest_piece(T());
-    T* e = reinterpret_cast<T*>(slot);
-    for (int i = 0; i < kE; ++i)
-        if (first + i >= 0 && first + i < n) e[i] = p[first + i];
+    auto fill = [&](int j) {
+        if (j % kRowThreads != static_cast<int>(threadIdx.x)) return; // its owner
+        part[j] = lowest_piece(T());
+        T* e = reinterpret_cast<T*>(part + j);
+        const int64_t at = p.lo + static_cast<int64_t>(j) * kE;
+        for (int i = 0; i < kE; ++i)
+            if (at + i >= 0 && at + i < vocab) e[i] = p.row[at + i];
+    };
+    if (p.from == 1 && p.n > 0) fill(0);
+    if (p.to < p.n && p.to >= p.from) fill(p.to);
 }
 
 struct RowShared {
-    float red[2][4][kRowWarps];      // maxima, sums; of the block's warps
-    float ranks[2][kMaxRanks][3];    // by row parity: every rank's maximum and sums
+    float most[2][kRowWarps];     // maxima of the block's warps: logits, teacher
+    float sum[4][kRowWarps];      // sums of the block's warps
+    float ranks[2][kMaxRanks][3]; // by row parity: every rank's maximum and sums
 };
 
 template <typename T, bool kGrad, int kExps>
@@ -331,11 +381,14 @@ row_kernel(const Args A, int ranks, int slots)
 {
     constexpr int kE = Piece<T>::kElems, kP = Piece<T>::kPairs;
     constexpr int kBatch = 4; // pieces a thread has in registers at once
-    extern __shared__ uint4 part[]; // [slots], then top_p, top_s, top_id
+    extern __shared__ uint4 part[]; // [slots]; top_p, top_s, top_id; marks
     __shared__ RowShared sh;
     float* top_p = reinterpret_cast<float*>(part + slots);
     float* top_s = top_p + A.top;
     int32_t* top_id = reinterpret_cast<int32_t*>(top_s + A.top);
+    // a bit for each of the part's columns: the teacher's entries
+    uint32_t* marks = reinterpret_cast<uint32_t*>(top_id + A.top);
+    const uint32_t part_at = static_cast<uint32_t>(__cvta_generic_to_shared(part));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = ranks > 1 ? static_cast<int>(blockIdx.x % ranks) : 0;
     const int64_t clusters = gridDim.x / ranks;
@@ -344,41 +397,35 @@ row_kernel(const Args A, int ranks, int slots)
     const int64_t vocab = A.vocab;
     const int64_t first_piece = static_cast<int64_t>(rank) * slots;
 
-    auto row_of = [&](int64_t row) { return static_cast<const T*>(A.logits) + row * A.stride; };
-    // This rank's pieces of a row (the number depends on where the row starts).
-    auto pieces = [&](const T* p) {
-        const int64_t mis = (reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T);
-        const int64_t n = (mis + vocab + kE - 1) / kE - first_piece;
-        return static_cast<int>(n < 0 ? 0 : n < slots ? n : slots);
+    auto part_of = [&](int64_t row) {
+        return Part<T>(static_cast<const T*>(A.logits) + row * A.stride, vocab, first_piece, slots);
     };
     auto weight = [&](int64_t row) { return A.row_weight ? A.row_weight[row] : 1.0f; };
 
+    if (kGrad)
+        for (int i = tid; i < (slots * kE + 31) / 32; i += kRowThreads) marks[i] = 0;
     if (ranks > 1) // every block has begun before another writes to its shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;\n"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
     int64_t row = blockIdx.x / ranks;
-    float w = 0.0f;
-    if (row < A.rows) {
-        w = weight(row);
-        if (w != 0.0f) {
-            const T* p = row_of(row);
-            const int n = pieces(p);
-            for (int j = tid; j < n; j += kRowThreads) fetch_piece(part + j, p, vocab, first_piece + j);
-        }
+    float w = row < A.rows ? weight(row) : 0.0f;
+    Part<T> here = part_of(row < A.rows ? row : 0);
+    if (w != 0.0f) {
+        for (int j = tid; j < here.to; j += kRowThreads) fetch_whole(part_at, here, j);
+        fetch_ends(part, here, vocab);
     }
     int parity = 0;
     for (; row < A.rows; row += clusters) {
         const int64_t next = row + clusters;
         const float w_next = next < A.rows ? weight(next) : 0.0f; // 0: nothing to fetch
-        const T* s = row_of(row);
+        Part<T> then = part_of(next < A.rows ? next : 0);
+        if (w_next == 0.0f) then.n = then.from = then.to = 0;
+        const T* s = here.row;
         T* ds = kGrad ? static_cast<T*>(A.dlogits) + row * A.dstride : nullptr;
-        const T* s_next = row_of(next);
-        const int n_next = w_next != 0.0f ? pieces(s_next) : 0;
-        const int n = pieces(s);
-        const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(s) & 15) / sizeof(T));
-        // element range of this rank
-        const int64_t lo = first_piece * kE - mis;
-        const int64_t hi = lo + static_cast<int64_t>(n) * kE;
+        const int n = here.n;
+        const int64_t lo = here.lo, hi = lo + static_cast<int64_t>(n) * kE;
         if (w == 0.0f) { // a masked row: not read
             if (rank == 0 && tid == 0) {
                 A.ce[row] = 0.0f;
@@ -387,13 +434,15 @@ row_kernel(const Args A, int ranks, int slots)
             if (kGrad)
                 for (int64_t j = lo + tid; j < hi; j += kRowThreads)
                     if (j >= 0 && j < vocab) dev::store1(ds + j, 0.0f);
-            for (int j = tid; j < n_next; j += kRowThreads)
-                fetch_piece(part + j, s_next, vocab, first_piece + j);
+            for (int j = tid; j < then.to; j += kRowThreads) fetch_whole(part_at, then, j);
+            fetch_ends(part, then, vocab);
             w = w_next;
+            here = part_of(next < A.rows ? next : 0);
             continue; // the whole cluster does
         }
         // the teacher's entries; the student's logits there
         float tm = -INFINITY;
+        bool twice = false; // an id of this part that an earlier entry has
         for (int k = tid; k < A.top; k += kRowThreads) {
             const int64_t id = dev::load_index(A.ids, A.id_type, row * A.top + k);
             const bool counted = id >= 0 && id < vocab;
@@ -403,6 +452,10 @@ row_kernel(const Args A, int ranks, int slots)
             top_id[k] = counted ? static_cast<int32_t>(id) : -1;
             top_p[k] = t[0];
             top_s[k] = counted ? dev::load1(s + id) : 0.0f;
+            if (kGrad && counted && id >= lo && id < hi) {
+                const uint32_t bit = 1u << (static_cast<uint32_t>(id - lo) & 31u);
+                twice |= (atomicOr(&marks[(id - lo) >> 5], bit) & bit) != 0;
+            }
         }
         const int64_t label = A.labels ? dev::load_index(A.labels, A.label_type, row) : -1;
         const bool labelled = label >= 0 && label < vocab;
@@ -412,7 +465,8 @@ row_kernel(const Args A, int ranks, int slots)
         asm volatile("cp.async.wait_all;" ::: "memory");
         float m = -INFINITY;
         float2 z1 = dev::pair(0.0f), z2 = z1;
-        for (int j0 = tid; j0 < n; j0 += kRowThreads * kBatch) {
+        int j0 = tid;
+        for (; j0 < n; j0 += kRowThreads * kBatch) {
             uint4 raw[kBatch];
             float mx = -INFINITY;
 #pragma unroll
@@ -443,36 +497,24 @@ row_kernel(const Args A, int ranks, int slots)
                     if (kExps == kTwo)
                         z1 = dev::add2(z1, exp2_pair(dev::mul2(d, dev::pair(kLog2e))));
                 }
-                if (!kGrad) {
-                    const int j = j0 + u * kRowThreads;
-                    if (j < n_next) fetch_piece(part + j, s_next, vocab, first_piece + j);
-                }
+                if (!kGrad) fetch_whole(part_at, then, j0 + u * kRowThreads);
             }
         }
-        if (!kGrad) { // slots that this row did not use, and the next does
-            for (int j = (n - tid + kRowThreads * kBatch - 1) / (kRowThreads * kBatch) *
-                             (kRowThreads * kBatch) + tid;
-                 j < n_next; j += kRowThreads)
-                fetch_piece(part + j, s_next, vocab, first_piece + j);
+        if (!kGrad) { // slots that the next row has beyond this one's
+            for (; j0 < then.to; j0 += kRowThreads) fetch_whole(part_at, then, j0);
+            fetch_ends(part, then, vocab);
         }
 
         // the block's maxima
-        float block_m = m;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            block_m = fmaxf(block_m, __shfl_xor_sync(0xFFFFFFFFu, block_m, off));
-            tm = fmaxf(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, off));
-        }
+        float block_m = warp_max(m);
+        tm = warp_max(tm);
         if (lane == 0) {
-            sh.red[0][0][warp] = block_m;
-            sh.red[0][1][warp] = tm;
+            sh.most[0][warp] = block_m;
+            sh.most[1][warp] = tm;
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kRowWarps; ++i) {
-            block_m = fmaxf(block_m, sh.red[0][0][i]);
-            tm = fmaxf(tm, sh.red[0][1][i]);
-        }
+        twice = __syncthreads_or(twice);
+        block_m = warp_max(sh.most[0][lane % kRowWarps]);
+        tm = warp_max(sh.most[1][lane % kRowWarps]);
         const float base = block_m == -INFINITY ? 0.0f : block_m;
         const float tbase = tm == -INFINITY ? 0.0f : tm;
         // its sums
@@ -489,27 +531,23 @@ row_kernel(const Args A, int ranks, int slots)
                 v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - base)) * inv_tau, v[3]);
             top_p[k] = e;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], off);
-            if (lane == 0) sh.red[1][i][warp] = v[i];
-        }
+        const float sum = warp_sum4(v, lane);
+        if (lane % 8 == 0) sh.sum[lane / 8][warp] = sum;
         __syncthreads();
+        float all = sh.sum[lane / 8][lane % 8];
+        static_assert(kRowWarps == 8, "a lane for each warp and value");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = 0.0f;
+        for (int off = 4; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
 #pragma unroll
-            for (int k = 0; k < kRowWarps; ++k) v[i] += sh.red[1][i][k];
-        }
+        for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, all, 8 * i);
         float row_m = base, zs1 = v[0], zs2 = v[1], cross = v[3];
         const float zt = v[2];
         if (ranks > 1) { // the cluster's
             if (tid < ranks) {
-                const uint32_t here =
+                const uint32_t mine =
                     static_cast<uint32_t>(__cvta_generic_to_shared(&sh.ranks[parity][rank][0]));
                 uint32_t there;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(tid));
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(tid));
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(block_m) : "memory");
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 4), "f"(v[0]) : "memory");
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + 8), "f"(v[1]) : "memory");
@@ -547,10 +585,11 @@ row_kernel(const Args A, int ranks, int slots)
         if constexpr (kGrad) {
             const float hit = has_label ? w * A.ce_weight : 0.0f;
             const float pull = has_top ? w * A.kl_weight * A.tau : 0.0f;
-            const float share = has_top ? pull / zt : 0.0f;
-            // an empty row is all 0: its exponentials are of -inf, and taken from 0
-            float a1 = has_label ? hit / zs1 : 0.0f, a2 = has_top ? pull / zs2 : 0.0f;
+            const float share = has_top ? __fdividef(pull, zt) : 0.0f;
+            float a1 = has_label ? __fdividef(hit, zs1) : 0.0f;
+            float a2 = has_top ? __fdividef(pull, zs2) : 0.0f;
             if (kExps == kOne) a2 += a1;
+            const bool has_any = has_top || has_label; // else +0, whatever the logits are
             auto dense = [&](float2 x) {
                 const float2 d = dev::add2(x, dev::pair(-row_m));
                 const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
@@ -560,56 +599,63 @@ row_kernel(const Args A, int ranks, int slots)
                     g = dev::fma2(exp2_pair(dev::mul2(d, dev::pair(kLog2e))), dev::pair(a1), g);
                 return g;
             };
-            const bool has_any = has_top || has_label; // else +0, whatever the logits are
             const bool alike = ((reinterpret_cast<uintptr_t>(ds) ^ reinterpret_cast<uintptr_t>(s)) & 15) == 0;
+            // slots that are written 16 bytes at once
+            const int wide_from = alike ? here.from : n, wide_to = alike ? here.to : n;
+            T* out = ds + lo;
+            int j = tid;
 #pragma unroll 4
-            for (int j = tid; j < n; j += kRowThreads) {
+            for (; j < n; j += kRowThreads) {
                 const uint4 raw = part[j];
                 float2 x[kP];
                 unpack_piece(raw, x, T());
 #pragma unroll
                 for (int e = 0; e < kP; ++e) x[e] = has_any ? dense(x[e]) : dev::pair(0.0f);
-                const int64_t at = lo + static_cast<int64_t>(j) * kE;
-                if (alike && at >= 0 && at + kE <= vocab) {
-                    __stcs(reinterpret_cast<uint4*>(ds + at), pack_piece(x, T()));
+                if (j >= wide_from && j < wide_to) {
+                    __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * kE),
+                           pack_piece(x, T()));
                 } else {
+                    const int64_t at = lo + static_cast<int64_t>(j) * kE;
 #pragma unroll
                     for (int e = 0; e < kE; ++e)
                         if (at + e >= 0 && at + e < vocab)
                             dev::store1(ds + at + e, e & 1 ? x[e / 2].y : x[e / 2].x);
                 }
-                if (j < n_next) fetch_piece(part + j, s_next, vocab, first_piece + j);
+                fetch_whole(part_at, then, j);
             }
-            for (int j = (n - tid + kRowThreads - 1) / kRowThreads * kRowThreads + tid; j < n_next;
-                 j += kRowThreads)
-                fetch_piece(part + j, s_next, vocab, first_piece + j);
+            for (; j < then.to; j += kRowThreads) fetch_whole(part_at, then, j);
+            fetch_ends(part, then, vocab);
             __syncthreads(); // before the teacher's entries are written over
-            bool label_in_top = false;
+            if (labelled && label >= lo && label < hi && has_label && tid == 0 &&
+                !(marks[(label - lo) >> 5] >> ((label - lo) & 31) & 1))
+                dev::store1(ds + label, dense(dev::pair(s_label)).x - hit);
             for (int k = tid; k < A.top; k += kRowThreads) {
                 const int32_t id = top_id[k];
-                if (id < 0) continue;
-                if (labelled && id == label) label_in_top = true;
-                if (id < lo || id >= hi) continue; // another rank's
-                bool first = true; // the first entry of an id writes for all of them
-                float p = 0.0f;
-                for (int q = 0; q < A.top; ++q) {
-                    if (top_id[q] != id) continue;
-                    if (q < k) first = false;
-                    p += top_p[q];
+                if (id < lo || id >= hi || id < 0) continue; // not counted, or another rank's
+                float p = top_p[k];
+                if (twice) { // the first entry of an id writes for all of them
+                    bool first = true;
+                    p = 0.0f;
+                    for (int q = 0; q < A.top; ++q) {
+                        if (top_id[q] != id) continue;
+                        if (q < k) first = false;
+                        p += top_p[q];
+                    }
+                    if (!first) continue;
                 }
-                if (!first) continue;
-                float g = dense(dev::pair(top_s[k])).x;
-                g = fmaf(-share, p, g);
+                float g = has_any ? fmaf(-share, p, dense(dev::pair(top_s[k])).x) : 0.0f;
                 if (id == label) g -= hit;
                 dev::store1(ds + id, g);
             }
-            // also orders this row's use of top_* before the next row's
-            if (!__syncthreads_or(label_in_top) && has_label && tid == 0 && label >= lo && label < hi)
-                dev::store1(ds + label, dense(dev::pair(s_label)).x - hit);
-        } else {
-            __syncthreads(); // this row's use of top_* before the next row's
+            __syncthreads(); // the label's look at the marks
+            for (int k = tid; k < A.top; k += kRowThreads) {
+                const int32_t id = top_id[k];
+                if (id >= lo && id < hi && id >= 0) marks[(id - lo) >> 5] = 0;
+            }
         }
+        __syncthreads(); // this row's use of top_* and marks before the next row's
         w = w_next;
+        here = part_of(next < A.rows ? next : 0);
     }
     // no block ends while another may still write to its shared memory
     if (ranks > 1)
@@ -618,7 +664,10 @@ row_kernel(const Args A, int ranks, int slots)
 }
 
 // Bytes of a row that a block should hold, and may hold.
-constexpr int64_t kPartBytes = 56 * 1024, kMostPartBytes = 196 * 1024;
+#ifndef PART_KB
+#define PART_KB 104
+#endif
+constexpr int64_t kPartBytes = PART_KB * 1024, kMostPartBytes = 192 * 1024;
 
 template <typename T, bool kGrad, int kExps>
 int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
@@ -629,7 +678,8 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
            ((pieces + ranks - 1) / ranks * 16 > kPartBytes || A.rows * ranks * 2 <= 152))
         ranks *= 2;
     const int64_t slots = (pieces + ranks - 1) / ranks;
-    const size_t smem = static_cast<size_t>(slots) * 16 + static_cast<size_t>(A.top) * 12;
+    const size_t smem = static_cast<size_t>(slots) * 16 + static_cast<size_t>(A.top) * 12 +
+                        (kGrad ? (slots * Piece<T>::kElems + 31) / 32 * 4 : 0);
     fits = slots * 16 <= kMostPartBytes;
     if (!fits) return ZERO_OK;
     auto* kernel = row_kernel<T, kGrad, kExps>;
