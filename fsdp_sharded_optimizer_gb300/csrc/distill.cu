@@ -28,6 +28,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -238,9 +239,8 @@ distill_kernel(const Args A)
 // for all rows and is the only one that reads or fills them, so it asks for
 // the next row's piece (cp.async) as soon as it has used this row's for the
 // last time, and no barrier stands between a row's loads and the one before.
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxRanks = 8;
+constexpr int kMaxRowWarps = 16;
 
 // How many exponentials a logit takes.
 //   kOne     one: temperature 1, or no labels
@@ -343,22 +343,24 @@ struct Part {
         to = static_cast<int>(whole < n ? whole : n);
     }
 };
+__device__ __forceinline__ void fetch16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 // Asks for slot j where it lies inside the row.
 template <typename T>
 __device__ __forceinline__ void fetch_whole(uint32_t part, const Part<T>& p, int j)
 {
     if (j >= p.from && j < p.to)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(part + 16u * j),
-                     "l"(p.row + p.lo + static_cast<int64_t>(j) * Piece<T>::kElems)
-                     : "memory");
+        fetch16(part + 16u * j, p.row + p.lo + static_cast<int64_t>(j) * Piece<T>::kElems);
 }
 // Fills the slots at the row's ends: at most one before `from`, one from `to`.
-template <typename T>
+template <int kThreadsOf, typename T>
 __device__ __forceinline__ void fetch_ends(uint4* part, const Part<T>& p, int64_t vocab)
 {
     constexpr int kE = Piece<T>::kElems;
     auto fill = [&](int j) {
-        if (j % kRowThreads != static_cast<int>(threadIdx.x)) return; // its owner
+        if (j % kThreadsOf != static_cast<int>(threadIdx.x)) return; // its owner
         part[j] = lowest_piece(T());
         T* e = reinterpret_cast<T*>(part + j);
         const int64_t at = p.lo + static_cast<int64_t>(j) * kE;
@@ -370,17 +372,41 @@ __device__ __forceinline__ void fetch_ends(uint4* part, const Part<T>& p, int64_
 }
 
 struct RowShared {
-    float most[2][kRowWarps];     // maxima of the block's warps: logits, teacher
-    float sum[4][kRowWarps];      // sums of the block's warps
+    float most[2][kMaxRowWarps];  // maxima of the block's warps: logits, teacher
+    float sum[4][kMaxRowWarps];   // sums of the block's warps
     float ranks[2][kMaxRanks][3]; // by row parity: every rank's maximum and sums
 };
 
-template <typename T, bool kGrad, int kExps>
-__global__ void __launch_bounds__(kRowThreads)
+// 2^(x c - m c) for a row's, or a thread's, maximum m.  The reference m c is
+// rounded once and the product inside the fma is not, so the terms agree to
+// rounding; what the reference was off by is taken out of the sum's logarithm.
+// c is 1 where m c might overflow: there only logits equal to m have a term
+// that is not 0, whatever c is.
+struct Scale {
+    float c, ref;
+    __device__ __forceinline__ Scale(float m, float factor)
+    {
+        c = fabsf(m) > 1e38f ? 1.0f : factor;
+        ref = m == -INFINITY ? 0.0f : m * c;
+    }
+    __device__ __forceinline__ float2 exp2(float2 x) const
+    {
+        return exp2_pair(dev::fma2(x, dev::pair(c), dev::pair(-ref)));
+    }
+    // log of the sum of e^(x - m) / T, given the sum of the terms
+    __device__ __forceinline__ float log_of(float sum, float m) const
+    {
+        return fmaf(fmaf(m, c, -ref), -kLn2, logf(sum));
+    }
+};
+
+template <typename T, bool kGrad, int kExps, int kThreadsOf>
+__global__ void __launch_bounds__(kThreadsOf, kThreadsOf == 256 ? 3 : 2)
 row_kernel(const Args A, int ranks, int slots)
 {
     constexpr int kE = Piece<T>::kElems, kP = Piece<T>::kPairs;
     constexpr int kBatch = 4; // pieces a thread has in registers at once
+    constexpr int kStep = kThreadsOf * kBatch, kRowWarps = kThreadsOf / 32;
     extern __shared__ uint4 part[]; // [slots]; top_p, top_s, top_id; marks
     __shared__ RowShared sh;
     float* top_p = reinterpret_cast<float*>(part + slots);
@@ -400,109 +426,161 @@ row_kernel(const Args A, int ranks, int slots)
     auto part_of = [&](int64_t row) {
         return Part<T>(static_cast<const T*>(A.logits) + row * A.stride, vocab, first_piece, slots);
     };
-    auto weight = [&](int64_t row) { return A.row_weight ? A.row_weight[row] : 1.0f; };
+    // What a row needs beside its logits is read a row ahead (the weight two, as
+    // it decides whether the next row is fetched); rows past the last weigh 0.
+    auto weight = [&](int64_t row) {
+        return row >= A.rows ? 0.0f : A.row_weight ? A.row_weight[row] : 1.0f;
+    };
+    auto label_of = [&](int64_t row) {
+        return A.labels && row < A.rows ? dev::load_index(A.labels, A.label_type, row) : int64_t(-1);
+    };
+    auto entry_of = [&](int64_t row, int k, int32_t& id, float& t) { // -1: not counted
+        id = -1;
+        t = -INFINITY;
+        if (k >= A.top || row >= A.rows) return;
+        const int64_t i = dev::load_index(A.ids, A.id_type, row * A.top + k);
+        float x[1];
+        dev::load_any<1>(A.teacher, A.teacher_type, row * A.top + k, x);
+        if (i >= 0 && i < vocab) {
+            id = static_cast<int32_t>(i);
+            t = x[0];
+        }
+    };
 
     if (kGrad)
-        for (int i = tid; i < (slots * kE + 31) / 32; i += kRowThreads) marks[i] = 0;
+        for (int i = tid; i < (slots * kE + 31) / 32; i += kThreadsOf) marks[i] = 0;
     if (ranks > 1) // every block has begun before another writes to its shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;\n"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
     else
         __syncthreads();
     int64_t row = blockIdx.x / ranks;
-    float w = row < A.rows ? weight(row) : 0.0f;
+    if (row >= A.rows) row = A.rows;
+    float w = weight(row), w_next = weight(row + clusters);
+    int64_t label = label_of(row);
+    int32_t my_id; // entry tid
+    float my_t;
+    entry_of(row, tid, my_id, my_t);
     Part<T> here = part_of(row < A.rows ? row : 0);
     if (w != 0.0f) {
-        for (int j = tid; j < here.to; j += kRowThreads) fetch_whole(part_at, here, j);
-        fetch_ends(part, here, vocab);
+        for (int j = tid; j < here.to; j += kThreadsOf) fetch_whole(part_at, here, j);
+        fetch_ends<kThreadsOf>(part, here, vocab);
     }
     int parity = 0;
-    for (; row < A.rows; row += clusters) {
+    while (row < A.rows) {
         const int64_t next = row + clusters;
-        const float w_next = next < A.rows ? weight(next) : 0.0f; // 0: nothing to fetch
-        Part<T> then = part_of(next < A.rows ? next : 0);
-        if (w_next == 0.0f) then.n = then.from = then.to = 0;
-        const T* s = here.row;
-        T* ds = kGrad ? static_cast<T*>(A.dlogits) + row * A.dstride : nullptr;
-        const int n = here.n;
-        const int64_t lo = here.lo, hi = lo + static_cast<int64_t>(n) * kE;
-        if (w == 0.0f) { // a masked row: not read
+        const int64_t this_row = row, this_label = label;
+        const float this_w = w;
+        const Part<T> now = here;
+        const int32_t this_id = my_id;
+        const float this_t = my_t;
+        here = part_of(next < A.rows ? next : 0);
+        Part<T> then = here;
+        if (w_next == 0.0f) then.n = then.from = then.to = 0; // nothing to fetch
+        w = w_next;
+        row = next;
+        const T* s = now.row;
+        T* ds = kGrad ? static_cast<T*>(A.dlogits) + this_row * A.dstride : nullptr;
+        const int n = now.n;
+        const int64_t lo = now.lo, hi = lo + static_cast<int64_t>(n) * kE;
+        // the student's logits at the label and at entry tid, then the next row's
+        const bool labelled = this_label >= 0 && this_label < vocab;
+        float s_label = 0.0f, my_s = 0.0f;
+        if (this_w != 0.0f) {
+            if (labelled) s_label = dev::load1(s + this_label);
+            if (this_id >= 0) my_s = dev::load1(s + this_id);
+        }
+        w_next = weight(next + clusters);
+        label = label_of(next);
+        entry_of(next, tid, my_id, my_t);
+        if (this_w == 0.0f) { // a masked row: not read
             if (rank == 0 && tid == 0) {
-                A.ce[row] = 0.0f;
-                A.kl[row] = 0.0f;
+                A.ce[this_row] = 0.0f;
+                A.kl[this_row] = 0.0f;
             }
             if (kGrad)
-                for (int64_t j = lo + tid; j < hi; j += kRowThreads)
+                for (int64_t j = lo + tid; j < hi; j += kThreadsOf)
                     if (j >= 0 && j < vocab) dev::store1(ds + j, 0.0f);
-            for (int j = tid; j < then.to; j += kRowThreads) fetch_whole(part_at, then, j);
-            fetch_ends(part, then, vocab);
-            w = w_next;
-            here = part_of(next < A.rows ? next : 0);
+            for (int j = tid; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
+            fetch_ends<kThreadsOf>(part, then, vocab);
             continue; // the whole cluster does
         }
-        // the teacher's entries; the student's logits there
-        float tm = -INFINITY;
-        bool twice = false; // an id of this part that an earlier entry has
-        for (int k = tid; k < A.top; k += kRowThreads) {
-            const int64_t id = dev::load_index(A.ids, A.id_type, row * A.top + k);
-            const bool counted = id >= 0 && id < vocab;
-            float t[1] = {-INFINITY};
-            if (counted) dev::load_any<1>(A.teacher, A.teacher_type, row * A.top + k, t);
-            tm = fmaxf(tm, t[0]);
-            top_id[k] = counted ? static_cast<int32_t>(id) : -1;
-            top_p[k] = t[0];
-            top_s[k] = counted ? dev::load1(s + id) : 0.0f;
-            if (kGrad && counted && id >= lo && id < hi) {
-                const uint32_t bit = 1u << (static_cast<uint32_t>(id - lo) & 31u);
-                twice |= (atomicOr(&marks[(id - lo) >> 5], bit) & bit) != 0;
-            }
-        }
-        const int64_t label = A.labels ? dev::load_index(A.labels, A.label_type, row) : -1;
-        const bool labelled = label >= 0 && label < vocab;
-        const float s_label = labelled ? dev::load1(s + label) : 0.0f;
 
         // pass 1: the maximum, and the sums relative to it
         asm volatile("cp.async.wait_all;" ::: "memory");
         float m = -INFINITY;
         float2 z1 = dev::pair(0.0f), z2 = z1;
-        int j0 = tid;
-        for (; j0 < n; j0 += kRowThreads * kBatch) {
-            uint4 raw[kBatch];
-            float mx = -INFINITY;
+        auto take = [&](const uint4& w, const Scale& k1, const Scale& k2) {
+            float2 x[kP];
+            unpack_piece(w, x, T());
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int j = j0 + u * kRowThreads;
-                raw[u] = j < n ? part[j] : lowest_piece(T());
-                mx = fmaxf(mx, piece_max(raw[u], T()));
+            for (int e = 0; e < kP; ++e) {
+                const float2 e2 = k2.exp2(x[e]);
+                z2 = dev::add2(z2, e2);
+                if (kExps == kSquare) z1 = dev::fma2(e2, e2, z1);
+                if (kExps == kTwo) z1 = dev::add2(z1, k1.exp2(x[e]));
             }
+        };
+        auto raise = [&](float mx) { // a larger maximum: the sums so far shrink
             if (mx > m) {
-                const float f2 = exp2_approx((m - mx) * c2);
+                const float from2 = Scale(m, c2).ref, to2 = Scale(mx, c2).ref;
+                const float f2 = m == -INFINITY ? 0.0f : exp2_approx(from2 - to2);
                 z2 = dev::mul2(z2, dev::pair(f2));
                 if (kExps == kSquare) z1 = dev::mul2(z1, dev::pair(f2 * f2));
-                if (kExps == kTwo)
-                    z1 = dev::mul2(z1, dev::pair(exp2_approx((m - mx) * kLog2e)));
+                if (kExps == kTwo) {
+                    const float from1 = Scale(m, kLog2e).ref, to1 = Scale(mx, kLog2e).ref;
+                    z1 = dev::mul2(z1, dev::pair(m == -INFINITY ? 0.0f : exp2_approx(from1 - to1)));
+                }
                 m = mx;
             }
-            const float2 base = dev::pair(m == -INFINITY ? 0.0f : -m);
+        };
+        int j = tid;
+        for (; j + kStep - kThreadsOf < n; j += kStep) {
+            uint4 raw[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                float2 x[kP];
-                unpack_piece(raw[u], x, T());
+            for (int u = 0; u < kBatch; ++u) raw[u] = part[j + u * kThreadsOf];
+            float mx = piece_max(raw[0], T());
 #pragma unroll
-                for (int e = 0; e < kP; ++e) {
-                    const float2 d = dev::add2(x[e], base);
-                    const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
-                    z2 = dev::add2(z2, e2);
-                    if (kExps == kSquare) z1 = dev::fma2(e2, e2, z1);
-                    if (kExps == kTwo)
-                        z1 = dev::add2(z1, exp2_pair(dev::mul2(d, dev::pair(kLog2e))));
-                }
-                if (!kGrad) fetch_whole(part_at, then, j0 + u * kRowThreads);
+            for (int u = 1; u < kBatch; ++u) mx = fmaxf(mx, piece_max(raw[u], T()));
+            raise(mx);
+            const Scale k1(m, kLog2e), k2(m, c2);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) take(raw[u], k1, k2);
+            if (!kGrad) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) fetch_whole(part_at, then, j + u * kThreadsOf);
             }
         }
+        for (; j < n; j += kThreadsOf) {
+            const uint4 raw = part[j];
+            raise(piece_max(raw, T()));
+            const Scale k1(m, kLog2e), k2(m, c2);
+            take(raw, k1, k2);
+            if (!kGrad) fetch_whole(part_at, then, j);
+        }
         if (!kGrad) { // slots that the next row has beyond this one's
-            for (; j0 < then.to; j0 += kRowThreads) fetch_whole(part_at, then, j0);
-            fetch_ends(part, then, vocab);
+            for (; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
+            fetch_ends<kThreadsOf>(part, then, vocab);
+        }
+
+        // the teacher's entries; the student's logits there
+        float tm = -INFINITY;
+        bool twice = false; // an id of this part that an earlier entry has
+        for (int k = tid; k < A.top; k += kThreadsOf) {
+            int32_t id = this_id;
+            float t = this_t, at = my_s;
+            if (k != tid) {
+                entry_of(this_row, k, id, t);
+                at = id >= 0 ? dev::load1(s + id) : 0.0f;
+            }
+            tm = fmaxf(tm, t);
+            top_id[k] = id;
+            top_p[k] = t;
+            top_s[k] = at;
+            if (kGrad && id >= 0 && id >= lo && id < hi) {
+                const uint32_t place = static_cast<uint32_t>(id - lo), bit = 1u << (place & 31u);
+                twice |= (atomicOr(&marks[place >> 5], bit) & bit) != 0;
+            }
         }
 
         // the block's maxima
@@ -515,32 +593,38 @@ row_kernel(const Args A, int ranks, int slots)
         twice = __syncthreads_or(twice);
         block_m = warp_max(sh.most[0][lane % kRowWarps]);
         tm = warp_max(sh.most[1][lane % kRowWarps]);
+        const Scale b1(block_m, kLog2e), b2(block_m, c2);
         const float base = block_m == -INFINITY ? 0.0f : block_m;
         const float tbase = tm == -INFINITY ? 0.0f : tm;
         // its sums
         float v[4] = {z1.x + z1.y, z2.x + z2.y, 0.0f, 0.0f};
         if (m > -INFINITY) {
-            const float f2 = exp2_approx((m - base) * c2);
+            const float f2 = exp2_approx(Scale(m, c2).ref - b2.ref);
             v[1] *= f2;
-            v[0] *= kExps == kSquare ? f2 * f2 : kExps == kTwo ? exp2_approx((m - base) * kLog2e) : 0.0f;
+            v[0] *= kExps == kSquare ? f2 * f2
+                    : kExps == kTwo  ? exp2_approx(Scale(m, kLog2e).ref - b1.ref)
+                                     : 0.0f;
         }
-        for (int k = tid; k < A.top; k += kRowThreads) {
+        for (int k = tid; k < A.top; k += kThreadsOf) {
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
             v[2] += e;
             if (e != 0.0f)
                 v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - base)) * inv_tau, v[3]);
             top_p[k] = e;
         }
+        const bool marked = kGrad && labelled && this_label >= lo && this_label < hi &&
+                            (marks[(this_label - lo) >> 5] >> ((this_label - lo) & 31) & 1);
         const float sum = warp_sum4(v, lane);
         if (lane % 8 == 0) sh.sum[lane / 8][warp] = sum;
         __syncthreads();
         float all = sh.sum[lane / 8][lane % 8];
-        static_assert(kRowWarps == 8, "a lane for each warp and value");
+        if (kRowWarps == 16) all += sh.sum[lane / 8][lane % 8 + 8];
+        static_assert(kRowWarps == 8 || kRowWarps == 16, "8 lanes for a value");
 #pragma unroll
         for (int off = 4; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, all, 8 * i);
-        float row_m = base, zs1 = v[0], zs2 = v[1], cross = v[3];
+        float row_m = block_m, zs1 = v[0], zs2 = v[1], cross = v[3];
         const float zt = v[2];
         if (ranks > 1) { // the cluster's
             if (tid < ranks) {
@@ -554,108 +638,140 @@ row_kernel(const Args A, int ranks, int slots)
             }
             asm volatile("barrier.cluster.arrive.release.aligned;\n"
                          "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            float most = -INFINITY;
-            for (int r = 0; r < ranks; ++r) most = fmaxf(most, sh.ranks[parity][r][0]);
-            row_m = most == -INFINITY ? 0.0f : most;
+            for (int r = 0; r < ranks; ++r) row_m = fmaxf(row_m, sh.ranks[parity][r][0]);
+            const Scale to1(row_m, kLog2e), to2(row_m, c2);
             zs1 = zs2 = 0.0f;
             for (int r = 0; r < ranks; ++r) {
                 const float rm = sh.ranks[parity][r][0];
                 // a part without anything above -inf holds 0, or NaN
-                const float f2 = rm == -INFINITY ? 1.0f : exp2_approx((rm - row_m) * c2);
+                const float f2 = rm == -INFINITY ? 1.0f : exp2_approx(Scale(rm, c2).ref - to2.ref);
                 const float f1 = kExps == kSquare ? f2 * f2
                                  : kExps == kTwo && rm != -INFINITY
-                                     ? exp2_approx((rm - row_m) * kLog2e)
+                                     ? exp2_approx(Scale(rm, kLog2e).ref - to1.ref)
                                      : 1.0f;
                 zs1 = fmaf(sh.ranks[parity][r][1], f1, zs1);
                 zs2 = fmaf(sh.ranks[parity][r][2], f2, zs2);
             }
-            cross = fmaf(zt, (row_m - base) * inv_tau, cross);
+            if (row_m > -INFINITY) cross = fmaf(zt, (row_m - base) * inv_tau, cross);
             parity ^= 1;
         }
         if (kExps == kOne) zs1 = zs2;
+        const Scale r1(row_m, kLog2e), r2(row_m, c2);
         // a row whose logits are all -inf has no distribution, a teacher whose
         // counted entries are all -inf (or none) has none either; a NaN is neither
         const bool empty = zs2 == 0.0f;
         const bool has_top = zt != 0.0f && !empty;
         const bool has_label = labelled && !empty;
         if (rank == 0 && tid == 0) {
-            A.ce[row] = has_label ? logf(zs1) - (s_label - row_m) : 0.0f;
-            A.kl[row] = has_top ? A.tau * A.tau * (cross / zt + (logf(zs2) - logf(zt))) : 0.0f;
+            const float from = row_m == -INFINITY ? 0.0f : row_m;
+            const float log1 = kExps == kOne      ? r2.log_of(zs1, from)
+                               : kExps == kSquare ? fmaf(fmaf(from, r2.c, -r2.ref), -2.0f * kLn2, logf(zs1))
+                                                  : r1.log_of(zs1, from);
+            A.ce[this_row] = has_label ? log1 - (s_label - from) : 0.0f;
+            A.kl[this_row] = has_top ? A.tau * A.tau * (cross / zt + (r2.log_of(zs2, from) - logf(zt)))
+                                     : 0.0f;
         }
         if constexpr (kGrad) {
-            const float hit = has_label ? w * A.ce_weight : 0.0f;
-            const float pull = has_top ? w * A.kl_weight * A.tau : 0.0f;
+            for (int k = tid; k < A.top; k += kThreadsOf) { // the marks are read: clear them
+                const int32_t id = top_id[k];
+                if (id >= lo && id < hi && id >= 0) marks[(id - lo) >> 5] = 0;
+            }
+            const float hit = has_label ? this_w * A.ce_weight : 0.0f;
+            const float pull = has_top ? this_w * A.kl_weight * A.tau : 0.0f;
             const float share = has_top ? __fdividef(pull, zt) : 0.0f;
             float a1 = has_label ? __fdividef(hit, zs1) : 0.0f;
             float a2 = has_top ? __fdividef(pull, zs2) : 0.0f;
             if (kExps == kOne) a2 += a1;
             const bool has_any = has_top || has_label; // else +0, whatever the logits are
             auto dense = [&](float2 x) {
-                const float2 d = dev::add2(x, dev::pair(-row_m));
-                const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
-                float2 g = dev::mul2(e2, dev::pair(a2));
-                if (kExps == kSquare) g = dev::fma2(dev::mul2(e2, e2), dev::pair(a1), g);
-                if (kExps == kTwo)
-                    g = dev::fma2(exp2_pair(dev::mul2(d, dev::pair(kLog2e))), dev::pair(a1), g);
-                return g;
+                const float2 e2 = r2.exp2(x);
+                if (kExps == kSquare) // (a1 e2 + a2) e2
+                    return dev::mul2(dev::fma2(dev::pair(a1), e2, dev::pair(a2)), e2);
+                const float2 g = dev::mul2(e2, dev::pair(a2));
+                return kExps == kTwo ? dev::fma2(r1.exp2(x), dev::pair(a1), g) : g;
             };
             const bool alike = ((reinterpret_cast<uintptr_t>(ds) ^ reinterpret_cast<uintptr_t>(s)) & 15) == 0;
             // slots that are written 16 bytes at once
-            const int wide_from = alike ? here.from : n, wide_to = alike ? here.to : n;
+            const int wide_from = alike ? now.from : n, wide_to = alike ? now.to : n;
             T* out = ds + lo;
-            int j = tid;
-#pragma unroll 4
-            for (; j < n; j += kRowThreads) {
-                const uint4 raw = part[j];
-                float2 x[kP];
-                unpack_piece(raw, x, T());
-#pragma unroll
-                for (int e = 0; e < kP; ++e) x[e] = has_any ? dense(x[e]) : dev::pair(0.0f);
+            auto write = [&](int j, const float2 (&x)[kP]) {
                 if (j >= wide_from && j < wide_to) {
                     __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * kE),
                            pack_piece(x, T()));
-                } else {
-                    const int64_t at = lo + static_cast<int64_t>(j) * kE;
-#pragma unroll
-                    for (int e = 0; e < kE; ++e)
-                        if (at + e >= 0 && at + e < vocab)
-                            dev::store1(ds + at + e, e & 1 ? x[e / 2].y : x[e / 2].x);
+                    return;
                 }
+                const int64_t at = lo + static_cast<int64_t>(j) * kE;
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if (at + e >= 0 && at + e < vocab)
+                        dev::store1(ds + at + e, e & 1 ? x[e / 2].y : x[e / 2].x);
+            };
+            int j = tid;
+            if (!has_any) {
+                const float2 zero[kP] = {};
+                for (; j < n; j += kThreadsOf) {
+                    write(j, zero);
+                    fetch_whole(part_at, then, j);
+                }
+            }
+            // whole batches: nothing of them at the ends, of this row or the next
+            const int first = now.from > then.from ? now.from : then.from;
+            int batches = wide_to < then.to || then.to == 0 ? wide_to : then.to;
+            if (!alike) batches = 0;
+            for (; j + kStep - kThreadsOf < batches; j += kStep) {
+                uint4 raw[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) raw[u] = part[j + u * kThreadsOf];
+                T* to = out + static_cast<int64_t>(j) * kE;
+                const T* from = then.row + then.lo + static_cast<int64_t>(j) * kE;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    float2 x[kP];
+                    unpack_piece(raw[u], x, T());
+#pragma unroll
+                    for (int e = 0; e < kP; ++e) x[e] = dense(x[e]);
+                    if (u == 0 && j < first) {
+                        write(j, x);
+                        fetch_whole(part_at, then, j);
+                    } else {
+                        __stcs(reinterpret_cast<uint4*>(to + u * kThreadsOf * kE), pack_piece(x, T()));
+                        if (then.to) fetch16(part_at + 16u * (j + u * kThreadsOf), from + u * kThreadsOf * kE);
+                    }
+                }
+            }
+            for (; j < n; j += kThreadsOf) {
+                float2 x[kP];
+                unpack_piece(part[j], x, T());
+#pragma unroll
+                for (int e = 0; e < kP; ++e) x[e] = dense(x[e]);
+                write(j, x);
                 fetch_whole(part_at, then, j);
             }
-            for (; j < then.to; j += kRowThreads) fetch_whole(part_at, then, j);
-            fetch_ends(part, then, vocab);
+            for (; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
+            fetch_ends<kThreadsOf>(part, then, vocab);
             __syncthreads(); // before the teacher's entries are written over
-            if (labelled && label >= lo && label < hi && has_label && tid == 0 &&
-                !(marks[(label - lo) >> 5] >> ((label - lo) & 31) & 1))
-                dev::store1(ds + label, dense(dev::pair(s_label)).x - hit);
-            for (int k = tid; k < A.top; k += kRowThreads) {
+            if (has_label && !marked && tid == 0 && this_label >= lo && this_label < hi)
+                dev::store1(ds + this_label, dense(dev::pair(s_label)).x - hit);
+            for (int k = tid; k < A.top; k += kThreadsOf) {
                 const int32_t id = top_id[k];
                 if (id < lo || id >= hi || id < 0) continue; // not counted, or another rank's
                 float p = top_p[k];
                 if (twice) { // the first entry of an id writes for all of them
-                    bool first = true;
+                    bool first_of = true;
                     p = 0.0f;
                     for (int q = 0; q < A.top; ++q) {
                         if (top_id[q] != id) continue;
-                        if (q < k) first = false;
+                        if (q < k) first_of = false;
                         p += top_p[q];
                     }
-                    if (!first) continue;
+                    if (!first_of) continue;
                 }
                 float g = has_any ? fmaf(-share, p, dense(dev::pair(top_s[k])).x) : 0.0f;
-                if (id == label) g -= hit;
+                if (id == this_label) g -= hit;
                 dev::store1(ds + id, g);
             }
-            __syncthreads(); // the label's look at the marks
-            for (int k = tid; k < A.top; k += kRowThreads) {
-                const int32_t id = top_id[k];
-                if (id >= lo && id < hi && id >= 0) marks[(id - lo) >> 5] = 0;
-            }
+            if (twice) __syncthreads(); // others' entries were read
         }
-        __syncthreads(); // this row's use of top_* and marks before the next row's
-        w = w_next;
-        here = part_of(next < A.rows ? next : 0);
     }
     // no block ends while another may still write to its shared memory
     if (ranks > 1)
@@ -669,33 +785,28 @@ row_kernel(const Args A, int ranks, int slots)
 #endif
 constexpr int64_t kPartBytes = PART_KB * 1024, kMostPartBytes = 192 * 1024;
 
-template <typename T, bool kGrad, int kExps>
-int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
+#ifndef WIDE_KB
+#define WIDE_KB 1000
+#endif
+template <typename T, bool kGrad, int kExps, int kThreadsOf>
+int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
 {
-    const int64_t pieces = (A.vocab + 2 * (Piece<T>::kElems - 1)) / Piece<T>::kElems + 1;
-    int ranks = 1;
-    while (ranks < kMaxRanks &&
-           ((pieces + ranks - 1) / ranks * 16 > kPartBytes || A.rows * ranks * 2 <= 152))
-        ranks *= 2;
-    const int64_t slots = (pieces + ranks - 1) / ranks;
     const size_t smem = static_cast<size_t>(slots) * 16 + static_cast<size_t>(A.top) * 12 +
                         (kGrad ? (slots * Piece<T>::kElems + 31) / 32 * 4 : 0);
-    fits = slots * 16 <= kMostPartBytes;
-    if (!fits) return ZERO_OK;
-    auto* kernel = row_kernel<T, kGrad, kExps>;
+    auto* kernel = row_kernel<T, kGrad, kExps, kThreadsOf>;
     const void* k = reinterpret_cast<const void*>(kernel);
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
         return ZERO_ECUDA;
-    const int resident = persistent_blocks(k, kRowThreads, smem);
+    const int resident = persistent_blocks(k, kThreadsOf, smem);
     if (resident < 1) return ZERO_ECUDA;
     int64_t clusters = resident / ranks;
     if (clusters < 1) clusters = 1;
     if (clusters > A.rows) clusters = A.rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(kThreadsOf);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -705,6 +816,21 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A, ranks, static_cast<int>(slots)));
+}
+
+template <typename T, bool kGrad, int kExps>
+int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
+{
+    const int64_t pieces = (A.vocab + 2 * (Piece<T>::kElems - 1)) / Piece<T>::kElems + 1;
+    int ranks = 1;
+    while (ranks < kMaxRanks &&
+           ((pieces + ranks - 1) / ranks * 16 > kPartBytes || A.rows * ranks * 2 <= 152))
+        ranks *= 2;
+    const int64_t slots = (pieces + ranks - 1) / ranks;
+    fits = slots * 16 <= kMostPartBytes;
+    if (!fits) return ZERO_OK;
+    return slots * 16 > WIDE_KB * 1024 ? launch_rows<T, kGrad, kExps, 512>(A, ranks, slots, stream)
+                                       : launch_rows<T, kGrad, kExps, 256>(A, ranks, slots, stream);
 }
 
 template <typename T, bool kGrad>
