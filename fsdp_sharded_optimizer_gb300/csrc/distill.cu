@@ -426,6 +426,30 @@ row_kernel(const Args A, int ranks, int slots)
     auto part_of = [&](int64_t row) {
         return Part<T>(static_cast<const T*>(A.logits) + row * A.stride, vocab, first_piece, slots);
     };
+    // A row's fetches are two groups: slots below half, which a row's first pass
+    // waits for at its start, and the others (some below may wait with them).
+    const int half = slots / 2;
+    bool split = false;
+    auto close_group = [&] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    auto at_slot = [&](int j) {
+        if (!split && j >= half) {
+            close_group();
+            split = true;
+        }
+    };
+    auto close_row = [&] {
+        if (!split) close_group();
+        close_group();
+        split = false;
+    };
+    auto fetch_from = [&](const Part<T>& p, int j) { // and the row's ends
+        for (; j < p.to; j += kThreadsOf) {
+            at_slot(j);
+            fetch_whole(part_at, p, j);
+        }
+        fetch_ends<kThreadsOf>(part, p, vocab);
+        close_row();
+    };
     // What a row needs beside its logits is read a row ahead (the weight two, as
     // it decides whether the next row is fetched); rows past the last weigh 0.
     auto weight = [&](int64_t row) {
@@ -449,11 +473,14 @@ row_kernel(const Args A, int ranks, int slots)
 
     if (kGrad)
         for (int i = tid; i < (slots * kE + 31) / 32; i += kThreadsOf) marks[i] = 0;
+    if (tid < kMaxRowWarps) { // places without a warp
+        sh.most[0][tid] = sh.most[1][tid] = -INFINITY;
+        for (int i = 0; i < 4; ++i) sh.sum[i][tid] = 0.0f;
+    }
+    __syncthreads();
     if (ranks > 1) // every block has begun before another writes to its shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;\n"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else
-        __syncthreads();
     int64_t row = blockIdx.x / ranks;
     if (row >= A.rows) row = A.rows;
     float w = weight(row), w_next = weight(row + clusters);
@@ -462,10 +489,9 @@ row_kernel(const Args A, int ranks, int slots)
     float my_t;
     entry_of(row, tid, my_id, my_t);
     Part<T> here = part_of(row < A.rows ? row : 0);
-    if (w != 0.0f) {
-        for (int j = tid; j < here.to; j += kThreadsOf) fetch_whole(part_at, here, j);
-        fetch_ends<kThreadsOf>(part, here, vocab);
-    }
+    if (w == 0.0f) here.n = here.from = here.to = 0;
+    fetch_from(here, tid);
+    here = part_of(row < A.rows ? row : 0);
     int parity = 0;
     while (row < A.rows) {
         const int64_t next = row + clusters;
@@ -501,13 +527,11 @@ row_kernel(const Args A, int ranks, int slots)
             if (kGrad)
                 for (int64_t j = lo + tid; j < hi; j += kThreadsOf)
                     if (j >= 0 && j < vocab) dev::store1(ds + j, 0.0f);
-            for (int j = tid; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
-            fetch_ends<kThreadsOf>(part, then, vocab);
+            fetch_from(then, tid);
             continue; // the whole cluster does
         }
 
         // pass 1: the maximum, and the sums relative to it
-        asm volatile("cp.async.wait_all;" ::: "memory");
         float m = -INFINITY;
         float2 z1 = dev::pair(0.0f), z2 = z1;
         auto take = [&](const uint4& w, const Scale& k1, const Scale& k2) {
@@ -535,7 +559,14 @@ row_kernel(const Args A, int ranks, int slots)
             }
         };
         int j = tid;
+        // the fetches of the first half have been under way for longer
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        bool rest = false; // whether the others have been waited for
         for (; j + kStep - kThreadsOf < n; j += kStep) {
+            if (!rest && j + kStep - kThreadsOf >= half) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                rest = true;
+            }
             uint4 raw[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) raw[u] = part[j + u * kThreadsOf];
@@ -547,21 +578,23 @@ row_kernel(const Args A, int ranks, int slots)
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) take(raw[u], k1, k2);
             if (!kGrad) {
+                at_slot(j);
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) fetch_whole(part_at, then, j + u * kThreadsOf);
             }
         }
+        if (!rest) asm volatile("cp.async.wait_group 0;" ::: "memory");
         for (; j < n; j += kThreadsOf) {
             const uint4 raw = part[j];
             raise(piece_max(raw, T()));
             const Scale k1(m, kLog2e), k2(m, c2);
             take(raw, k1, k2);
-            if (!kGrad) fetch_whole(part_at, then, j);
+            if (!kGrad) {
+                at_slot(j);
+                fetch_whole(part_at, then, j);
+            }
         }
-        if (!kGrad) { // slots that the next row has beyond this one's
-            for (; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
-            fetch_ends<kThreadsOf>(part, then, vocab);
-        }
+        if (!kGrad) fetch_from(then, j); // slots that the next row has beyond this one's
 
         // the teacher's entries; the student's logits there
         float tm = -INFINITY;
@@ -591,8 +624,8 @@ row_kernel(const Args A, int ranks, int slots)
             sh.most[1][warp] = tm;
         }
         twice = __syncthreads_or(twice);
-        block_m = warp_max(sh.most[0][lane % kRowWarps]);
-        tm = warp_max(sh.most[1][lane % kRowWarps]);
+        block_m = warp_max(sh.most[0][lane % kMaxRowWarps]);
+        tm = warp_max(sh.most[1][lane % kMaxRowWarps]);
         const Scale b1(block_m, kLog2e), b2(block_m, c2);
         const float base = block_m == -INFINITY ? 0.0f : block_m;
         const float tbase = tm == -INFINITY ? 0.0f : tm;
@@ -618,8 +651,7 @@ row_kernel(const Args A, int ranks, int slots)
         if (lane % 8 == 0) sh.sum[lane / 8][warp] = sum;
         __syncthreads();
         float all = sh.sum[lane / 8][lane % 8];
-        if (kRowWarps == 16) all += sh.sum[lane / 8][lane % 8 + 8];
-        static_assert(kRowWarps == 8 || kRowWarps == 16, "8 lanes for a value");
+        if (kRowWarps > 8) all += sh.sum[lane / 8][lane % 8 + 8];
 #pragma unroll
         for (int off = 4; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
 #pragma unroll
@@ -711,6 +743,7 @@ row_kernel(const Args A, int ranks, int slots)
                 const float2 zero[kP] = {};
                 for (; j < n; j += kThreadsOf) {
                     write(j, zero);
+                    at_slot(j);
                     fetch_whole(part_at, then, j);
                 }
             }
@@ -719,6 +752,7 @@ row_kernel(const Args A, int ranks, int slots)
             int batches = wide_to < then.to || then.to == 0 ? wide_to : then.to;
             if (!alike) batches = 0;
             for (; j + kStep - kThreadsOf < batches; j += kStep) {
+                at_slot(j);
                 uint4 raw[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) raw[u] = part[j + u * kThreadsOf];
@@ -745,10 +779,10 @@ row_kernel(const Args A, int ranks, int slots)
 #pragma unroll
                 for (int e = 0; e < kP; ++e) x[e] = dense(x[e]);
                 write(j, x);
+                at_slot(j);
                 fetch_whole(part_at, then, j);
             }
-            for (; j < then.to; j += kThreadsOf) fetch_whole(part_at, then, j);
-            fetch_ends<kThreadsOf>(part, then, vocab);
+            fetch_from(then, j);
             __syncthreads(); // before the teacher's entries are written over
             if (has_label && !marked && tid == 0 && this_label >= lo && this_label < hi)
                 dev::store1(ds + this_label, dense(dev::pair(s_label)).x - hit);
@@ -786,7 +820,10 @@ row_kernel(const Args A, int ranks, int slots)
 constexpr int64_t kPartBytes = PART_KB * 1024, kMostPartBytes = 192 * 1024;
 
 #ifndef WIDE_KB
-#define WIDE_KB 1000
+#define WIDE_KB 72
+#endif
+#ifndef WIDE_T
+#define WIDE_T 384
 #endif
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
@@ -829,7 +866,7 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
     const int64_t slots = (pieces + ranks - 1) / ranks;
     fits = slots * 16 <= kMostPartBytes;
     if (!fits) return ZERO_OK;
-    return slots * 16 > WIDE_KB * 1024 ? launch_rows<T, kGrad, kExps, 512>(A, ranks, slots, stream)
+    return slots * 16 > WIDE_KB * 1024 ? launch_rows<T, kGrad, kExps, WIDE_T>(A, ranks, slots, stream)
                                        : launch_rows<T, kGrad, kExps, 256>(A, ranks, slots, stream);
 }
 
