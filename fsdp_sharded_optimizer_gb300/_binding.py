@@ -745,39 +745,36 @@ def zero_cast_bf16(src, dst, stream=None):
 
 
 # ------------------------------------------------- operators of the model
-def _shape(what, t, *shape):
-    if tuple(t.shape) != shape:
-        raise ValueError("%s: expected shape %s, got %s" % (what, shape, tuple(t.shape)))
+# These calls are short (a few microseconds on the GPU for a few tokens), so
+# each tensor is looked at once and attributes are not read twice.
+_FLOATS = {torch.bfloat16: ZERO_TYPE_BF16, torch.int16: ZERO_TYPE_BF16,
+           torch.uint16: ZERO_TYPE_BF16, torch.float32: ZERO_TYPE_F32}
+_INDEXES = {torch.int32: ZERO_TYPE_I32, torch.int64: ZERO_TYPE_I64}
+_KINDS = {"rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
 
 
-def _float_type(t, what):
-    """ZERO_TYPE_BF16 (bfloat16, or its bits as int16/uint16) or ZERO_TYPE_F32."""
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
-        return ZERO_TYPE_BF16
-    if t.dtype == torch.float32:
-        return ZERO_TYPE_F32
-    raise ValueError("%s must be bf16 or fp32, got %s" % (what, t.dtype))
+def _type(t, what, types=_FLOATS):
+    """ZERO_TYPE_* of a tensor (bf16 may be given as its bits, int16 or uint16)."""
+    try:
+        return types[t.dtype]
+    except KeyError:
+        raise ValueError("%s must be %s, got %s" % (
+            what, "bf16 or fp32" if types is _FLOATS else "int32 or int64", t.dtype)) from None
 
 
-def _index_type(t, what):
-    if t.dtype == torch.int32:
-        return ZERO_TYPE_I32
-    if t.dtype == torch.int64:
-        return ZERO_TYPE_I64
-    raise ValueError("%s must be int32 or int64, got %s" % (what, t.dtype))
-
-
-def _ptr(t, what):
-    """The address of a contiguous device-addressable tensor, None for None."""
-    if t is None:
-        return None
-    if not _addressable(t) or not t.is_contiguous():
+def _at(t, what, shape=None):
+    """The address of a contiguous device-addressable tensor of a shape."""
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous() or not _addressable(t):
         raise ValueError("%s must be a contiguous CUDA or pinned host tensor" % what)
     return t.data_ptr()
 
 
-def _scratch(t):
-    return _ptr(t, "scratch"), t.numel() * t.element_size()
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def zero_embed_forward(table, ids, out, scale=1.0, stream=None):
@@ -786,11 +783,10 @@ def zero_embed_forward(table, ids, out, scale=1.0, stream=None):
     if table.dim() != 2:
         raise ValueError("table must have two dimensions")
     V, D = table.shape
-    _shape("out", out, *ids.shape, D)
     _check("zero_embed_forward", lib.zero_embed_forward(
-        _ptr(table, "table"), _float_type(table, "table"), V, D, _ptr(ids, "ids"),
-        _index_type(ids, "ids"), ids.numel(), float(scale), _ptr(out, "out"),
-        _float_type(out, "out"), _stream(stream)))
+        _at(table, "table"), _type(table, "table"), V, D, _at(ids, "ids"),
+        _type(ids, "ids", _INDEXES), ids.numel(), scale, _at(out, "out", (*ids.shape, D)),
+        _type(out, "out"), _raw_stream(stream)))
 
 
 def _bytes(fn, n):
@@ -811,43 +807,38 @@ def zero_embed_backward(dout, ids, dtable, scratch, scale=1.0, accumulate=False,
     if dtable.dim() != 2:
         raise ValueError("dtable must have two dimensions")
     V, D = dtable.shape
-    _shape("dout", dout, *ids.shape, D)
     _check("zero_embed_backward", lib.zero_embed_backward(
-        _ptr(dout, "dout"), _float_type(dout, "dout"), _ptr(ids, "ids"), _index_type(ids, "ids"),
-        ids.numel(), float(scale), _ptr(dtable, "dtable"), _float_type(dtable, "dtable"), V, D,
-        1 if accumulate else 0, *_scratch(scratch), _stream(stream)))
+        _at(dout, "dout", (*ids.shape, D)), _type(dout, "dout"), _at(ids, "ids"),
+        _type(ids, "ids", _INDEXES), ids.numel(), scale, _at(dtable, "dtable"),
+        _type(dtable, "dtable"), V, D, 1 if accumulate else 0, _at(scratch, "scratch"),
+        scratch.nbytes, _raw_stream(stream)))
 
 
-def _norm_spec(stream_rows, act, gate, params, kind, rows_per_gate, post_norm, pre_norm, eps,
-               residual_scale, branch_scale):
-    """The zero_block_norm_t of a call, with its tensors' shapes and types checked."""
-    if stream_rows.dim() != 2:
+class _Alike:
+    """Addresses of tensors that share a shape and one of the float types; None
+    for None."""
+
+    def __init__(self, shape, what, type=None):
+        self.shape, self.what, self.type = shape, what, type
+
+    def __call__(self, t, name):
+        if t is None:
+            return None
+        at, type = _at(t, name, self.shape), _type(t, name)
+        if self.type is None:
+            self.type = type
+        elif self.type != type:
+            raise ValueError("%s must have one type: %s" % (self.what, name))
+        return at
+
+
+def _norm_call(rows, kind, rows_per_gate):
+    """Shape, gate span and kind of a call on the residual stream `rows`."""
+    if rows.dim() != 2:
         raise ValueError("the residual stream must have two dimensions")
-    R, D = stream_rows.shape
-    res = _float_type(stream_rows, "the residual stream")
-    for name, t in act.items():
-        if t is not None:
-            _shape(name, t, R, D)
-    types = {_float_type(t, name) for name, t in act.items() if t is not None}
-    if len(types) > 1:
-        raise ValueError("activations must have one type")
-    span = int(rows_per_gate) if rows_per_gate else max(1, R)
-    if gate is not None:
-        _shape("gate", gate, max(1, -(-R // span)), D)
-    for name, t in params.items():
-        if t is not None:
-            _shape(name, t, D)
-    ptypes = {_float_type(t, name) for name, t in params.items() if t is not None}
-    if len(ptypes) > 1:
-        raise ValueError("norm weights and biases must have one type")
-    kinds = {"rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
-    if kind not in kinds:
+    if kind not in _KINDS:
         raise ValueError("kind must be 'rms' or 'layer'")
-    return zero_block_norm_t(R, D, span, kinds[kind], int(bool(post_norm)), int(bool(pre_norm)),
-                             types.pop() if types else res, res,
-                             ptypes.pop() if ptypes else ZERO_TYPE_BF16,
-                             _float_type(gate, "gate") if gate is not None else ZERO_TYPE_BF16,
-                             float(eps), float(residual_scale), float(branch_scale))
+    return rows.shape, int(rows_per_gate) if rows_per_gate else max(1, rows.shape[0]), _KINDS[kind]
 
 
 def zero_block_norm_forward(x, branch=None, gate=None, post_weight=None, post_bias=None,
@@ -861,21 +852,20 @@ def zero_block_norm_forward(x, branch=None, gate=None, post_weight=None, post_bi
     one gate row by default), weights and biases (D).  post_norm / pre_norm False
     leaves out the branch's norm / the norm of y (u is then None).  Without a
     branch (before the first block) u = norm(x), and y is None."""
-    if branch is None:
-        post_norm = False
-    if y is not None:
-        _shape("y", y, *x.shape)
-        if _float_type(y, "y") != _float_type(x, "x"):
-            raise ValueError("x and y must have one type")
-    spec = _norm_spec(x, {"branch": branch, "u": u}, gate,
-                      {"post_weight": post_weight, "post_bias": post_bias,
-                       "pre_weight": pre_weight, "pre_bias": pre_bias}, kind, rows_per_gate,
-                      post_norm, pre_norm, eps, residual_scale, branch_scale)
-    _check("zero_block_norm_forward", lib.zero_block_norm_forward(
-        C.byref(spec), _ptr(x, "x"), _ptr(branch, "branch"), _ptr(gate, "gate"),
-        _ptr(post_weight, "post_weight"), _ptr(post_bias, "post_bias"),
-        _ptr(pre_weight, "pre_weight"), _ptr(pre_bias, "pre_bias"), _ptr(y, "y"), _ptr(u, "u"),
-        _stream(stream)))
+    shape, span, kind = _norm_call(x, kind, rows_per_gate)
+    R, D = shape
+    res, act = _Alike(shape, "x and y"), _Alike(shape, "branch and u")
+    par = _Alike((D,), "weights and biases")
+    gates = _Alike((max(1, -(-R // span)), D), "gate")
+    args = (res(x, "x"), act(branch, "branch"), gates(gate, "gate"),
+            par(post_weight, "post_weight"), par(post_bias, "post_bias"),
+            par(pre_weight, "pre_weight"), par(pre_bias, "pre_bias"), res(y, "y"), act(u, "u"))
+    spec = zero_block_norm_t(R, D, span, kind, 1 if post_norm and branch is not None else 0,
+                             1 if pre_norm else 0, act.type or res.type, res.type,
+                             par.type or ZERO_TYPE_BF16, gates.type or ZERO_TYPE_BF16, eps,
+                             residual_scale, branch_scale)
+    _check("zero_block_norm_forward", lib.zero_block_norm_forward(C.byref(spec), *args,
+                                                                  _raw_stream(stream)))
 
 
 def zero_block_norm_scratch_bytes(n_rows, dim, rows_per_gate=None):
@@ -896,45 +886,41 @@ def zero_block_norm_backward(y, scratch, dy=None, du=None, branch=None, gate=Non
     (with a branch), dgate, and the weights' and biases' sums over the rows, which
     may lie in a rank's gradient buffer.  scratch: a device tensor of
     zero_block_norm_scratch_bytes(rows, D, rows_per_gate) bytes."""
-    if branch is None:
-        post_norm = False
-    for name, t in (("dy", dy), ("dx", dx)):
-        if t is not None:
-            _shape(name, t, *y.shape)
-            if _float_type(t, name) != _float_type(y, "y"):
-                raise ValueError("y and %s must have one type" % name)
-    spec = _norm_spec(y, {"branch": branch, "du": du, "dbranch": dbranch}, gate,
-                      {"post_weight": post_weight, "post_bias": post_bias,
-                       "pre_weight": pre_weight}, kind, rows_per_gate, post_norm, pre_norm, eps,
-                      residual_scale, branch_scale)
-    grads = {"dpost_weight": dpost_weight, "dpost_bias": dpost_bias, "dpre_weight": dpre_weight,
-             "dpre_bias": dpre_bias}
-    for name, t in grads.items():
-        if t is not None:
-            _shape(name, t, spec.dim)
-    types = {_float_type(t, name) for name, t in grads.items() if t is not None}
-    if len(types) > 1:
-        raise ValueError("the gradients of weights and biases must have one type")
-    if dgate is not None:
-        _shape("dgate", dgate, max(1, -(-spec.n_rows // spec.rows_per_gate)), spec.dim)
-    out = zero_block_norm_grads_t(
-        _ptr(dgate, "dgate"), *[_ptr(t, name) for name, t in grads.items()],
-        _float_type(dgate, "dgate") if dgate is not None else ZERO_TYPE_BF16,
-        types.pop() if types else ZERO_TYPE_BF16)
+    shape, span, kind = _norm_call(y, kind, rows_per_gate)
+    R, D = shape
+    gate_shape = (max(1, -(-R // span)), D)
+    res, act = _Alike(shape, "y, dy and dx"), _Alike(shape, "du, branch and dbranch")
+    par, gates = _Alike((D,), "weights and biases"), _Alike(gate_shape, "gate")
+    sums = _Alike((D,), "the gradients of weights and biases")
+    gate_sums = _Alike(gate_shape, "dgate")
+    y = res(y, "y")
+    args = (res(dy, "dy"), act(du, "du"), y, act(branch, "branch"), gates(gate, "gate"),
+            par(post_weight, "post_weight"), par(post_bias, "post_bias"),
+            par(pre_weight, "pre_weight"), res(dx, "dx"), act(dbranch, "dbranch"))
+    spec = zero_block_norm_t(R, D, span, kind, 1 if post_norm and branch is not None else 0,
+                             1 if pre_norm else 0, act.type or res.type, res.type,
+                             par.type or ZERO_TYPE_BF16, gates.type or ZERO_TYPE_BF16, eps,
+                             residual_scale, branch_scale)
+    grads = zero_block_norm_grads_t(
+        gate_sums(dgate, "dgate"), sums(dpost_weight, "dpost_weight"),
+        sums(dpost_bias, "dpost_bias"), sums(dpre_weight, "dpre_weight"),
+        sums(dpre_bias, "dpre_bias"), gate_sums.type or ZERO_TYPE_BF16,
+        sums.type or ZERO_TYPE_BF16)
     _check("zero_block_norm_backward", lib.zero_block_norm_backward(
-        C.byref(spec), _ptr(dy, "dy"), _ptr(du, "du"), _ptr(y, "y"), _ptr(branch, "branch"),
-        _ptr(gate, "gate"), _ptr(post_weight, "post_weight"), _ptr(post_bias, "post_bias"),
-        _ptr(pre_weight, "pre_weight"), _ptr(dx, "dx"), _ptr(dbranch, "dbranch"), C.byref(out),
-        *_scratch(scratch), _stream(stream)))
+        C.byref(spec), *args, C.byref(grads), _at(scratch, "scratch"), scratch.nbytes,
+        _raw_stream(stream)))
 
 
-def _matrix(t, what):
+def _matrix(t, what, shape=None):
     """Address and row stride of a matrix whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions" % what)
-    if not _addressable(t) or (t.shape[1] > 1 and t.stride(1) != 1):
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    rows, cols = t.shape
+    if not _addressable(t) or (cols > 1 and t.stride(1) != 1):
         raise ValueError("%s must be CUDA or pinned host memory with contiguous rows" % what)
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
 def _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight, temperature,
@@ -943,22 +929,17 @@ def _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weigh
     R, V = logits.shape
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids must have two dimensions")
-    K = teacher_ids.shape[1]
-    _shape("teacher_ids", teacher_ids, R, K)
-    _shape("teacher_logits", teacher_logits, R, K)
-    for name, t in (("ce", ce), ("kl", kl), ("labels", labels), ("row_weight", row_weight)):
-        if t is not None:
-            _shape(name, t, R)
-            if name != "labels" and t.dtype != torch.float32:
-                raise ValueError("%s must be fp32" % name)
-    spec = zero_distill_t(R, V, stride, K, _float_type(logits, "logits"),
-                          _float_type(teacher_logits, "teacher_logits"),
-                          _index_type(teacher_ids, "teacher_ids"),
-                          _index_type(labels, "labels") if labels is not None else ZERO_TYPE_I64,
-                          float(temperature), float(ce_weight), float(kl_weight))
-    return spec, (C.byref(spec), ptr, _ptr(teacher_logits, "teacher_logits"),
-                  _ptr(teacher_ids, "teacher_ids"), _ptr(labels, "labels"),
-                  _ptr(row_weight, "row_weight"), _ptr(ce, "ce"), _ptr(kl, "kl"))
+    entries = (R, teacher_ids.shape[1])
+    rows = _Alike((R,), "ce, kl and row_weight (fp32)", ZERO_TYPE_F32)
+    spec = zero_distill_t(R, V, stride, entries[1], _type(logits, "logits"),
+                          _type(teacher_logits, "teacher_logits"),
+                          _type(teacher_ids, "teacher_ids", _INDEXES),
+                          _type(labels, "labels", _INDEXES) if labels is not None
+                          else ZERO_TYPE_I64, temperature, ce_weight, kl_weight)
+    return spec, (C.byref(spec), ptr, _at(teacher_logits, "teacher_logits", entries),
+                  _at(teacher_ids, "teacher_ids", entries),
+                  _at(labels, "labels", (R,)) if labels is not None else None,
+                  rows(row_weight, "row_weight"), rows(ce, "ce"), rows(kl, "kl"))
 
 
 def zero_distill_forward(logits, teacher_logits, teacher_ids, ce, kl, labels=None,
@@ -970,7 +951,7 @@ def zero_distill_forward(logits, teacher_logits, teacher_ids, ce, kl, labels=Non
     kl, row_weight (rows): fp32; rows of weight 0 are not read."""
     _, args = _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight,
                             temperature, 0.0, 1.0)
-    _check("zero_distill_forward", lib.zero_distill_forward(*args, _stream(stream)))
+    _check("zero_distill_forward", lib.zero_distill_forward(*args, _raw_stream(stream)))
 
 
 def zero_distill_forward_backward(logits, teacher_logits, teacher_ids, ce, kl, dlogits,
@@ -980,9 +961,8 @@ def zero_distill_forward_backward(logits, teacher_logits, teacher_ids, ce, kl, d
     row_weight * (ce_weight * ce + kl_weight * kl).  dlogits may be logits."""
     spec, args = _distill_call(logits, teacher_logits, teacher_ids, ce, kl, labels, row_weight,
                                temperature, ce_weight, kl_weight)
-    ptr, stride = _matrix(dlogits, "dlogits")
-    _shape("dlogits", dlogits, spec.n_rows, spec.vocab)
-    if _float_type(dlogits, "dlogits") != spec.logits_type:
+    ptr, stride = _matrix(dlogits, "dlogits", logits.shape)
+    if _type(dlogits, "dlogits") != spec.logits_type:
         raise ValueError("logits and dlogits must have one type")
     _check("zero_distill_forward_backward", lib.zero_distill_forward_backward(
-        *args, ptr, stride, _stream(stream)))
+        *args, ptr, stride, _raw_stream(stream)))

@@ -12,17 +12,18 @@
 // make the sum's order, and so its bits, change from run to run, would need
 // an fp32 table, and would serialise on frequent tokens.  Here the tokens are
 // put in the order of their ids (stable: by position where ids are equal), and
-// the sorted list is cut into chunks of equal length, whatever rows they
-// belong to, so that a token that makes up a tenth of the text costs no more
-// than others.  A row whose tokens all lie in one chunk is finished there; one
-// that goes across chunk borders leaves an fp32 partial sum per chunk, and
-// those are added in order.  Every sum is fp32, in a fixed order, rounded once.
+// the sorted list is cut into chunks of 16 or 32 tokens, whatever rows they
+// belong to.  A chunk sums the rows that begin in it, a few tokens past its end
+// where the last one's run on.  A frequent row, of more tokens than a chunk, is
+// summed by all the chunks that it crosses, each leaving an fp32 partial sum,
+// and those are added in order: a token that makes up a tenth of the text costs
+// no more than others.  Every sum is fp32, in a fixed order, rounded once.
 //
 //   plan_kernel  each block owns a range of the vocabulary, counts its tokens
-//                and puts them at their sorted places; rows without tokens
-//                get their zeros here.
-//   rows_kernel  the chunks' sums.
-//   join_kernel  the rows that go across chunk borders.
+//                and puts them at their sorted places.
+//   rows_kernel  the chunks' sums, and beside them the zeros of the rows
+//                without tokens: reads and writes at once.
+//   join_kernel  the frequent rows' sums over their chunks.
 //
 // Read and written: T ids, T*D of dout, V*D of dtable (each row once), and
 // 8*D bytes of partial sums per chunk at most.  HBM-bound.
@@ -102,7 +103,7 @@ int launch_lookup(const void* table, int64_t vocab, int64_t dim, const void* ids
 constexpr int kPlanWarps = 32;
 constexpr int kPlanThreads = kPlanWarps * 32;
 constexpr int kPlanMaxBins = 1024; // rows of the vocabulary a block owns, at most
-constexpr int kPlanBlocks = 152;   // wanted: one block per SM
+constexpr int kPlanBlocks = 152;   // wanted: one block per SM at most
 
 struct PlanShape {
     int64_t bins, blocks;
@@ -111,20 +112,31 @@ struct PlanShape {
 PlanShape plan_shape(int64_t vocab)
 {
     PlanShape s;
-    s.bins = (vocab + kPlanBlocks - 1) / kPlanBlocks;
+    s.bins = ((vocab + kPlanBlocks - 1) / kPlanBlocks + 31) / 32 * 32; // whole words of `empty`
     if (s.bins > kPlanMaxBins) s.bins = kPlanMaxBins;
     s.blocks = (vocab + s.bins - 1) / s.bins;
-    s.smem = static_cast<size_t>(s.bins) * (kPlanWarps + 1) * sizeof(uint32_t);
+    s.smem = static_cast<size_t>(s.bins) * (kPlanWarps + 2) * sizeof(uint32_t);
     return s;
 }
 
-// Sorted tokens per chunk.
-constexpr int kChunk = 32;
+// Sorted tokens per chunk; a row of more is frequent.  Depends on the sizes alone,
+// so that the order of the sums does too.
+// Measured (device time): 16384 x 4096 takes 84.5, 81.5 and 82.4 us with 16, 32
+// and 64 a chunk, 8192 x 768 30.0, 32.3 and 40.0: few tokens want short chunks,
+// whose rows are read one after the other.
+constexpr int kMaxChunk = 32;
+inline int chunk_size(int64_t n_tokens, int64_t dim)
+{
+    return n_tokens * dim < (int64_t(1) << 24) ? 16 : kMaxChunk;
+}
 
 struct EmbedScratch {
-    int2* sorted;    // n_tokens: (token, id) in the order of (id, token)
-    int32_t* starts; // vocab + 1: first sorted place of each row
-    float* partial;  // chunks x 2 x dim: a chunk's first and last row, where they go on outside
+    int4* sorted;   // n_tokens: (token, id, first and end place of the id), by id, then token
+    int32_t* count; // tokens whose id lies in the table
+    uint32_t* empty; // a bit for each row of the table: no token has it
+    float* partial; // chunks x 2 x dim: of the frequent row that a chunk begins in, and of the
+                    // one that begins in it
+    int per_chunk;
     int64_t chunks, bytes;
 };
 EmbedScratch embed_scratch(void* base, int64_t n_tokens, int64_t vocab, int64_t dim)
@@ -133,11 +145,14 @@ EmbedScratch embed_scratch(void* base, int64_t n_tokens, int64_t vocab, int64_t 
     EmbedScratch s;
     char* p = static_cast<char*>(base);
     int64_t at = 0;
-    s.chunks = (n_tokens + kChunk - 1) / kChunk;
-    s.sorted = reinterpret_cast<int2*>(p + at);
-    at += up(n_tokens * 8);
-    s.starts = reinterpret_cast<int32_t*>(p + at);
-    at += up((vocab + 1) * 4);
+    s.per_chunk = chunk_size(n_tokens, dim);
+    s.chunks = (n_tokens + s.per_chunk - 1) / s.per_chunk;
+    s.sorted = reinterpret_cast<int4*>(p + at);
+    at += up(n_tokens * 16);
+    s.count = reinterpret_cast<int32_t*>(p + at);
+    at += 256;
+    s.empty = reinterpret_cast<uint32_t*>(p + at);
+    at += up((vocab + 31) / 32 * 4);
     s.partial = reinterpret_cast<float*>(p + at);
     at += up(s.chunks * 2 * dim * 4);
     s.bytes = at;
@@ -188,12 +203,13 @@ __device__ __forceinline__ uint32_t block_total(uint32_t x, uint32_t* red)
 template <typename Id>
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bins,
-            int2* __restrict__ sorted, int32_t* __restrict__ starts, char* __restrict__ dtable,
-            int64_t row_bytes, int elem_bytes, int write_zeros)
+            int4* __restrict__ sorted, int32_t* __restrict__ count, uint32_t* __restrict__ empty)
 {
-    extern __shared__ uint32_t hist[]; // [kPlanWarps][bins], then row totals [bins]
-    uint32_t* totals = hist + kPlanWarps * bins;
+    extern __shared__ uint32_t hist[]; // [kPlanWarps][bins], then per row: first place, total
+    uint32_t* firsts = hist + kPlanWarps * bins;
+    uint32_t* totals = firsts + bins;
     __shared__ uint32_t red[kPlanWarps + 1];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * bins;
     const int here = static_cast<int>(vocab - first < bins ? vocab - first : bins);
@@ -204,12 +220,13 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     const int64_t lo = warp * run;
     const int64_t hi = lo + run < n_tokens ? lo + run : n_tokens;
     uint32_t* mine = hist + warp * bins;
-    constexpr int kU = 4;
+    constexpr int kU = 8;
     uint32_t below = 0;
     for (int64_t i = lo + lane; i < hi; i += 32 * kU) {
         int64_t id[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) id[u] = i + 32 * u < hi ? static_cast<int64_t>(ids[i + 32 * u]) : -1;
+        for (int u = 0; u < kU; ++u)
+            id[u] = i + 32 * u < hi ? static_cast<int64_t>(ids[i + 32 * u]) : -1;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int64_t b = id[u] - first;
@@ -219,20 +236,13 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     }
     const uint32_t base = block_total(below, red);
 
-    // totals of the rows, and each warp's place among the row's tokens
-    for (int b = tid; b < here; b += kPlanThreads) {
-        uint32_t sum = 0;
-        for (int w = 0; w < kPlanWarps; ++w) {
-            const uint32_t n = hist[w * bins + b];
-            hist[w * bins + b] = sum;
-            sum += n;
-        }
-        totals[b] = sum;
+    // the row's total, and its first place: kPlanMaxBins rows at most, one per thread
+    uint32_t total = 0;
+    if (tid < here) {
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) total += hist[w * bins + tid];
     }
-    __syncthreads();
-    // exclusive sum over the rows: kPlanMaxBins rows at most, one per thread
-    const uint32_t mine_total = tid < here ? totals[tid] : 0;
-    uint32_t incl = mine_total;
+    uint32_t incl = total;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, off);
@@ -241,13 +251,28 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     __syncthreads();
     if (lane == 31) red[warp] = incl;
     __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += red[w];
-    const uint32_t start = base + before + incl - mine_total;
+    uint32_t start = base + incl - total;
+    for (int w = 0; w < warp; ++w) start += red[w];
+    const uint32_t none = __ballot_sync(0xFFFFFFFFu, tid < here && total == 0);
+    if (lane == 0 && tid < here) empty[(first + tid) / 32] = none;
     if (tid < here) {
-        starts[first + tid] = static_cast<int32_t>(start);
-        if (first + tid == vocab - 1) starts[vocab] = static_cast<int32_t>(start + mine_total);
-        for (int w = 0; w < kPlanWarps; ++w) hist[w * bins + tid] += start;
+        totals[tid] = total;
+        firsts[tid] = start;
+        if (first + tid == vocab - 1) *count = static_cast<int32_t>(start + total);
+        if (total != 0) {
+            uint32_t at = start;
+#pragma unroll
+            for (int w0 = 0; w0 < kPlanWarps; w0 += 8) {
+                uint32_t n[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) n[w] = hist[(w0 + w) * bins + tid];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    hist[(w0 + w) * bins + tid] = at;
+                    at += n[w];
+                }
+            }
+        }
     }
     __syncthreads();
 
@@ -273,174 +298,251 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
             if (in) {
                 const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
                 if (rank == 0) mine[b] = place + __popc(peers);
-                sorted[place + rank] = make_int2(static_cast<int>(i0 + 32 * u + lane),
-                                                 static_cast<int>(id[u]));
+                const int at = static_cast<int>(firsts[b]);
+                sorted[place + rank] =
+                    make_int4(static_cast<int>(i0 + 32 * u + lane), static_cast<int>(id[u]), at,
+                              at + static_cast<int>(totals[b]));
             }
             __syncwarp();
         }
     }
-    if (!write_zeros) return;
-    for (int b = warp; b < here; b += kPlanWarps)
-        if (totals[b] == 0) warp_zero(dtable + (first + b) * row_bytes, row_bytes, elem_bytes, lane);
 }
 
 // One chunk of sorted tokens times one tile of columns; a thread holds kVec
-// columns.  Loads of kRowsUnroll rows are issued together, whatever row
-// borders lie between them.
+// columns.  The chunk's entries come to shared memory at once; then the loads of
+// kRowsUnroll rows are issued together, whatever row borders lie between them.
+constexpr int kRowsThreads = 256;
 constexpr int kRowsUnroll = 8;
+template <typename T, int kVec>
+struct RawOf { // kVec elements as loaded
+    T x;
+};
+template <typename T>
+struct RawOf<T, 8> {
+    dev::Raw8<T> x;
+};
+__device__ __forceinline__ void load_of(const Bf16* p, RawOf<Bf16, 8>& r) { dev::stream_raw8(p, r.x); }
+__device__ __forceinline__ void load_of(const float* p, RawOf<float, 8>& r) { dev::stream_raw8(p, r.x); }
+template <typename T>
+__device__ __forceinline__ void load_of(const T* p, RawOf<T, 1>& r)
+{
+    r.x = *p;
+}
+template <typename T>
+__device__ __forceinline__ void unpack_of(const RawOf<T, 8>& r, float (&x)[8])
+{
+    dev::unpack8(r.x, x);
+}
+template <typename T>
+__device__ __forceinline__ void unpack_of(const RawOf<T, 1>& r, float (&x)[1])
+{
+    x[0] = dev::load1(&r.x);
+}
 
 template <int kVec, typename In, typename Out>
-__global__ void __launch_bounds__(256)
-rows_kernel(const In* __restrict__ dout, int64_t dim, const int2* __restrict__ sorted,
-            const int32_t* __restrict__ starts, int64_t vocab, float scale, int accumulate,
+__global__ void __launch_bounds__(kRowsThreads, sizeof(In) == 2 ? 4 : 2)
+rows_kernel(const In* __restrict__ dout, int64_t dim, int zero_blocks, int tiles, int per_chunk,
+            const int4* __restrict__ sorted, const int32_t* __restrict__ count,
+            const uint32_t* __restrict__ empty, float scale, int accumulate,
             Out* __restrict__ dtable, float* __restrict__ partial)
 {
-    const int64_t n = starts[vocab];
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+    __shared__ int4 entry[2 * kMaxChunk];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the zeros first: 16384 x 4096 takes 87.2 us with the chunks first, 87.5 in turn
+    const int z = static_cast<int>(blockIdx.x), c = z - zero_blocks;
+    if (z < zero_blocks) { // 32 rows of the table, a warp at one
+        const uint32_t word = empty[z];
+        for (int r = threadIdx.x >> 5; r < 32; r += static_cast<int>(blockDim.x) >> 5)
+            if (word >> r & 1)
+                warp_zero(reinterpret_cast<char*>(dtable + (static_cast<int64_t>(z) * 32 + r) * dim),
+                          dim * sizeof(Out), sizeof(Out), threadIdx.x & 31);
+        return;
+    }
+    const int n = *count;
+    const int chunk = c / tiles, tile = c - chunk * tiles;
+    const int c0 = chunk * per_chunk;
     if (c0 >= n) return;
-    const int64_t c1 = c0 + kChunk < n ? c0 + kChunk : n;
-    const int64_t col = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * kVec;
+    const int c1 = c0 + per_chunk < n ? c0 + per_chunk : n;
+    for (int i = threadIdx.x; i < 2 * per_chunk; i += blockDim.x)
+        if (c0 + i < n) entry[i] = sorted[c0 + i];
+    __syncthreads();
+    const int64_t col = (static_cast<int64_t>(tile) * blockDim.x + threadIdx.x) * kVec;
     if (col >= dim) return;
-    int cur = sorted[c0].y;
-    bool open = c0 > 0 && sorted[c0 - 1].y == cur; // begun in an earlier chunk
+    // A row of no more than per_chunk tokens belongs to the chunk it begins in.
+    auto frequent = [&](const int4& e) { return e.w - e.z > per_chunk; };
+    const int4 head = entry[0], tail = entry[c1 - 1 - c0];
+    const int begin = head.z < c0 && !frequent(head) ? head.w : c0;
+    const int end = frequent(tail) ? c1 : tail.w;
     float acc[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
 
-    auto finish = [&] {
-        Out* o = dtable + static_cast<int64_t>(cur) * dim + col;
-        float y[kVec];
-        if (accumulate) {
-            dev::load_vec<kVec>(o, y);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) y[e] = fmaf(scale, acc[e], y[e]);
+    auto leave = [&](const int4& row) { // the sum of a row's tokens here
+        if (frequent(row)) {
+            const int slot = row.z < c0 ? 0 : 1;
+            dev::store_vec<kVec>(
+                partial + (2 * static_cast<int64_t>(chunk) + slot) * dim + col, acc);
         } else {
+            Out* o = dtable + static_cast<int64_t>(row.y) * dim + col;
+            float y[kVec];
+            if (accumulate) {
+                dev::load_vec<kVec>(o, y);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) y[e] = scale * acc[e];
+                for (int e = 0; e < kVec; ++e) y[e] = fmaf(scale, acc[e], y[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) y[e] = scale * acc[e];
+            }
+            dev::store_vec<kVec>(o, y);
         }
-        dev::store_vec<kVec>(o, y);
-    };
-    auto leave = [&](int slot) {
-        dev::store_vec<kVec>(partial + (2 * static_cast<int64_t>(blockIdx.x) + slot) * dim + col,
-                             acc);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
     };
 
-    for (int64_t i = c0; i < c1; i += kRowsUnroll) {
-        float x[kRowsUnroll][kVec];
-        int id[kRowsUnroll];
+    for (int i = begin; i < end; i += kRowsUnroll) {
+        RawOf<In, kVec> raw[kRowsUnroll];
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u)
+            if (i + u < end)
+                load_of(dout + static_cast<int64_t>(entry[i + u - c0].x) * dim + col, raw[u]);
 #pragma unroll
         for (int u = 0; u < kRowsUnroll; ++u) {
-            if (i + u < c1) {
-                const int2 s = sorted[i + u];
-                id[u] = s.y;
-                dev::load_vec<kVec>(dout + static_cast<int64_t>(s.x) * dim + col, x[u]);
-            }
-        }
+            if (i + u < end) {
+                float x[kVec];
+                unpack_of(raw[u], x);
 #pragma unroll
-        for (int u = 0; u < kRowsUnroll; ++u) {
-            if (i + u < c1) {
-                if (id[u] != cur) {
-                    if (open)
-                        leave(0);
-                    else
-                        finish();
-                    open = false;
-                    cur = id[u];
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) acc[e] = 0.0f;
-                }
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) acc[e] += x[u][e];
+                for (int e = 0; e < kVec; ++e) acc[e] += x[e];
+                const int4 row = entry[i + u - c0];
+                if (i + u + 1 == row.w || i + u + 1 == end) leave(row);
             }
         }
     }
-    if (open)
-        leave(0);
-    else if (c1 < n && sorted[c1].y == cur)
-        leave(1);
-    else
-        finish();
 }
 
-// Rows that go across chunk borders: the block of the chunk in which a row
-// begins adds that chunk's last partial and the first partials of the chunks
-// up to the row's last token.  32 columns, kJoinSlices threads each; a slice
-// adds a run of the chunks in order, the slices are added in order.
-constexpr int kJoinSlices = 8;
+// The frequent rows: the chunk that one begins in holds its first partial sum,
+// the chunks up to its last token the others.  Block x looks after the chunks
+// x, x + gridDim.x, ...; kVec columns a lane, kJoinSlices threads for each: a
+// slice adds a run of the chunks in order, the slices are added in order.
+constexpr int kJoinSlices = 8, kJoinBlocks = 64;
 
-template <typename Out>
+template <int kVec, typename Out>
 __global__ void __launch_bounds__(32 * kJoinSlices)
-join_kernel(int64_t dim, const int2* __restrict__ sorted, const int32_t* __restrict__ starts,
-            int64_t vocab, float scale, int accumulate, Out* __restrict__ dtable,
+join_kernel(int64_t dim, int per_chunk, const int4* __restrict__ sorted, const int32_t* __restrict__ count,
+            float scale, int accumulate, Out* __restrict__ dtable,
             const float* __restrict__ partial)
 {
-    const int64_t n = starts[vocab];
-    const int64_t c = blockIdx.x, c0 = c * kChunk, c1 = c0 + kChunk;
-    if (c1 >= n) return;
-    const int row = sorted[c1 - 1].y;
-    if (sorted[c1].y != row) return;                 // ends here
-    const int64_t begin = starts[row];
-    if (begin < c0) return;                          // an earlier chunk's row
-    const int64_t last = (starts[row + 1] - 1) / kChunk; // its last chunk
+    __shared__ float sums[kJoinSlices][32][kVec];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = *count;
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t count = last - c; // first partials of chunks c + 1 .. last
-    const int64_t per = (count + kJoinSlices - 1) / kJoinSlices;
-    const int64_t lo = c + 1 + slice * per;
-    const int64_t hi = lo + per < last + 1 ? lo + per : last + 1;
-    __shared__ float sums[kJoinSlices][32];
-    for (int64_t col0 = static_cast<int64_t>(blockIdx.y) * 32; col0 < dim;
-         col0 += static_cast<int64_t>(gridDim.y) * 32) {
-        const int64_t col = col0 + lane;
-        float acc = 0.0f;
-        if (col < dim) {
-            if (slice == 0) acc = partial[(2 * c + 1) * dim + col];
-#pragma unroll 4
-            for (int64_t k = lo; k < hi; ++k) acc += partial[2 * k * dim + col];
-        }
-        __syncthreads();
-        sums[slice][lane] = acc;
-        __syncthreads();
-        if (slice == 0 && col < dim) {
-            float total = 0.0f;
+    const int64_t col = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * kVec;
+    // 32 chunks at a time are looked at, one by each lane
+    for (int64_t c_base = blockIdx.x; c_base * per_chunk < n; c_base += 32 * static_cast<int64_t>(gridDim.x)) {
+        const int64_t c_mine = c_base + static_cast<int64_t>(lane) * gridDim.x;
+        int4 e = make_int4(0, 0, 0, 0);
+        if ((c_mine + 1) * per_chunk <= n) e = sorted[(c_mine + 1) * per_chunk - 1]; // its last token
+        uint32_t found = __ballot_sync(0xFFFFFFFFu, e.w - e.z > per_chunk && e.z >= c_mine * per_chunk);
+        while (found) {
+            const int who = __ffs(found) - 1;
+            found &= found - 1;
+            const int64_t c = c_base + static_cast<int64_t>(who) * gridDim.x;
+            const int row = __shfl_sync(0xFFFFFFFFu, e.y, who);
+            const int64_t last = (__shfl_sync(0xFFFFFFFFu, e.w, who) - 1) / per_chunk;
+            const int64_t per = (last - c + kJoinSlices - 1) / kJoinSlices;
+            const int64_t lo = c + 1 + slice * per;
+            const int64_t hi = lo + per < last + 1 ? lo + per : last + 1;
+            float acc[kVec], x[kVec];
 #pragma unroll
-            for (int s = 0; s < kJoinSlices; ++s) total += sums[s][lane];
-            Out* o = dtable + static_cast<int64_t>(row) * dim + col;
-            dev::store1(o, accumulate ? fmaf(scale, total, dev::load1(o)) : scale * total);
+            for (int v = 0; v < kVec; ++v) acc[v] = 0.0f;
+            auto add = [&](const float* p) {
+                if constexpr (kVec == 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(p);
+                    x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+                } else {
+                    x[0] = *p;
+                }
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) acc[v] += x[v];
+            };
+            if (col < dim) {
+                if (slice == 0) add(partial + (2 * c + 1) * dim + col);
+#pragma unroll 4
+                for (int64_t k = lo; k < hi; ++k) add(partial + 2 * k * dim + col);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) sums[slice][lane][v] = acc[v];
+            __syncthreads();
+            if (slice == 0 && col < dim) {
+                Out* o = dtable + static_cast<int64_t>(row) * dim + col;
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    float total = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < kJoinSlices; ++s) total += sums[s][lane][v];
+                    dev::store1(o + v,
+                                accumulate ? fmaf(scale, total, dev::load1(o + v)) : scale * total);
+                }
+            }
         }
     }
+}
+
+// A launch that may begin while the kernel before it on the stream drains; the
+// kernel waits for that one's results itself.
+template <typename... Params, typename... Given>
+int launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Given... given)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...));
 }
 
 template <typename In, typename Out>
-int launch_rows(const void* dout, int64_t dim, const EmbedScratch& s, int64_t vocab, float scale,
+int launch_rows(const void* dout, int64_t dim, int64_t vocab, const EmbedScratch& s, float scale,
                 int32_t accumulate, void* dtable, cudaStream_t stream)
 {
     const bool wide = dim % 8 == 0 && aligned16(dout) && aligned16(dtable);
     const int64_t vecs = wide ? dim / 8 : dim;
-    int threads = 256;
+    int threads = kRowsThreads;
     if (vecs < threads) threads = static_cast<int>((vecs + 31) / 32 * 32);
-    const dim3 grid(static_cast<unsigned>(s.chunks),
-                    static_cast<unsigned>((vecs + threads - 1) / threads));
+    const int64_t tiles = (vecs + threads - 1) / threads;
+    const int64_t zero_blocks = accumulate ? 0 : (vocab + 31) / 32;
+    const int64_t blocks = zero_blocks + s.chunks * tiles;
+    if (blocks == 0) return ZERO_OK;
+    if (blocks > 0x7FFFFFFF) return ZERO_EINVAL;
+    const dim3 grid(static_cast<unsigned>(blocks));
     const auto* in = static_cast<const In*>(dout);
     auto* out = static_cast<Out*>(dtable);
-    if (wide)
-        rows_kernel<8, In, Out><<<grid, threads, 0, stream>>>(in, dim, s.sorted, s.starts, vocab,
-                                                              scale, accumulate, out, s.partial);
-    else
-        rows_kernel<1, In, Out><<<grid, threads, 0, stream>>>(in, dim, s.sorted, s.starts, vocab,
-                                                              scale, accumulate, out, s.partial);
-    const int rc = cuda_status(cudaGetLastError());
+    const int rc =
+        wide ? launch_after(rows_kernel<8, In, Out>, grid, dim3(threads), stream, in, dim,
+                            zero_blocks, tiles, s.per_chunk, s.sorted, s.count, s.empty, scale, accumulate, out,
+                            s.partial)
+             : launch_after(rows_kernel<1, In, Out>, grid, dim3(threads), stream, in, dim,
+                            zero_blocks, tiles, s.per_chunk, s.sorted, s.count, s.empty, scale, accumulate, out,
+                            s.partial);
     if (rc != ZERO_OK || s.chunks < 2) return rc;
-    const int64_t tiles = (dim + 31) / 32;
-    const dim3 jgrid(static_cast<unsigned>(s.chunks - 1),
-                     static_cast<unsigned>(tiles < 1024 ? tiles : 1024));
-    join_kernel<Out><<<jgrid, 32 * kJoinSlices, 0, stream>>>(dim, s.sorted, s.starts, vocab, scale,
-                                                             accumulate, out, s.partial);
-    return cuda_status(cudaGetLastError());
+    const bool four = dim % 4 == 0;
+    const int64_t strips = (dim + (four ? 127 : 31)) / (four ? 128 : 32);
+    const dim3 jgrid(static_cast<unsigned>(s.chunks < kJoinBlocks ? s.chunks : kJoinBlocks),
+                     static_cast<unsigned>(strips));
+    return four ? launch_after(join_kernel<4, Out>, jgrid, dim3(32 * kJoinSlices), stream, dim,
+                               s.per_chunk, s.sorted, s.count, scale, accumulate, out, s.partial)
+                : launch_after(join_kernel<1, Out>, jgrid, dim3(32 * kJoinSlices), stream, dim,
+                               s.per_chunk, s.sorted, s.count, scale, accumulate, out, s.partial);
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30; // places and starts are 32-bit
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
-constexpr int64_t kMaxDim = int64_t(1) << 22;
+constexpr int64_t kMaxDim = int64_t(1) << 20;
 
 bool embed_sizes_ok(int64_t vocab, int64_t dim, int64_t n_tokens)
 {
@@ -505,30 +607,29 @@ extern "C" int zero_embed_backward(const void* dout, int32_t dout_type, const vo
     if (n_tokens == 0 && accumulate) return ZERO_OK;
 
     const PlanShape p = plan_shape(vocab);
-    const int elem = type_bytes(dtable_type);
     const void* plan = id_type == ZERO_TYPE_I64
                            ? reinterpret_cast<const void*>(plan_kernel<int64_t>)
                            : reinterpret_cast<const void*>(plan_kernel<int32_t>);
-    if (p.smem > 48 * 1024 &&
+    if (p.smem > 32 * 1024 && // beside the static words
         cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(p.smem)) != cudaSuccess)
         return ZERO_ECUDA;
+    const unsigned blocks = static_cast<unsigned>(p.blocks);
+    const int bins = static_cast<int>(p.bins);
     if (id_type == ZERO_TYPE_I64)
-        plan_kernel<int64_t><<<static_cast<unsigned>(p.blocks), kPlanThreads, p.smem, stream>>>(
-            static_cast<const int64_t*>(ids), n_tokens, vocab, static_cast<int>(p.bins), s.sorted,
-            s.starts, static_cast<char*>(dtable), dim * elem, elem, !accumulate);
+        plan_kernel<int64_t><<<blocks, kPlanThreads, p.smem, stream>>>(
+            static_cast<const int64_t*>(ids), n_tokens, vocab, bins, s.sorted, s.count, s.empty);
     else
-        plan_kernel<int32_t><<<static_cast<unsigned>(p.blocks), kPlanThreads, p.smem, stream>>>(
-            static_cast<const int32_t*>(ids), n_tokens, vocab, static_cast<int>(p.bins), s.sorted,
-            s.starts, static_cast<char*>(dtable), dim * elem, elem, !accumulate);
+        plan_kernel<int32_t><<<blocks, kPlanThreads, p.smem, stream>>>(
+            static_cast<const int32_t*>(ids), n_tokens, vocab, bins, s.sorted, s.count, s.empty);
     const int rc = cuda_status(cudaGetLastError());
-    if (rc != ZERO_OK || n_tokens == 0) return rc;
+    if (rc != ZERO_OK) return rc;
     const float sc = static_cast<float>(scale);
     if (dout_type == ZERO_TYPE_BF16)
         return dtable_type == ZERO_TYPE_BF16
-                   ? launch_rows<Bf16, Bf16>(dout, dim, s, vocab, sc, accumulate, dtable, stream)
-                   : launch_rows<Bf16, float>(dout, dim, s, vocab, sc, accumulate, dtable, stream);
+                   ? launch_rows<Bf16, Bf16>(dout, dim, vocab, s, sc, accumulate, dtable, stream)
+                   : launch_rows<Bf16, float>(dout, dim, vocab, s, sc, accumulate, dtable, stream);
     return dtable_type == ZERO_TYPE_BF16
-               ? launch_rows<float, Bf16>(dout, dim, s, vocab, sc, accumulate, dtable, stream)
-               : launch_rows<float, float>(dout, dim, s, vocab, sc, accumulate, dtable, stream);
+               ? launch_rows<float, Bf16>(dout, dim, vocab, s, sc, accumulate, dtable, stream)
+               : launch_rows<float, float>(dout, dim, vocab, s, sc, accumulate, dtable, stream);
 }

@@ -816,7 +816,7 @@ const char* zero_strerror(int code);
  *   table   [vocab, dim], table_type ZERO_TYPE_BF16 or ZERO_TYPE_F32
  *   ids     [n_tokens], id_type ZERO_TYPE_I32 or ZERO_TYPE_I64
  *   out     [n_tokens, dim], out_type ZERO_TYPE_BF16 or ZERO_TYPE_F32
- * vocab and n_tokens up to 2^30, dim up to 2^22; n_tokens = 0 does nothing.
+ * vocab and n_tokens up to 2^30, dim up to 2^20; n_tokens = 0 does nothing.
  * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
 int zero_embed_forward(const void* table, int32_t table_type, int64_t vocab, int64_t dim,
                        const void* ids, int32_t id_type, int64_t n_tokens, double scale,

@@ -49,7 +49,7 @@ def test_embed_backward_refuses(B):
 
     for kw in (dict(dout=None), dict(ids=None), dict(dtable=None), dict(scratch=None),
                dict(bytes=need - 1), dict(dt=5), dict(gt=4), dict(it=2), dict(acc=2), dict(n=-1),
-               dict(V=0), dict(D=(1 << 22) + 1)):
+               dict(V=0), dict(D=(1 << 22) + 1), dict(D=(1 << 20) + 1)):
         assert call(**kw) == EINVAL, kw
     for kw in (dict(dout=P + 1), dict(ids=P + 4), dict(dtable=P + 1), dict(scratch=P + 8)):
         assert call(**kw) == EALIGN, kw
