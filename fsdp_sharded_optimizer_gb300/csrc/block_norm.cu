@@ -170,6 +170,15 @@ __device__ __forceinline__ void store_edge(T* p, int col, int dim, const float2 
     for (int e = 0; e < 8; ++e)
         if (col + e >= 0 && col + e < dim) dev::store1(p + col + e, part(x, e));
 }
+// 16 bytes at once where the address allows.
+template <typename T>
+__device__ __forceinline__ void store_cols(T* p, int col, int dim, const float2 (&x)[4])
+{
+    if ((reinterpret_cast<uintptr_t>(p + col) & 15) == 0 && col >= 0 && col + 8 <= dim)
+        dev::store8_stream(p + col, x);
+    else
+        store_edge(p, col, dim, x);
+}
 // Weights, biases and gate rows: read seldom, at any alignment.
 __device__ __forceinline__ void load_vector(const void* p, int32_t type, int64_t row, int col,
                                             int dim, float absent, float2 (&x)[4])
@@ -405,22 +414,23 @@ forward_kernel(const Geometry G, const Params P, const Res* __restrict__ x,
 // ----------------------------------------------------------------- backward
 // Per-column factors that a thread keeps in shared memory, where the sums take
 // its registers: its own 8 columns of vector k, piece i, as two 16-byte words;
-// consecutive threads have consecutive words.  No other thread reads them.
+// consecutive threads have consecutive words, and a thread's words lie a constant
+// kThreads apart.  No other thread reads them.
 template <int kNV>
 struct Slots {
     float4* base;
     __device__ __forceinline__ float4* at(int k, int i) const
     {
-        return base + (k * kNV + i) * 2 * blockDim.x + threadIdx.x;
+        return base + (k * kNV + i) * 2 * kThreads + threadIdx.x;
     }
     __device__ __forceinline__ void put(int k, int i, const float2 (&x)[4]) const
     {
         at(k, i)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-        at(k, i)[blockDim.x] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+        at(k, i)[kThreads] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
     }
     __device__ __forceinline__ void get(int k, int i, float2 (&x)[4]) const
     {
-        const float4 a = at(k, i)[0], b = at(k, i)[blockDim.x];
+        const float4 a = at(k, i)[0], b = at(k, i)[kThreads];
         x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
         x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
     }
@@ -710,9 +720,413 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
     }
 }
 
-// Sums the blocks' partials (blockIdx.y < vectors) and the shared gate rows'.
-// 32 columns x kSlices threads; a slice adds a run of the partials in order,
-// the slices are added in order.
+// ------------------------------------------- backward, two rows at a time
+// For rows of whole 16-byte pieces, at most one piece a thread (dim <= 4096): the
+// usual case.  A group takes two rows at once: their sums share the exchanges
+// between the warps, whose latency is what a row costs most (measured, 16384 x
+// 2048 with an fp32 residual: one row at a time 119 us).  The next two rows come to
+// shared memory meanwhile (cp.async), each thread's pieces to its own slots,
+// which no other thread touches, so no barrier is needed for them and no
+// register is held.
+
+// One tensor's two pieces of a thread: 16-byte words, kThreads apart.
+template <typename T>
+struct Pieces {
+    static constexpr int kWords = sizeof(T) / 2; // of one piece
+    uint4* base;                                 // word 0 of row 0
+
+    __device__ __forceinline__ uint4* word(int row, int w) const
+    {
+        return base + (row * kWords + w) * kThreads;
+    }
+    __device__ __forceinline__ void fetch(int row, const T* p) const
+    {
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(base));
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            // the two words of an fp32 piece are half a sector each: through the L1,
+            // where the second finds the first's
+            if constexpr (kWords == 1)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 to + (row * kWords + w) * (16 * kThreads)),
+                             "l"(p)
+                             : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                 to + (row * kWords + w) * (16 * kThreads)),
+                             "l"(reinterpret_cast<const uint4*>(p) + w)
+                             : "memory");
+        }
+    }
+    __device__ __forceinline__ void clear(int row) const
+    {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) *word(row, w) = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(int row, float2 (&x)[4]) const
+    {
+        dev::Raw8<T> r;
+        if constexpr (kWords == 1) {
+            r.a = *word(row, 0);
+        } else {
+            r.a = *reinterpret_cast<const float4*>(word(row, 0));
+            r.b = *reinterpret_cast<const float4*>(word(row, 1));
+        }
+        dev::unpack8(r, x);
+    }
+};
+
+// Sums of 8 values over the group, valid in all its threads: 9 shuffles in the
+// warp (a lane keeps half of its values at each of the first three steps), a
+// word per warp and value in shared memory (`red`: two buffers of 8 x 16 words
+// for the group, zero where there is no warp), and 8 to hand them round.
+__device__ __forceinline__ void group_sum8(Group& g, float* red, float (&v)[8])
+{
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    float a[4], b[2];
+    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a[i] = (b4 ? v[i + 4] : v[i]) + __shfl_xor_sync(kAll, b4 ? v[i] : v[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = (b3 ? a[i + 2] : a[i]) + __shfl_xor_sync(kAll, b3 ? a[i] : a[i + 2], 8);
+    float x = (b2 ? b[1] : b[0]) + __shfl_xor_sync(kAll, b2 ? b[0] : b[1], 4);
+    x += __shfl_xor_sync(kAll, x, 2);
+    x += __shfl_xor_sync(kAll, x, 1); // the sum of value lane >> 2
+    if (g.warps > 1) {
+        float* buf = red + g.buffer * (8 * kMaxWarps);
+        if ((lane & 3) == 0)
+            buf[(lane >> 2) * kMaxWarps + (threadIdx.x >> 5) - g.first_warp] = x;
+        asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.threads) : "memory");
+        const float4 w = *reinterpret_cast<const float4*>(buf + 4 * lane);
+        x = (w.x + w.y) + (w.z + w.w);
+        x += __shfl_xor_sync(kAll, x, 2);
+        x += __shfl_xor_sync(kAll, x, 1);
+        g.buffer ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kAll, x, 4 * i);
+}
+
+template <int kMode, typename Act, typename Res>
+__global__ void __launch_bounds__(kThreads)
+backward_pair_kernel(const Geometry G, const Params P, const Grads D, const Res* __restrict__ dy,
+                     const Act* __restrict__ du, const Res* __restrict__ y,
+                     const Act* __restrict__ h, Res* __restrict__ dx, Act* __restrict__ dh)
+{
+    constexpr bool kFull = kMode != kPlain;
+    constexpr int kSums = kFull ? kVectors + 1 : 3;
+    constexpr int kFactors = kFull ? 4 : 3;
+    extern __shared__ float4 shared[];
+    // [kFactors x 2] words of factors, then the pieces of two rows, then the
+    // groups' exchange words
+    const Slots<1> slots = {shared};
+    const int block = static_cast<int>(blockDim.x);
+    constexpr int kRes = 2 * Pieces<Res>::kWords * kThreads, kAct = 2 * Pieces<Act>::kWords * kThreads;
+    uint4* pieces = reinterpret_cast<uint4*>(shared) + kFactors * 2 * kThreads;
+    const Pieces<Res> s_dy = {pieces + threadIdx.x};
+    const Pieces<Res> s_y = {pieces + kRes + threadIdx.x};
+    const Pieces<Act> s_du = {pieces + 2 * kRes + threadIdx.x};
+    const Pieces<Act> s_h = {pieces + 2 * kRes + kAct + threadIdx.x};
+    Group g = make_group(G.threads);
+    float* red = reinterpret_cast<float*>(pieces + 2 * kRes + 2 * kAct) + g.id * (2 * 8 * kMaxWarps);
+    for (int i = g.thread; i < 2 * 8 * kMaxWarps; i += g.threads) red[i] = 0.0f;
+
+    const int64_t worker = static_cast<int64_t>(blockIdx.x) * G.groups + g.id;
+    const int64_t lo = worker * G.run;
+    const int64_t hi = lo + G.run < G.rows ? lo + G.run : G.rows;
+    const int dim = static_cast<int>(G.dim);
+    const float inv = 1.0f / static_cast<float>(dim);
+    const int col = g.thread * 8;
+    const bool full = col < dim;
+    // dw post, dw pre, dgate / branch_scale; dc post, dc pre
+    float2 sums[kSums][4];
+#pragma unroll
+    for (int a = 0; a < kSums; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[a][e] = dev::pair(0.0f);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) { // what is absent, or outside the row, stays 0
+        s_dy.clear(r);
+        s_y.clear(r);
+        s_du.clear(r);
+        s_h.clear(r);
+    }
+
+    const bool by_rows = D.gate_rows > 1;
+    int64_t gate_row = P.gate && lo < hi ? lo / G.span : 0;
+    int64_t gate_end = P.gate ? (gate_row + 1) * G.span : G.rows;
+    const int64_t first_gate = gate_row;
+    auto load_gate = [&] { // branch_scale * gate
+        float2 w[4];
+        load_vector(P.gate, P.gate_type, gate_row, col, dim, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = dev::mul2(w[e], dev::pair(P.branch_scale));
+        slots.put(kSlotGate, 0, w);
+    };
+    // The sum of one gate row: final where this worker has all its rows.
+    auto leave_gate = [&] {
+        const int64_t from = gate_row * G.span;
+        const int64_t to = from + G.span < G.rows ? from + G.span : G.rows;
+        float2 t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t[e] = dev::mul2(dev::pair(P.branch_scale), sums[2][e]);
+            sums[2][e] = dev::pair(0.0f);
+        }
+        if (!full) return;
+        if (!(from >= lo && to <= hi)) {
+            const int slot = gate_row == first_gate ? 0 : 1;
+            store_cols(D.gate_partial + (2 * worker + slot) * G.dim, col, dim, t);
+        } else if (D.dgate_type == ZERO_TYPE_BF16) {
+            store_cols(static_cast<Bf16*>(D.dgate) + gate_row * G.dim, col, dim, t);
+        } else {
+            store_cols(static_cast<float*>(D.dgate) + gate_row * G.dim, col, dim, t);
+        }
+    };
+    // Rows of the pair that begins at `row`: one where the run or the gate row ends.
+    auto pair_rows = [&](int64_t row, int64_t end_of_gate) {
+        return row + 1 < hi && row + 1 < end_of_gate ? 2 : 1;
+    };
+    auto fetch = [&](int64_t row, int rows) {
+        if (full) {
+            for (int r = 0; r < rows; ++r) {
+                const int64_t at = (row + r) * G.dim + col;
+                if (dy) s_dy.fetch(r, dy + at);
+                if (P.pre) {
+                    s_y.fetch(r, y + at);
+                    s_du.fetch(r, du + at);
+                }
+            }
+        }
+    };
+    // The branch's pieces are read twice, and fetched once they are done with.
+    auto fetch_branch = [&](int64_t row, int rows) {
+        if (full && h)
+            for (int r = 0; r < rows; ++r) s_h.fetch(r, h + (row + r) * G.dim + col);
+    };
+    auto clear_second = [&] { // a pair of one row
+        s_dy.clear(1);
+        s_y.clear(1);
+        s_du.clear(1);
+    };
+    int rows = 0;
+    if (lo < hi) {
+        rows = pair_rows(lo, gate_end);
+        fetch(lo, rows);
+        fetch_branch(lo, rows);
+        load_gate();
+        float2 w[4];
+        load_vector(P.post_w, P.param_type, 0, col, dim, 1.0f, w);
+        slots.put(kSlotPost, 0, w);
+        load_vector(P.pre_w, P.param_type, 0, col, dim, 1.0f, w);
+        slots.put(kSlotPre, 0, w);
+        if (kFull) {
+            load_vector(P.post_b, P.param_type, 0, col, dim, 0.0f, w);
+            slots.put(kSlotBias, 0, w);
+        }
+    }
+    __syncthreads(); // the exchange words are 0
+
+    for (int64_t row = lo; row < hi;) {
+        const int64_t next = row + rows;
+        if (row >= gate_end) {
+            if (by_rows) leave_gate();
+            gate_row = row / G.span;
+            gate_end = (gate_row + 1) * G.span;
+            load_gate();
+        }
+        int next_rows = 0;
+        if (next < hi) {
+            const int64_t end = P.gate && next >= gate_end ? (next / G.span + 1) * G.span : gate_end;
+            next_rows = pair_rows(next, end);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        float2 t[2][4], v[2][4], d[2][4]; // dy, then g; y; du
+        float s[8] = {};                  // of row r: s[r], s[2 + r], s[4 + r]
+        float mean_n[2] = {0.0f, 0.0f}, m0[2] = {0.0f, 0.0f};
+        float2 w[4];
+        slots.get(kSlotPre, 0, w);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            s_dy.get(r, t[r]);
+            s_y.get(r, v[r]);
+            s_du.get(r, d[r]);
+        }
+        if (kFull && P.layer) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float2 n[4], a = dev::pair(0.0f), b = a, c = a;
+                s_h.get(r, n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    a = dev::add2(a, v[r][e]);
+                    b = dev::fma2(d[r][e], w[e], b);
+                    c = dev::add2(c, n[e]);
+                }
+                s[r] = a.x + a.y;
+                s[2 + r] = b.x + b.y;
+                s[4 + r] = c.x + c.y;
+            }
+            group_sum8(g, red, s);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 mean = dev::pair(full ? -s[r] * inv : 0.0f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[r][e] = dev::add2(v[r][e], mean);
+                m0[r] = s[2 + r] * inv;
+                mean_n[r] = full && P.post ? -s[4 + r] * inv : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float2 n[4], a = dev::pair(0.0f), b = a, c = a;
+            s_h.get(r, n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (kFull) n[e] = dev::add2(n[e], dev::pair(mean_n[r]));
+                a = dev::fma2(v[r][e], v[r][e], a);
+                b = dev::fma2(dev::mul2(d[r][e], w[e]), v[r][e], b);
+                c = dev::fma2(n[e], n[e], c);
+            }
+            s[r] = a.x + a.y;
+            s[2 + r] = b.x + b.y;
+            s[4 + r] = c.x + c.y;
+        }
+        s[6] = s[7] = 0.0f;
+        // the three tensors are in registers: their slots take the next rows
+        if (next_rows) {
+            fetch(next, next_rows);
+            if (next_rows == 1) clear_second();
+        }
+        group_sum8(g, red, s);
+        if (P.pre) {
+            slots.get(kSlotPre, 0, w);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float rstd = rsqrtf(fmaf(s[r], inv, P.eps));
+                const float2 rr = dev::pair(rstd);
+                const float2 k = dev::pair(-rstd * rstd * rstd * s[2 + r] * inv); // -r^2 mean(du w y^)
+                const float2 k0 = dev::pair(full ? -rstd * m0[r] : 0.0f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (kFull) sums[4][e] = dev::add2(sums[4][e], d[r][e]);
+                    d[r][e] = dev::mul2(d[r][e], rr);
+                    sums[1][e] = dev::fma2(d[r][e], v[r][e], sums[1][e]);
+                    t[r][e] = dev::fma2(k, v[r][e], dev::fma2(d[r][e], w[e], t[r][e]));
+                    if (kFull) t[r][e] = dev::add2(t[r][e], k0);
+                }
+            }
+        }
+        if (dx && full) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float2 o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = dev::mul2(dev::pair(P.res_scale), t[r][e]);
+                if (r < rows) dev::store8_stream(dx + (row + r) * G.dim + col, o);
+            }
+        }
+        if (h) {
+            float2 n[2][4], pw[4], gate[4], pb[4];
+            slots.get(kSlotPost, 0, pw);
+            slots.get(kSlotGate, 0, gate);
+            if (kFull) slots.get(kSlotBias, 0, pb);
+            float2 rr[2];
+            float m[4] = {};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                s_h.get(r, n[r]);
+                rr[r] = dev::pair(P.post ? rsqrtf(fmaf(s[4 + r], inv, P.eps)) : 1.0f);
+                float2 a = dev::pair(0.0f), b = a;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (kFull) n[r][e] = dev::add2(n[r][e], dev::pair(mean_n[r]));
+                    n[r][e] = dev::mul2(n[r][e], rr[r]);
+                    const float2 x =
+                        kFull ? dev::fma2(n[r][e], pw[e], pb[e]) : dev::mul2(n[r][e], pw[e]);
+                    sums[2][e] = dev::fma2(t[r][e], x, sums[2][e]);
+                    t[r][e] = dev::mul2(t[r][e], gate[e]);
+                    if (kFull) sums[3][e] = dev::add2(sums[3][e], t[r][e]);
+                    sums[0][e] = dev::fma2(t[r][e], n[r][e], sums[0][e]);
+                    t[r][e] = dev::mul2(t[r][e], pw[e]);
+                    if (kFull) b = dev::add2(b, t[r][e]);
+                    a = dev::fma2(t[r][e], n[r][e], a);
+                }
+                m[r] = a.x + a.y;
+                m[2 + r] = b.x + b.y;
+            }
+            if (next_rows) {
+                fetch_branch(next, next_rows);
+                if (next_rows == 1) s_h.clear(1);
+            }
+            if (P.post) {
+                if (kFull) {
+                    group_sum(g, m);
+                } else {
+                    float two[2] = {m[0], m[1]};
+                    group_sum(g, two);
+                    m[0] = two[0];
+                    m[1] = two[1];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 k1 = dev::pair(P.post ? -m[r] * inv : 0.0f);
+                const float2 k0 = dev::pair(kFull && P.post && P.layer ? -m[2 + r] * inv : 0.0f);
+                float2 o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[e] = kFull ? dev::add2(t[r][e], k0) : t[r][e];
+                    o[e] = dev::mul2(rr[r], dev::fma2(k1, n[r][e], o[e]));
+                }
+                if (full && r < rows) dev::store8_stream(dh + (row + r) * G.dim + col, o);
+            }
+        }
+        row = next;
+        rows = next_rows;
+    }
+    if (by_rows && lo < hi) leave_gate();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // The block's sums, its groups added in order: every thread's sums to shared
+    // memory, 16-byte words of the same columns G.threads apart.
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < kSums; ++a) {
+        const float k = a == 2 ? P.branch_scale : 1.0f;
+        shared[(2 * a) * block + threadIdx.x] =
+            make_float4(k * sums[a][0].x, k * sums[a][0].y, k * sums[a][1].x, k * sums[a][1].y);
+        shared[(2 * a + 1) * block + threadIdx.x] =
+            make_float4(k * sums[a][2].x, k * sums[a][2].y, k * sums[a][3].x, k * sums[a][3].y);
+    }
+    __syncthreads();
+    constexpr int kPlace[kVectors + 1] = {0, 2, kVectors, 1, 3}; // in Finals' order
+#pragma unroll
+    for (int a = 0; a < kSums; ++a) {
+        if (kPlace[a] >= D.vectors) continue;
+        float* out = D.partial + (static_cast<int64_t>(blockIdx.x) * D.vectors + kPlace[a]) * G.dim;
+        for (int i = threadIdx.x; i < 2 * G.threads; i += block) {
+            const int half = i >= G.threads ? 1 : 0, thread = i - half * G.threads;
+            if (thread * 8 >= dim) continue;
+            const float4* p = shared + (2 * a + half) * block + thread;
+            float4 x = p[0];
+            for (int k = 1; k < G.groups; ++k) {
+                const float4 z = p[k * G.threads];
+                x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+            }
+            *reinterpret_cast<float4*>(out + thread * 8 + half * 4) = x;
+        }
+    }
+}
+
+// Sums the blocks' partials, and those of the gate rows that several workers
+// share: blockIdx.y is one of the sums over all rows, or, from D.vectors on, the
+// end of a worker's run that lies inside a gate row (the first such end, where
+// the gate row spans more than two runs).  kVec columns a lane, kSlices threads
+// each: a slice adds a run of the partials in order, the slices are added in order.
 constexpr int kSlices = 8;
 
 struct Finals {
@@ -720,66 +1134,76 @@ struct Finals {
     int32_t type[kVectors + 1];
 };
 
+template <int kVec>
 __global__ void __launch_bounds__(32 * kSlices)
 reduce_kernel(const Geometry G, const Grads D, const Finals F)
 {
-    // launched while the blocks of backward_kernel drain; waits for all of them
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    __shared__ float sums[kSlices][32];
-    const int64_t tasks = D.vectors + (D.gate_rows > 1 ? D.gate_rows : 0);
-    for (int64_t task = blockIdx.y; task < tasks; task += gridDim.y) {
-        const float* src;
-        int64_t first, count, step;
-        void* out;
-        int32_t type;
-        float acc = 0.0f;
-        if (task < D.vectors) {
-            out = F.out[task];
-            type = F.type[task];
-            if (!out) continue;
-            src = D.partial + task * G.dim;
-            first = 0;
-            count = G.blocks;
-            step = D.vectors * G.dim;
+    const int dim = static_cast<int>(G.dim);
+    const int col = (static_cast<int>(blockIdx.x) * 32 + lane) * kVec;
+    const int task = static_cast<int>(blockIdx.y);
+    __shared__ float sums[kSlices][32][kVec];
+    // launched while the blocks of the kernel before drain; every block waits for
+    // all of them, so that this kernel's end is also theirs
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float* src; // the slices' share: src + k * step, k < count
+    const float* head = nullptr;
+    int64_t step, count;
+    void* out;
+    int32_t type;
+    int64_t out_row = 0;
+    if (task < D.vectors) {
+        out = F.out[task];
+        type = F.type[task];
+        if (!out) return;
+        src = D.partial + task * G.dim;
+        count = G.blocks;
+        step = D.vectors * G.dim;
+    } else {
+        const int64_t worker = task - D.vectors; // the worker before the end looked at
+        const int64_t end = (worker + 1) * G.run;
+        if (end >= G.rows || end % G.span == 0) return;
+        const int64_t q = end / G.span, from = q * G.span; // the gate row
+        if (from / G.run != worker) return; // it began before
+        const int64_t to = from + G.span < G.rows ? from + G.span : G.rows;
+        // its first worker holds it as its last gate row, unless it is its first
+        // too; the others as their first
+        head = D.gate_partial + (2 * worker + (worker * G.run / G.span == q ? 0 : 1)) * G.dim;
+        src = D.gate_partial + 2 * (worker + 1) * G.dim;
+        step = 2 * G.dim;
+        count = (to - 1) / G.run - worker;
+        out = D.dgate;
+        type = D.dgate_type;
+        out_row = q * G.dim;
+    }
+    float acc[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) acc[v] = 0.0f;
+    auto add = [&](const float* p) {
+        if constexpr (kVec == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + col);
+            acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
         } else {
-            const int64_t q = task - D.vectors; // gate row
-            const int64_t from = q * G.span;
-            const int64_t to = from + G.span < G.rows ? from + G.span : G.rows;
-            if (G.classes != 1) continue; // rows of one token: final already
-            first = from / G.run;
-            count = (to - 1) / G.run - first + 1;
-            if (count == 1) continue; // one worker's: final already
-            src = D.gate_partial;
-            step = 2 * G.dim;
-            // the first worker holds it as its last row, unless it is its first too
-            if (slice == 0 && first * G.run / G.span != q) {
-                if (col < G.dim) acc = src[(2 * first + 1) * G.dim + col];
-                ++first;
-                --count;
-            } else if (first * G.run / G.span != q) {
-                ++first;
-                --count;
-            }
-            out = static_cast<char*>(D.dgate) +
-                  q * G.dim * (D.dgate_type == ZERO_TYPE_BF16 ? 2 : 4);
-            type = D.dgate_type;
+            acc[0] += p[col];
         }
-        const int64_t per = (count + kSlices - 1) / kSlices;
-        const int64_t lo = slice * per, hi = lo + per < count ? lo + per : count;
-        if (col < G.dim) {
+    };
+    const int64_t per = (count + kSlices - 1) / kSlices;
+    const int64_t lo = slice * per, hi = lo + per < count ? lo + per : count;
+    if (col < dim) {
+        if (slice == 0 && head) add(head);
 #pragma unroll 8
-            for (int64_t k = lo; k < hi; ++k) acc += src[(first + k) * step + col];
-        }
-        __syncthreads();
-        sums[slice][lane] = acc;
-        __syncthreads();
-        if (slice == 0 && col < G.dim) {
+        for (int64_t k = lo; k < hi; ++k) add(src + k * step);
+    }
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) sums[slice][lane][v] = acc[v];
+    __syncthreads();
+    if (slice == 0 && col < dim) {
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
             float all[1] = {0.0f};
 #pragma unroll
-            for (int w = 0; w < kSlices; ++w) all[0] += sums[w][lane];
-            dev::store_any<1>(out, type, col, all);
+            for (int w = 0; w < kSlices; ++w) all[0] += sums[w][lane][v];
+            dev::store_any<1>(out, type, out_row + col + v, all);
         }
     }
 }
@@ -902,10 +1326,11 @@ void start_forward(const Geometry& G, const Params& P, const Res* x, const Act* 
     const unsigned grid = static_cast<unsigned>(G.blocks);
     const unsigned block = static_cast<unsigned>(G.threads * G.groups);
     const Mode mode = mode_of(G, P.layer || P.post_b || P.pre_b);
+    constexpr int kP = kNV < 4 ? kPlain : kEdges, kW = kNV < 4 ? kWhole : kEdges;
     if (mode == kPlain)
-        forward_kernel<kNV, kPlain, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+        forward_kernel<kNV, kP, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
     else if (mode == kWhole)
-        forward_kernel<kNV, kWhole, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
+        forward_kernel<kNV, kW, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
     else
         forward_kernel<kNV, kEdges, Act, Res><<<grid, block, 0, stream>>>(G, P, x, h, y, u);
 }
@@ -934,12 +1359,27 @@ int start_backward(const Geometry& G, const Params& P, const Grads& D, bool full
     const unsigned grid = static_cast<unsigned>(G.blocks);
     const unsigned block = static_cast<unsigned>(G.threads * G.groups);
     const Mode mode = mode_of(G, full);
-    size_t smem = static_cast<size_t>(mode != kPlain && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * block;
+    if (kNV == 1 && mode != kEdges) {
+        auto* pairs = mode == kPlain ? backward_pair_kernel<kPlain, Act, Res>
+                                     : backward_pair_kernel<kWhole, Act, Res>;
+        const size_t words = (mode == kPlain ? 6 : 8) + 2 * sizeof(Res) + 2 * sizeof(Act);
+        const size_t bytes = words * 16 * kThreads + static_cast<size_t>(G.groups) * 2 * 8 * kMaxWarps * 4;
+        if (bytes > 32 * 1024 && // beside the static words
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(pairs),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(bytes)) != cudaSuccess)
+            return ZERO_ECUDA;
+        pairs<<<grid, block, bytes, stream>>>(G, P, D, dy, du, y, h, dx, dh);
+        return cuda_status(cudaGetLastError());
+    }
+    size_t smem = static_cast<size_t>((mode != kPlain || kNV != 2) && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * kThreads;
     const size_t combine = static_cast<size_t>(G.groups) * G.dim * sizeof(float);
     if (G.groups > 1 && combine > smem) smem = combine;
-    auto* kernel = mode == kPlain   ? backward_kernel<kNV, kPlain, Act, Res>
-                   : mode == kWhole ? backward_kernel<kNV, kWhole, Act, Res>
-                                    : backward_kernel<kNV, kEdges, Act, Res>;
+    // several pieces a thread, or ragged ends: one row at a time (kEdges does
+    // what kWhole does; the sums' registers bound both)
+    constexpr int kP = kNV == 2 ? kPlain : kEdges;
+    auto* kernel = mode == kPlain ? backward_kernel<kNV, kP, Act, Res>
+                                  : backward_kernel<kNV, kEdges, Act, Res>;
     if (smem > 32 * 1024 && // beside the static words
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1065,9 +1505,12 @@ extern "C" int zero_block_norm_backward(const zero_block_norm_t* norm, const voi
     F.out[4] = grads->dgate;
     for (int i = 0; i < kVectors; ++i) F.type[i] = grads->grad_type;
     F.type[kVectors] = grads->dgate_type;
-    const int64_t tasks = D.vectors + (D.gate_rows > 1 ? D.gate_rows : 0);
-    const dim3 grid(static_cast<unsigned>((G.dim + 31) / 32),
-                    static_cast<unsigned>(tasks < 1024 ? tasks : 1024));
+    // gate rows of one token are final already
+    const int64_t workers = static_cast<int64_t>(G.blocks) * G.groups;
+    const int64_t tasks = D.vectors + (D.gate_rows > 1 && G.span > 1 ? workers - 1 : 0);
+    const bool four = G.dim % 4 == 0;
+    const dim3 grid(static_cast<unsigned>((G.dim + (four ? 127 : 31)) / (four ? 128 : 32)),
+                    static_cast<unsigned>(tasks));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(32 * kSlices);
@@ -1077,5 +1520,6 @@ extern "C" int zero_block_norm_backward(const zero_block_norm_t* norm, const voi
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, reduce_kernel, G, D, F));
+    return cuda_status(four ? cudaLaunchKernelEx(&cfg, reduce_kernel<4>, G, D, F)
+                            : cudaLaunchKernelEx(&cfg, reduce_kernel<1>, G, D, F));
 }
