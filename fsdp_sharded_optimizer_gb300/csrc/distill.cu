@@ -245,8 +245,16 @@ constexpr int kMaxRowWarps = 16;
 // How many exponentials a logit takes.
 //   kOne     one: temperature 1, or no labels
 //   kSquare  temperature 2: e^(x/2), and its square
+//   kFourth  temperature 4: e^(x/4), and its square's square
 //   kTwo     two
-enum Exps { kOne = 0, kSquare = 1, kTwo = 2 };
+enum Exps { kOne = 0, kSquare = 1, kFourth = 2, kTwo = 3 };
+
+// e^x of e^(x/T), where a product gives it.
+template <int kExps>
+__device__ __forceinline__ float power_of(float e)
+{
+    return kExps == kSquare ? e * e : (e * e) * (e * e);
+}
 
 template <typename T>
 struct Piece { // 16 bytes of a row
@@ -393,10 +401,10 @@ struct Scale {
     {
         return exp2_pair(dev::fma2(x, dev::pair(c), dev::pair(-ref)));
     }
-    // log of the sum of e^(x - m) / T, given the sum of the terms
-    __device__ __forceinline__ float log_of(float sum, float m) const
+    // log of the sum of the terms, each to the power `power`, relative to m
+    __device__ __forceinline__ float log_of(float sum, float m, int power = 1) const
     {
-        return fmaf(fmaf(m, c, -ref), -kLn2, logf(sum));
+        return fmaf(fmaf(m, c, -ref), -kLn2 * power, logf(sum));
     }
 };
 
@@ -531,6 +539,12 @@ row_kernel(const Args A, int ranks, int slots)
             continue; // the whole cluster does
         }
 
+        // the next row comes to the L2 meanwhile
+        if (kGrad && tid == 0 && then.to > then.from)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             then.row + then.lo + static_cast<int64_t>(then.from) * kE),
+                         "r"(16 * (then.to - then.from))
+                         : "memory");
         // pass 1: the maximum, and the sums relative to it
         float m = -INFINITY;
         float2 z1 = dev::pair(0.0f), z2 = z1;
@@ -542,6 +556,10 @@ row_kernel(const Args A, int ranks, int slots)
                 const float2 e2 = k2.exp2(x[e]);
                 z2 = dev::add2(z2, e2);
                 if (kExps == kSquare) z1 = dev::fma2(e2, e2, z1);
+                if (kExps == kFourth) {
+                    const float2 q = dev::mul2(e2, e2);
+                    z1 = dev::fma2(q, q, z1);
+                }
                 if (kExps == kTwo) z1 = dev::add2(z1, k1.exp2(x[e]));
             }
         };
@@ -550,7 +568,8 @@ row_kernel(const Args A, int ranks, int slots)
                 const float from2 = Scale(m, c2).ref, to2 = Scale(mx, c2).ref;
                 const float f2 = m == -INFINITY ? 0.0f : exp2_approx(from2 - to2);
                 z2 = dev::mul2(z2, dev::pair(f2));
-                if (kExps == kSquare) z1 = dev::mul2(z1, dev::pair(f2 * f2));
+                if (kExps == kSquare || kExps == kFourth)
+                    z1 = dev::mul2(z1, dev::pair(power_of<kExps>(f2)));
                 if (kExps == kTwo) {
                     const float from1 = Scale(m, kLog2e).ref, to1 = Scale(mx, kLog2e).ref;
                     z1 = dev::mul2(z1, dev::pair(m == -INFINITY ? 0.0f : exp2_approx(from1 - to1)));
@@ -634,9 +653,9 @@ row_kernel(const Args A, int ranks, int slots)
         if (m > -INFINITY) {
             const float f2 = exp2_approx(Scale(m, c2).ref - b2.ref);
             v[1] *= f2;
-            v[0] *= kExps == kSquare ? f2 * f2
-                    : kExps == kTwo  ? exp2_approx(Scale(m, kLog2e).ref - b1.ref)
-                                     : 0.0f;
+            v[0] *= kExps == kOne   ? 0.0f
+                    : kExps == kTwo ? exp2_approx(Scale(m, kLog2e).ref - b1.ref)
+                                    : power_of<kExps>(f2);
         }
         for (int k = tid; k < A.top; k += kThreadsOf) {
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
@@ -677,8 +696,8 @@ row_kernel(const Args A, int ranks, int slots)
                 const float rm = sh.ranks[parity][r][0];
                 // a part without anything above -inf holds 0, or NaN
                 const float f2 = rm == -INFINITY ? 1.0f : exp2_approx(Scale(rm, c2).ref - to2.ref);
-                const float f1 = kExps == kSquare ? f2 * f2
-                                 : kExps == kTwo && rm != -INFINITY
+                const float f1 = kExps != kTwo ? power_of<kExps>(f2)
+                                 : rm != -INFINITY
                                      ? exp2_approx(Scale(rm, kLog2e).ref - to1.ref)
                                      : 1.0f;
                 zs1 = fmaf(sh.ranks[parity][r][1], f1, zs1);
@@ -696,9 +715,8 @@ row_kernel(const Args A, int ranks, int slots)
         const bool has_label = labelled && !empty;
         if (rank == 0 && tid == 0) {
             const float from = row_m == -INFINITY ? 0.0f : row_m;
-            const float log1 = kExps == kOne      ? r2.log_of(zs1, from)
-                               : kExps == kSquare ? fmaf(fmaf(from, r2.c, -r2.ref), -2.0f * kLn2, logf(zs1))
-                                                  : r1.log_of(zs1, from);
+            const float log1 = kExps == kTwo ? r1.log_of(zs1, from)
+                                             : r2.log_of(zs1, from, 1 << kExps);
             A.ce[this_row] = has_label ? log1 - (s_label - from) : 0.0f;
             A.kl[this_row] = has_top ? A.tau * A.tau * (cross / zt + (r2.log_of(zs2, from) - logf(zt)))
                                      : 0.0f;
@@ -720,6 +738,10 @@ row_kernel(const Args A, int ranks, int slots)
                 if (kExps == kSquare) // (a1 e2 + a2) e2
                     return dev::mul2(dev::fma2(dev::pair(a1), e2, dev::pair(a2)), e2);
                 const float2 g = dev::mul2(e2, dev::pair(a2));
+                if (kExps == kFourth) {
+                    const float2 q = dev::mul2(e2, e2);
+                    return dev::fma2(dev::mul2(q, dev::pair(a1)), q, g);
+                }
                 return kExps == kTwo ? dev::fma2(r1.exp2(x), dev::pair(a1), g) : g;
             };
             const bool alike = ((reinterpret_cast<uintptr_t>(ds) ^ reinterpret_cast<uintptr_t>(s)) & 15) == 0;
@@ -814,17 +836,13 @@ row_kernel(const Args A, int ranks, int slots)
 }
 
 // Bytes of a row that a block should hold, and may hold.
-#ifndef PART_KB
-#define PART_KB 104
-#endif
-constexpr int64_t kPartBytes = PART_KB * 1024, kMostPartBytes = 192 * 1024;
+constexpr int64_t kPartBytes = 104 * 1024, kMostPartBytes = 192 * 1024;
 
-#ifndef WIDE_KB
-#define WIDE_KB 72
-#endif
-#ifndef WIDE_T
-#define WIDE_T 384
-#endif
+// Parts above this leave two blocks to an SM, below it three; two take more
+// threads.  Measured (8191 x 50257 bf16, device time): 100 KB parts with 256, 384
+// and 512 threads 360, 334 and 471 us; a part of 50 KB, two blocks to a row, 542:
+// an exchange between the blocks of a cluster waits for their stores.
+constexpr int64_t kWidePartBytes = 72 * 1024;
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
 {
@@ -866,7 +884,7 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
     const int64_t slots = (pieces + ranks - 1) / ranks;
     fits = slots * 16 <= kMostPartBytes;
     if (!fits) return ZERO_OK;
-    return slots * 16 > WIDE_KB * 1024 ? launch_rows<T, kGrad, kExps, WIDE_T>(A, ranks, slots, stream)
+    return slots * 16 > kWidePartBytes ? launch_rows<T, kGrad, kExps, 384>(A, ranks, slots, stream)
                                        : launch_rows<T, kGrad, kExps, 256>(A, ranks, slots, stream);
 }
 
@@ -876,6 +894,7 @@ int launch(const Args& A, cudaStream_t stream)
     bool fits = false;
     const int rc = !A.labels || A.tau == 1.0f ? launch_rows<T, kGrad, kOne>(A, stream, fits)
                    : A.tau == 2.0f            ? launch_rows<T, kGrad, kSquare>(A, stream, fits)
+                   : A.tau == 4.0f            ? launch_rows<T, kGrad, kFourth>(A, stream, fits)
                                               : launch_rows<T, kGrad, kTwo>(A, stream, fits);
     if (rc != ZERO_OK || fits) return rc;
     // a row that not even 8 blocks can hold is read twice

@@ -133,14 +133,6 @@ __device__ __forceinline__ float2 from_pair(unsigned long long a)
                        __uint_as_float(static_cast<uint32_t>(a >> 32)));
 }
 __device__ __forceinline__ float2 pair(float a) { return make_float2(a, a); }
-#ifdef SCALAR2
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
-#else
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     unsigned long long d;
@@ -159,7 +151,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_pair(a)), "l"(as_pair(b)));
     return from_pair(d);
 }
-#endif
 __device__ __forceinline__ void unpack8(const Raw8<Bf16>& r, float2 (&x)[4])
 {
     x[0] = make_float2(bf16_lo(r.a.x), bf16_hi(r.a.x));

@@ -141,7 +141,7 @@ def check(c, tau=1.0, cw=0.4, kw=0.6, weight=True, out_stride=None, in_place=Fal
     (6, 4097, 20, dict(offset=1)), (6, 4097, 20, dict(offset=3, logits="f32", stride=4111)),
     (3, 131072, 64, dict()), (2, 200003, 8, dict(logits="f32")), (2, 400001, 8, dict()),
     (160, 8200, 7, dict(stride=8208))])
-@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0])
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0, 4.0])
 def test_losses_and_gradient(R, V, K, kw, tau):
     check(make(R, V, K, **kw), tau)
 

@@ -1,7 +1,7 @@
 """The model operators together: examples/distill_student.py trains, and the
 gradients that its first pass writes to a rank's flat buffer agree with those of
 the same model in fp32 (torch autograd).  Activations and gradients of the
-example are bf16 (half an ulp 2^-9 of the larger neighbour, 2^-8 at most) and
+example are bf16 (half an ulp is 2^-9 to 2^-8 of a value) and
 pass about ten roundings one after the other, which add as random errors do:
 2^-8 * sqrt(10) = 0.012 of a tensor's norm, times 3 for the chains' differing
 lengths."""
