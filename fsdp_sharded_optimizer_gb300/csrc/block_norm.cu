@@ -448,6 +448,7 @@ struct Grads {
     int32_t dgate_type;
     int32_t gate_rows;   // 0: no dgate wanted
     int32_t vectors;     // sums over all rows: kVectors, and the gate's where it has one row
+    int32_t by_ends;     // how reduce_kernel finds the gate rows that workers share
     float* partial;
     float* gate_partial;
 };
@@ -1152,9 +1153,9 @@ backward_pair_kernel(const Geometry G, const Params P, const Grads D, const Res*
 }
 
 // Sums the blocks' partials, and those of the gate rows that several workers
-// share: blockIdx.y is one of the sums over all rows, or, from D.vectors on, the
-// end of a worker's run that lies inside a gate row (the first such end, where
-// the gate row spans more than two runs).  kVec columns a lane, kSlices threads
+// share: blockIdx.y is one of the sums over all rows, or, from D.vectors on, a
+// gate row, or (by_ends, where those are fewer) the end of a worker's run that
+// lies inside a gate row, the first such end of it.  kVec columns a lane, kSlices threads
 // each: a slice adds a run of the partials in order, the slices are added in order.
 constexpr int kSlices = 16;
 
@@ -1189,12 +1190,19 @@ reduce_kernel(const Geometry G, const Grads D, const Finals F)
         count = G.blocks;
         step = D.vectors * G.dim;
     } else {
-        const int64_t worker = task - D.vectors; // the worker before the end looked at
-        const int64_t end = (worker + 1) * G.run;
-        if (end >= G.rows || end % G.span == 0) return;
-        const int64_t q = end / G.span, from = q * G.span; // the gate row
-        if (from / G.run != worker) return; // it began before
-        const int64_t to = from + G.span < G.rows ? from + G.span : G.rows;
+        int64_t worker, q; // the gate row, and the first worker that has rows of it
+        if (D.by_ends) {
+            worker = task - D.vectors;
+            const int64_t end = (worker + 1) * G.run;
+            if (end >= G.rows || end % G.span == 0) return;
+            q = end / G.span;
+            if (q * G.span / G.run != worker) return; // it began before
+        } else {
+            q = task - D.vectors;
+            worker = q * G.span / G.run;
+        }
+        const int64_t to = (q + 1) * G.span < G.rows ? (q + 1) * G.span : G.rows;
+        if ((to - 1) / G.run == worker) return; // one worker's: final already
         // its first worker holds it as its last gate row, unless it is its first
         // too; the others as their first
         head = D.gate_partial + (2 * worker + (worker * G.run / G.span == q ? 0 : 1)) * G.dim;
@@ -1536,7 +1544,9 @@ extern "C" int zero_block_norm_backward(const zero_block_norm_t* norm, const voi
     F.type[kVectors] = grads->dgate_type;
     // gate rows of one token are final already
     const int64_t workers = static_cast<int64_t>(G.blocks) * G.groups;
-    const int64_t tasks = D.vectors + (D.gate_rows > 1 && G.span > 1 ? workers - 1 : 0);
+    const int64_t shared = D.gate_rows > 1 && G.span > 1 ? D.gate_rows : 0;
+    D.by_ends = shared > workers - 1;
+    const int64_t tasks = D.vectors + (D.by_ends ? workers - 1 : shared);
     const bool four = G.dim % 4 == 0;
     const dim3 grid(static_cast<unsigned>((G.dim + (four ? 127 : 31)) / (four ? 128 : 32)),
                     static_cast<unsigned>(tasks));
