@@ -19,11 +19,19 @@
 //
 // One group of warps holds a row in registers, 8 columns to a thread, reads
 // every tensor once and writes every result once: 4 row lengths forward, 6
-// backward, HBM-bound (and latency-bound for a few rows).  A thread keeps the
-// same columns for all rows of its group, so the sums over rows (dw, dc,
-// dgate) stay in its registers in fp32; the groups of a block are added in
-// shared memory, and the blocks, whose number depends on the sizes alone, by
-// reduce_kernel in order: the same bits in every run.
+// backward, so HBM bounds it if the exchanges between a row's warps are kept few
+// and other rows are under way meanwhile.  A thread keeps the same columns for
+// all rows of its group, so the sums over rows (dw, dc, dgate) stay in its
+// registers in fp32; the groups of a block are added in shared memory, and the
+// blocks, whose number depends on the sizes alone, by reduce_kernel in order:
+// the same bits in every run.
+//
+// Measured (device time, one GB300): forward 16384 x 4096 bf16 91 us, 5.9 TB/s, of
+// 345 us with one row's loads, weights and exchanges after another; backward
+// 16384 x 2048 with an fp32 residual 105 us, 5.8 TB/s (288 at first), 16384 x 4096
+// bf16 160 us; 8191 x 768 LayerNorm with biases 32 us, of which 11 are the two
+// launches, their first loads and the sums over blocks, and the rest is bound by
+// instructions (three exchanges a row); a single row 3.7 us forward.
 //
 // Rows whose length is no multiple of 8 start at every alignment.  A thread
 // then takes the 8 columns of an aligned 16-byte (bf16) or 32-byte (fp32)

@@ -14,6 +14,17 @@
 //
 // Both softmaxes have the same maximum m, so one pass over the row keeps it
 // and both sums of exponentials, rescaled when m grows.  Everything is fp32.
+// Read and written: the logits once and the gradient once, where the row stays
+// on the chip between the two (row_kernel); HBM bounds it as long as a logit
+// costs about ten instructions, an exponential per pass among them.
+//
+// Measured (device time, one GB300): 4096 x 32000 fp32, soft targets only, 164 us,
+// 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 172 us, 6.1 TB/s, at 1.5 with
+// labels 226 us (two exponentials a logit and pass); 8191 x 50257 bf16 at
+// temperature 2 317-322 us, 5.1 TB/s (100 KB a row: two blocks to an SM, whose
+// phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
+// 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
+// no cluster holds) took 255, 553 and 212 us for the first, third and last.
 //   kl = tau^2 * ( sum_k p_k ((t_k - tm) - (s_ik - m)) / tau + log Z - log Zt )
 // with Zt the teacher's sum: the large terms cancel before the products.
 #include "typed.cuh"

@@ -181,17 +181,21 @@ __device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int elem_bytes
         zero_elem(at);
 }
 
-// Sum over the block, valid in every thread.  `red` holds kPlanWarps + 1 words.
-__device__ __forceinline__ uint32_t block_total(uint32_t x, uint32_t* red)
+// An id as one word: those that are negative, or past 2^31, become 0xFFFFFFFF,
+// which no row has.
+__device__ __forceinline__ uint32_t id_word(int32_t id) { return id < 0 ? ~0u : static_cast<uint32_t>(id); }
+__device__ __forceinline__ uint32_t id_word(int64_t id)
+{
+    return (id >> 31) != 0 ? ~0u : static_cast<uint32_t>(id);
+}
+__device__ __forceinline__ uint32_t warp_inclusive(uint32_t x, int lane)
 {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    uint32_t total = 0;
-    for (int w = 0; w < kPlanWarps; ++w) total += red[w];
-    return total;
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, x, off);
+        if (lane >= off) x += n;
+    }
+    return x;
 }
 
 // A block owns rows [first, first + bins) of the vocabulary.  Warp w owns an
@@ -210,7 +214,7 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     extern __shared__ uint32_t hist[]; // [kPlanWarps][bins], then per row: first place, total
     uint32_t* firsts = hist + kPlanWarps * bins;
     uint32_t* totals = firsts + bins;
-    __shared__ uint32_t red[kPlanWarps + 1];
+    __shared__ uint32_t red[2][kPlanWarps]; // of each warp: tokens of lower rows, of its rows
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * bins;
@@ -218,25 +222,28 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     for (int i = tid; i < kPlanWarps * bins; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
 
-    const int64_t run = ((n_tokens + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
-    const int64_t lo = warp * run;
-    const int64_t hi = lo + run < n_tokens ? lo + run : n_tokens;
+    // n_tokens <= 2^30: places and tokens are 32-bit
+    const int tokens = static_cast<int>(n_tokens);
+    const int run = ((tokens + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const int lo = warp * run;
+    const int hi = tokens - lo < run ? tokens : lo + run; // at or below lo where nothing is left
+    const uint32_t base_row = static_cast<uint32_t>(first), rows = static_cast<uint32_t>(here);
     uint32_t* mine = hist + warp * bins;
     constexpr int kU = 8;
     uint32_t below = 0;
-    for (int64_t i = lo + lane; i < hi; i += 32 * kU) {
-        int64_t id[kU];
+    for (int i = lo + lane; i < hi; i += 32 * kU) {
+        uint32_t id[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            id[u] = i + 32 * u < hi ? static_cast<int64_t>(ids[i + 32 * u]) : -1;
+        for (int u = 0; u < kU; ++u) id[u] = i + 32 * u < hi ? id_word(ids[i + 32 * u]) : ~0u;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int64_t b = id[u] - first;
-            if (id[u] >= 0 && b < 0) ++below;
-            if (b >= 0 && b < here && id[u] >= 0) atomicAdd(&mine[b], 1u);
+            below += id[u] < base_row;
+            if (id[u] - base_row < rows) atomicAdd(&mine[id[u] - base_row], 1u);
         }
     }
-    const uint32_t base = block_total(below, red);
+    below = __reduce_add_sync(0xFFFFFFFFu, below);
+    if (lane == 0) red[0][warp] = below;
+    __syncthreads();
 
     // the row's total, and its first place: kPlanMaxBins rows at most, one per thread
     uint32_t total = 0;
@@ -244,17 +251,12 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
 #pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) total += hist[w * bins + tid];
     }
-    uint32_t incl = total;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-        if (lane >= off) incl += n;
-    }
+    const uint32_t incl = warp_inclusive(total, lane);
+    if (lane == 31) red[1][warp] = incl;
     __syncthreads();
-    if (lane == 31) red[warp] = incl;
-    __syncthreads();
-    uint32_t start = base + incl - total;
-    for (int w = 0; w < warp; ++w) start += red[w];
+    const uint32_t base = __reduce_add_sync(0xFFFFFFFFu, red[0][lane]);
+    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? red[1][lane] : 0u);
+    const uint32_t start = base + before + incl - total;
     const uint32_t none = __ballot_sync(0xFFFFFFFFu, tid < here && total == 0);
     if (lane == 0 && tid < here) empty[(first + tid) / 32] = none;
     if (tid < here) {
@@ -278,22 +280,22 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
     }
     __syncthreads();
 
-    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kU) {
-        int64_t id[kU];
+    for (int i0 = lo; i0 < hi; i0 += 32 * kU) {
+        uint32_t id[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int64_t i = i0 + 32 * u + lane;
-            id[u] = i < hi ? static_cast<int64_t>(ids[i]) : -1;
+            const int i = i0 + 32 * u + lane;
+            id[u] = i < hi ? id_word(ids[i]) : ~0u;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int64_t b = id[u] - first;
-            const bool in = id[u] >= 0 && b >= 0 && b < here;
+            const uint32_t b = id[u] - base_row;
+            const bool in = b < rows;
             const uint32_t any = __ballot_sync(0xFFFFFFFFu, in);
             if (any == 0) continue;
             uint32_t peers = 0, place = 0;
             if (in) {
-                peers = __match_any_sync(any, static_cast<int>(b));
+                peers = __match_any_sync(any, b);
                 place = mine[b];
             }
             __syncwarp();
@@ -301,9 +303,8 @@ plan_kernel(const Id* __restrict__ ids, int64_t n_tokens, int64_t vocab, int bin
                 const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
                 if (rank == 0) mine[b] = place + __popc(peers);
                 const int at = static_cast<int>(firsts[b]);
-                sorted[place + rank] =
-                    make_int4(static_cast<int>(i0 + 32 * u + lane), static_cast<int>(id[u]), at,
-                              at + static_cast<int>(totals[b]));
+                sorted[place + rank] = make_int4(i0 + 32 * u + lane, static_cast<int>(id[u]), at,
+                                                 at + static_cast<int>(totals[b]));
             }
             __syncwarp();
         }
