@@ -21,7 +21,7 @@
 // Measured (device time, one GB300): 4096 x 32000 fp32, soft targets only, 164 us,
 // 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 172 us, 6.1 TB/s, at 1.5 with
 // labels 226 us (two exponentials a logit and pass); 8191 x 50257 bf16 at
-// temperature 2 317-322 us, 5.1 TB/s (100 KB a row: two blocks to an SM, whose
+// temperature 2 307 us, 5.4 TB/s (100 KB a row: two blocks to an SM, whose
 // phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
 // 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
 // no cluster holds) took 255, 553 and 212 us for the first, third and last.
@@ -896,8 +896,10 @@ row_kernel(const Args A, int ranks, int slots)
 constexpr int64_t kPartBytes = 104 * 1024, kMostPartBytes = 192 * 1024;
 
 // Parts above this leave two blocks to an SM, below it three; two take more
-// threads.  Measured (8191 x 50257 bf16, device time): 100 KB parts with 256, 384
-// and 512 threads 360, 334 and 471 us.
+// threads.  Measured with 256, 320 and 384 threads (8192 rows, device time): 38000
+// bf16 logits at temperature 2 262, 248 and 264 us, 48000 at 1 273, 267 and 281,
+// 24000 fp32 245, 237 and 248; 8191 x 50257 bf16 at 2 with 320, 352, 384, 416 and
+// 448 threads 307, 329, 322, 358 and 354.
 constexpr int64_t kWidePartBytes = 72 * 1024;
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
@@ -940,7 +942,7 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
     const int64_t slots = (pieces + ranks - 1) / ranks;
     fits = slots * 16 <= kMostPartBytes;
     if (!fits) return ZERO_OK;
-    return slots * 16 > kWidePartBytes ? launch_rows<T, kGrad, kExps, 384>(A, ranks, slots, stream)
+    return slots * 16 > kWidePartBytes ? launch_rows<T, kGrad, kExps, 320>(A, ranks, slots, stream)
                                        : launch_rows<T, kGrad, kExps, 256>(A, ranks, slots, stream);
 }
 

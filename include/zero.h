@@ -798,7 +798,7 @@ const char* zero_strerror(int code);
  *    only (ZERO_EALIGN otherwise); wide loads are used where addresses allow.
  *  - All arithmetic and all sums are fp32; an output of bf16 is rounded once,
  *    to nearest even.  Sums have a fixed order: the same call on the same
- *    inputs gives the same bits.
+ *    inputs, at the same alignment to 16 bytes, gives the same bits.
  *  - Scratch is the caller's, 16-byte aligned, of the size the *_scratch_bytes
  *    call gives; calls that share it must be ordered.  Its contents need not
  *    be kept from one call to the next.

@@ -1,7 +1,7 @@
 """The model operators as a program uses them: in a CUDA graph with other
 launches, and on tensors whose offsets pass 2^31 elements (compared, bit for
-bit, with the same rows on their own: a row's result does not depend on where
-it lies or on how many rows there are)."""
+bit, with the same rows on their own, at the same alignment to 16 bytes, on which
+the order of a loss's sums depends)."""
 import pytest
 import torch
 
@@ -100,7 +100,10 @@ def test_distillation_past_2_31_elements():
     B.zero_distill_forward_backward(x, tl, ti, ce, kl, x, temperature=2.0)
     # the same split of a row over blocks as with many rows: 20 rows alone would
     # use more blocks a row, and another order of the sums
-    many = tail.repeat(8, 1)
+    shift = x[-20].data_ptr() % 16 // 2
+    many = torch.empty(160 * V + 8, dtype=torch.bfloat16, device="cuda")[shift:shift + 160 * V]
+    many = many.view(160, V)
+    many.copy_(tail.repeat(8, 1))
     a, b = (torch.empty(160, device="cuda") for _ in range(2))
     B.zero_distill_forward_backward(many, tl[-20:].repeat(8, 1), ti[-20:].repeat(8, 1), a, b, many,
                                     temperature=2.0)
