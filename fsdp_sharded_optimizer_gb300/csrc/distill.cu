@@ -19,8 +19,8 @@
 // costs about ten instructions, an exponential per pass among them.
 //
 // Measured (device time, one GB300): 4096 x 32000 fp32, soft targets only, 164 us,
-// 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 172 us, 6.1 TB/s, at 1.5 with
-// labels 226 us (two exponentials a logit and pass); 8191 x 50257 bf16 at
+// 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 175 us, 6.0 TB/s, at 1.5 with
+// labels 213 us (two exponentials a logit and pass); 8191 x 50257 bf16 at
 // temperature 2 307 us, 5.4 TB/s (100 KB a row: two blocks to an SM, whose
 // phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
 // 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
@@ -457,7 +457,7 @@ struct Scale {
 };
 
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
-__global__ void __launch_bounds__(kThreadsOf, kThreadsOf == 256 ? 3 : 2)
+__global__ void __launch_bounds__(kThreadsOf, kThreadsOf == 128 ? 5 : kThreadsOf == 160 ? 3 : 2)
 row_kernel(const Args A, int ranks, int slots)
 {
     constexpr int kE = Piece<T>::kElems, kP = Piece<T>::kPairs;
@@ -895,12 +895,13 @@ row_kernel(const Args A, int ranks, int slots)
 // power of two: 2000 x 131072 bf16 takes 340 us on 3 ranks, 267 on 4.
 constexpr int64_t kPartBytes = 104 * 1024, kMostPartBytes = 192 * 1024;
 
-// Parts above this leave two blocks to an SM, below it three; two take more
-// threads.  Measured with 256, 320 and 384 threads (8192 rows, device time): 38000
-// bf16 logits at temperature 2 262, 248 and 264 us, 48000 at 1 273, 267 and 281,
-// 24000 fp32 245, 237 and 248; 8191 x 50257 bf16 at 2 with 320, 352, 384, 416 and
-// 448 threads 307, 329, 322, 358 and 354.
-constexpr int64_t kWidePartBytes = 72 * 1024;
+// Five blocks with parts up to the first of these fit an SM, three up to the second,
+// then two; the more threads they have.  Measured (8192 rows bf16, device time): 20000
+// logits at temperature 2 with 128, 160 and 256 threads 120, 128 and 153 us; 32000 at
+// temperature 1 with 128, 160 and 256 187, 175 and 179, at 1.5 223, 213 and 228; with
+// 256, 320 and 384 threads 38000 at 2 262, 248 and 264, 48000 at 1 273, 267 and 281,
+// 24000 fp32 245, 237 and 248.
+constexpr int64_t kSmallPartBytes = 43 * 1024, kWidePartBytes = 72 * 1024;
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
 {
@@ -942,8 +943,10 @@ int launch_rows(const Args& A, cudaStream_t stream, bool& fits)
     const int64_t slots = (pieces + ranks - 1) / ranks;
     fits = slots * 16 <= kMostPartBytes;
     if (!fits) return ZERO_OK;
-    return slots * 16 > kWidePartBytes ? launch_rows<T, kGrad, kExps, 320>(A, ranks, slots, stream)
-                                       : launch_rows<T, kGrad, kExps, 256>(A, ranks, slots, stream);
+    if (slots * 16 > kWidePartBytes)
+        return launch_rows<T, kGrad, kExps, 320>(A, ranks, slots, stream);
+    return slots * 16 > kSmallPartBytes ? launch_rows<T, kGrad, kExps, 160>(A, ranks, slots, stream)
+                                        : launch_rows<T, kGrad, kExps, 128>(A, ranks, slots, stream);
 }
 
 template <typename T, bool kGrad>
