@@ -25,8 +25,11 @@
 // phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
 // 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
 // no cluster holds) took 255, 553 and 212 us for the first, third and last.
-//   kl = tau^2 * ( sum_k p_k ((t_k - tm) - (s_ik - m)) / tau + log Z - log Zt )
-// with Zt the teacher's sum: the large terms cancel before the products.
+//   kl = tau^2 * ( sum_k p_k ((t_k - tm) - (s_ik - so)) / tau + (m - so) / tau + log Z - log Zt )
+// with Zt the teacher's sum and so the student's largest logit at a counted entry:
+// every block of a row can form the sum about it before it knows the row's maximum m,
+// and neither so - s_ik nor m - so is negative, so that nothing cancels, however far
+// below m the logits of a block's own part lie.  One block alone takes so = m.
 #include "typed.cuh"
 #include "zero_internal.h"
 
@@ -573,7 +576,7 @@ row_kernel(const Args A, int ranks, int slots)
         const int64_t lo = now.lo, hi = lo + static_cast<int64_t>(n) * kE;
         // the student's logits at the label and at entry tid, then the next row's
         const bool labelled = this_label >= 0 && this_label < vocab;
-        float s_label = 0.0f, my_s = 0.0f;
+        float s_label = 0.0f, my_s = -INFINITY; // -inf: not counted
         if (this_w != 0.0f) {
             if (labelled) s_label = dev::load1(s + this_label);
             if (this_id >= 0) my_s = dev::load1(s + this_id);
@@ -677,7 +680,7 @@ row_kernel(const Args A, int ranks, int slots)
             float t = this_t, at = my_s;
             if (k != tid) {
                 entry_of(this_row, k, id, t);
-                at = id >= 0 ? dev::load1(s + id) : 0.0f;
+                at = id >= 0 ? dev::load1(s + id) : -INFINITY;
             }
             tm = fmaxf(tm, t);
             top_id[k] = id;
@@ -700,7 +703,13 @@ row_kernel(const Args A, int ranks, int slots)
         block_m = warp_max(sh.most[0][lane % kMaxRowWarps]);
         tm = warp_max(sh.most[1][lane % kMaxRowWarps]);
         const Scale b1(block_m, kLog2e), b2(block_m, c2);
-        const float base = block_m == -INFINITY ? 0.0f : block_m;
+        float sbase = block_m;
+        if (ranks > 1) {
+            sbase = -INFINITY;
+            for (int k = lane; k < A.top; k += 32) sbase = fmaxf(sbase, top_s[k]);
+            sbase = warp_max(sbase);
+        }
+        if (sbase == -INFINITY) sbase = 0.0f;
         const float tbase = tm == -INFINITY ? 0.0f : tm;
         // its sums
         float v[4] = {z1.x + z1.y, z2.x + z2.y, 0.0f, 0.0f};
@@ -715,7 +724,7 @@ row_kernel(const Args A, int ranks, int slots)
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
             v[2] += e;
             if (e != 0.0f)
-                v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - base)) * inv_tau, v[3]);
+                v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - sbase)) * inv_tau, v[3]);
             top_p[k] = e;
         }
         const bool marked = kGrad && labelled && this_label >= lo && this_label < hi &&
@@ -757,7 +766,7 @@ row_kernel(const Args A, int ranks, int slots)
                 zs2 = fmaf(sh.ranks[parity][r].z, f2, zs2);
             }
             if (!here_all) zs1 = zs2 = __int_as_float(0x7FC00000);
-            if (row_m > -INFINITY) cross = fmaf(zt, (row_m - base) * inv_tau, cross);
+            if (row_m > -INFINITY) cross = fmaf(zt, (row_m - sbase) * inv_tau, cross);
             parity ^= 1;
         }
         if (kExps == kOne) zs1 = zs2;
