@@ -436,28 +436,90 @@ __device__ __forceinline__ bool wait_phase(uint32_t barrier, uint32_t phase)
     return false;
 }
 
-// 2^(x c - m c) for a row's, or a thread's, maximum m.  The reference m c is
-// rounded once and the product inside the fma is not, so the terms agree to
-// rounding; what the reference was off by is taken out of the sum's logarithm.
-// c is 1 where m c might overflow: there only logits equal to m have a term
-// that is not 0, whatever c is.
+// 2^(x c - m c) for a thread's maximum m so far.  The reference m c is rounded once
+// and the product inside the fma is not, so the terms agree to rounding; what the
+// reference was off by, at most 1, is taken out of the sum's logarithm.  Where |m c|
+// is above 2^24 (a mask value, mostly; or m is -inf) it would be off by any amount, or
+// out of range: there the terms are only kept finite, and count for nothing.  A
+// thread's sum is used, times its factor, where the row's maximum is below half of
+// that, and then each of those logits is at least 2^23 below it.
+constexpr float kFar = 16777216.0f;
 struct Scale {
     float c, ref;
+    bool far;
     __device__ __forceinline__ Scale(float m, float factor)
     {
-        c = fabsf(m) > 1e38f ? 1.0f : factor;
-        ref = m == -INFINITY ? 0.0f : m * c;
+        far = fabsf(m) * factor > kFar;
+        c = far ? 0x1p-126f : factor;
+        ref = far ? 0.0f : m * factor;
     }
     __device__ __forceinline__ float2 exp2(float2 x) const
     {
         return exp2_pair(dev::fma2(x, dev::pair(c), dev::pair(-ref)));
     }
-    // log of the sum of the terms, each to the power `power`, relative to m
-    __device__ __forceinline__ float log_of(float sum, float m, int power = 1) const
+    // the factor that takes a sum relative to this to one relative to `ref`
+    __device__ __forceinline__ float to(float ref_there) const
     {
-        return fmaf(fmaf(m, c, -ref), -kLn2 * power, logf(sum));
+        return far ? 0.0f : exp2_approx(ref - ref_there);
     }
 };
+
+// The same for the maximum of a block's part or of the row.  Where |m c| is above
+// 2^23 (far) the terms are 2^((x - m) c), x - m exact wherever that is not 0: an
+// operation more, and outside the loops that all rows go through.
+struct RowScale {
+    float m, c, ref;
+    bool far;
+    __device__ __forceinline__ RowScale(float most, float factor)
+    {
+        m = most == -INFINITY ? 0.0f : most; // nothing above -inf: every term is 0
+        c = factor;
+        far = fabsf(m) * factor > kFar / 2;
+        ref = far ? 0.0f : m * factor;
+    }
+    __device__ __forceinline__ float2 exp2(float2 x) const // where not far
+    {
+        return exp2_pair(dev::fma2(x, dev::pair(c), dev::pair(-ref)));
+    }
+    __device__ __forceinline__ float exp2_any(float x) const
+    {
+        return exp2_approx(fmaf(x - (far ? m : 0.0f), c, -ref));
+    }
+    __device__ __forceinline__ float off() const { return far ? 0.0f : fmaf(m, c, -ref); }
+    // the factor that takes a sum relative to this to one relative to `there`
+    __device__ __forceinline__ float to(const RowScale& there) const
+    {
+        return exp2_approx(fmaf(m - there.m, c, there.off() - off()));
+    }
+    // log of the sum of the terms, each to the power `power`, relative to m
+    __device__ __forceinline__ float log_of(float sum, int power = 1) const
+    {
+        return fmaf(off(), -kLn2 * power, logf(sum));
+    }
+};
+
+// Columns [from, to) of a row with a far maximum m, read again: its sums, and its
+// gradient a1 2^((x - m) c1) + a2 2^((x - m) c2).
+template <typename T>
+__device__ __noinline__ float2 far_sums(const T* s, int64_t from, int64_t to, float m, float c1, float c2)
+{
+    float2 z = make_float2(0.0f, 0.0f);
+    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x) {
+        const float d = dev::load1(s + i) - m;
+        z.x += exp2_approx(d * c1);
+        z.y += exp2_approx(d * c2);
+    }
+    return z;
+}
+template <typename T>
+__device__ __noinline__ void far_gradient(const T* s, T* ds, int64_t from, int64_t to, float m, float c1,
+                                          float c2, float a1, float a2)
+{
+    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x) {
+        const float d = dev::load1(s + i) - m;
+        dev::store1(ds + i, fmaf(a1, exp2_approx(d * c1), a2 * exp2_approx(d * c2)));
+    }
+}
 
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 __global__ void __launch_bounds__(kThreadsOf, kThreadsOf == 128 ? 5 : kThreadsOf == 160 ? 3 : 2)
@@ -622,15 +684,12 @@ row_kernel(const Args A, int ranks, int slots)
         };
         auto raise = [&](float mx) { // a larger maximum: the sums so far shrink
             if (mx > m) {
-                const float from2 = Scale(m, c2).ref, to2 = Scale(mx, c2).ref;
-                const float f2 = m == -INFINITY ? 0.0f : exp2_approx(from2 - to2);
+                const float f2 = Scale(m, c2).to(Scale(mx, c2).ref);
                 z2 = dev::mul2(z2, dev::pair(f2));
                 if (kExps == kSquare || kExps == kFourth)
                     z1 = dev::mul2(z1, dev::pair(power_of<kExps>(f2)));
-                if (kExps == kTwo) {
-                    const float from1 = Scale(m, kLog2e).ref, to1 = Scale(mx, kLog2e).ref;
-                    z1 = dev::mul2(z1, dev::pair(m == -INFINITY ? 0.0f : exp2_approx(from1 - to1)));
-                }
+                if (kExps == kTwo)
+                    z1 = dev::mul2(z1, dev::pair(Scale(m, kLog2e).to(Scale(mx, kLog2e).ref)));
                 m = mx;
             }
         };
@@ -702,7 +761,7 @@ row_kernel(const Args A, int ranks, int slots)
         twice = __syncthreads_or(twice);
         block_m = warp_max(sh.most[0][lane % kMaxRowWarps]);
         tm = warp_max(sh.most[1][lane % kMaxRowWarps]);
-        const Scale b1(block_m, kLog2e), b2(block_m, c2);
+        const RowScale b1(block_m, kLog2e), b2(block_m, c2);
         float sbase = block_m;
         if (ranks > 1) {
             sbase = -INFINITY;
@@ -713,11 +772,15 @@ row_kernel(const Args A, int ranks, int slots)
         const float tbase = tm == -INFINITY ? 0.0f : tm;
         // its sums
         float v[4] = {z1.x + z1.y, z2.x + z2.y, 0.0f, 0.0f};
-        if (m > -INFINITY) {
-            const float f2 = exp2_approx(Scale(m, c2).ref - b2.ref);
+        if (b2.far || (kExps == kTwo && b1.far)) {
+            const float2 z = far_sums(s, lo < 0 ? 0 : lo, hi < vocab ? hi : vocab, b2.m, kLog2e, c2);
+            v[0] = kExps == kTwo ? z.x * exp2_approx(b1.off()) : z.x;
+            v[1] = z.y * exp2_approx(b2.off());
+        } else { // a thread without anything above -inf has 0, or NaN
+            const float f2 = Scale(m, c2).to(b2.ref);
             v[1] *= f2;
             v[0] *= kExps == kOne   ? 0.0f
-                    : kExps == kTwo ? exp2_approx(Scale(m, kLog2e).ref - b1.ref)
+                    : kExps == kTwo ? Scale(m, kLog2e).to(b1.ref)
                                     : power_of<kExps>(f2);
         }
         for (int k = tid; k < A.top; k += kThreadsOf) {
@@ -752,16 +815,15 @@ row_kernel(const Args A, int ranks, int slots)
             const bool here_all = wait_phase(barrier, phase >> parity & 1);
             phase ^= 1u << parity;
             for (int r = 0; r < ranks; ++r) row_m = fmaxf(row_m, sh.ranks[parity][r].x);
-            const Scale to1(row_m, kLog2e), to2(row_m, c2);
+            const RowScale to1(row_m, kLog2e), to2(row_m, c2);
             zs1 = zs2 = 0.0f;
             for (int r = 0; r < ranks; ++r) {
                 const float rm = sh.ranks[parity][r].x;
                 // a part without anything above -inf holds 0, or NaN
-                const float f2 = rm == -INFINITY ? 1.0f : exp2_approx(Scale(rm, c2).ref - to2.ref);
-                const float f1 = kExps != kTwo ? power_of<kExps>(f2)
-                                 : rm != -INFINITY
-                                     ? exp2_approx(Scale(rm, kLog2e).ref - to1.ref)
-                                     : 1.0f;
+                const float f2 = rm == -INFINITY ? 1.0f : RowScale(rm, c2).to(to2);
+                const float f1 = kExps != kTwo     ? power_of<kExps>(f2)
+                                 : rm != -INFINITY ? RowScale(rm, kLog2e).to(to1)
+                                                   : 1.0f;
                 zs1 = fmaf(sh.ranks[parity][r].y, f1, zs1);
                 zs2 = fmaf(sh.ranks[parity][r].z, f2, zs2);
             }
@@ -770,7 +832,7 @@ row_kernel(const Args A, int ranks, int slots)
             parity ^= 1;
         }
         if (kExps == kOne) zs1 = zs2;
-        const Scale r1(row_m, kLog2e), r2(row_m, c2);
+        const RowScale r1(row_m, kLog2e), r2(row_m, c2);
         // a row whose logits are all -inf has no distribution, a teacher whose
         // counted entries are all -inf (or none) has none either; a NaN is neither
         const bool empty = zs2 == 0.0f;
@@ -778,10 +840,9 @@ row_kernel(const Args A, int ranks, int slots)
         const bool has_label = labelled && !empty;
         if (rank == 0 && tid == 0) {
             const float from = row_m == -INFINITY ? 0.0f : row_m;
-            const float log1 = kExps == kTwo ? r1.log_of(zs1, from)
-                                             : r2.log_of(zs1, from, 1 << kExps);
+            const float log1 = kExps == kTwo ? r1.log_of(zs1) : r2.log_of(zs1, 1 << kExps);
             A.ce[this_row] = has_label ? log1 - (s_label - from) : 0.0f;
-            A.kl[this_row] = has_top ? A.tau * A.tau * (cross / zt + (r2.log_of(zs2, from) - logf(zt)))
+            A.kl[this_row] = has_top ? A.tau * A.tau * (cross / zt + (r2.log_of(zs2) - logf(zt)))
                                      : 0.0f;
         }
         if constexpr (kGrad) {
@@ -796,8 +857,7 @@ row_kernel(const Args A, int ranks, int slots)
             float a2 = has_top ? __fdividef(pull, zs2) : 0.0f;
             if (kExps == kOne) a2 += a1;
             const bool has_any = has_top || has_label; // else +0, whatever the logits are
-            auto dense = [&](float2 x) {
-                const float2 e2 = r2.exp2(x);
+            auto combine = [&](float2 e2, auto e1) {
                 if (kExps == kSquare) // (a1 e2 + a2) e2
                     return dev::mul2(dev::fma2(dev::pair(a1), e2, dev::pair(a2)), e2);
                 const float2 g = dev::mul2(e2, dev::pair(a2));
@@ -805,8 +865,15 @@ row_kernel(const Args A, int ranks, int slots)
                     const float2 q = dev::mul2(e2, e2);
                     return dev::fma2(dev::mul2(q, dev::pair(a1)), q, g);
                 }
-                return kExps == kTwo ? dev::fma2(r1.exp2(x), dev::pair(a1), g) : g;
+                return kExps == kTwo ? dev::fma2(e1(), dev::pair(a1), g) : g;
             };
+            auto dense = [&](float2 x) { // where the row is not far
+                return combine(r2.exp2(x), [&] { return r1.exp2(x); });
+            };
+            auto dense1 = [&](float x) {
+                return combine(dev::pair(r2.exp2_any(x)), [&] { return dev::pair(r1.exp2_any(x)); }).x;
+            };
+            const bool far = r2.far || (kExps == kTwo && r1.far);
             const bool alike = ((reinterpret_cast<uintptr_t>(ds) ^ reinterpret_cast<uintptr_t>(s)) & 15) == 0;
             // slots that are written 16 bytes at once
             const int wide_from = alike ? now.from : n, wide_to = alike ? now.to : n;
@@ -832,10 +899,15 @@ row_kernel(const Args A, int ranks, int slots)
                     fetch_whole(part_at, then, j);
                 }
             }
+            const int end = far ? 0 : n;
+            if (far && has_any)
+                far_gradient(s, ds, lo < 0 ? 0 : lo, hi < vocab ? hi : vocab, r2.m, kLog2e, c2,
+                             kExps == kOne ? 0.0f : kExps == kTwo ? a1 * exp2_approx(r1.off()) : a1,
+                             a2 * exp2_approx(r2.off()));
             // whole batches: nothing of them at the ends, of this row or the next
             const int first = now.from > then.from ? now.from : then.from;
             int batches = wide_to < then.to || then.to == 0 ? wide_to : then.to;
-            if (!alike) batches = 0;
+            if (!alike || far) batches = 0;
             for (; j + kStep - kThreadsOf < batches; j += kStep) {
                 at_slot(j);
                 uint4 raw[kBatch];
@@ -858,7 +930,7 @@ row_kernel(const Args A, int ranks, int slots)
                     }
                 }
             }
-            for (; j < n; j += kThreadsOf) {
+            for (; j < end; j += kThreadsOf) {
                 float2 x[kP];
                 unpack_piece(part[j], x, T());
 #pragma unroll
@@ -870,7 +942,7 @@ row_kernel(const Args A, int ranks, int slots)
             fetch_from(then, j);
             __syncthreads(); // before the teacher's entries are written over
             if (has_label && !marked && tid == 0 && this_label >= lo && this_label < hi)
-                dev::store1(ds + this_label, dense(dev::pair(s_label)).x - hit);
+                dev::store1(ds + this_label, dense1(s_label) - hit);
             for (int k = tid; k < A.top; k += kThreadsOf) {
                 const int32_t id = top_id[k];
                 if (id < lo || id >= hi || id < 0) continue; // not counted, or another rank's
@@ -885,7 +957,7 @@ row_kernel(const Args A, int ranks, int slots)
                     }
                     if (!first_of) continue;
                 }
-                float g = has_any ? fmaf(-share, p, dense(dev::pair(top_s[k])).x) : 0.0f;
+                float g = has_any ? fmaf(-share, p, dense1(top_s[k])) : 0.0f;
                 if (id == this_label) g -= hit;
                 dev::store1(ds + id, g);
             }
