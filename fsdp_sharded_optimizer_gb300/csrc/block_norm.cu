@@ -614,7 +614,8 @@ backward_kernel(const Geometry G, const Params P, const Grads D, const Res* __re
         if (P.pre) {
             const float rstd = rsqrtf(fmaf(s[0], inv, P.eps));
             const float2 r = dev::pair(rstd);
-            const float2 k = dev::pair(-rstd * rstd * rstd * s[1] * inv); // -r^2 mean(du w y^)
+            // -r^2 mean(du w y^); a row of zeros has 0, though r^3 may be out of range
+            const float2 k = dev::pair(-rstd * (rstd * (rstd * (s[1] * inv))));
 #pragma unroll
             for (int i = 0; i < kNV; ++i) {
                 const float2 k0 = dev::pair(kMode == kEdges || c.full[i] ? -rstd * m0 : 0.0f);
@@ -1047,7 +1048,9 @@ backward_pair_kernel(const Geometry G, const Params P, const Grads D, const Res*
             for (int r = 0; r < 2; ++r) {
                 const float rstd = rsqrtf(fmaf(s[r], inv, P.eps));
                 const float2 rr = dev::pair(rstd);
-                const float2 k = dev::pair(-rstd * rstd * rstd * s[2 + r] * inv); // -r^2 mean(du w y^)
+                // -r^2 mean(du w y^); a row of zeros, or no second row, has 0, though
+                // r^3 may be out of range
+                const float2 k = dev::pair(-rstd * (rstd * (rstd * (s[2 + r] * inv))));
                 const float2 k0 = dev::pair(full ? -rstd * m0[r] : 0.0f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
