@@ -1414,28 +1414,23 @@ int start_backward(const Geometry& G, const Params& P, const Grads& D, bool full
         auto* pairs = mode == kPlain ? backward_pair_kernel<kPlain, Act, Res>
                                      : backward_pair_kernel<kWhole, Act, Res>;
         const size_t words = (mode == kPlain ? 6 : 8) + 2 * sizeof(Res) + 2 * sizeof(Act);
-        const size_t bytes = words * 16 * kThreads + static_cast<size_t>(G.groups) * 2 * 8 * kMaxWarps * 4;
-        if (bytes > 32 * 1024 && // beside the static words
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(pairs),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(bytes)) != cudaSuccess)
-            return ZERO_ECUDA;
+        auto bytes_of = [&](int groups) {
+            return words * 16 * kThreads + static_cast<size_t>(groups) * 2 * 8 * kMaxWarps * 4;
+        };
+        const size_t bytes = bytes_of(G.groups);
+        if (!allow_shared(reinterpret_cast<const void*>(pairs), bytes_of(kMaxWarps))) return ZERO_ECUDA;
         pairs<<<grid, block, bytes, stream>>>(G, P, D, dy, du, y, h, dx, dh);
         return cuda_status(cudaGetLastError());
     }
-    size_t smem = static_cast<size_t>((mode != kPlain || kNV != 2) && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * kThreads;
-    const size_t combine = static_cast<size_t>(G.groups) * G.dim * sizeof(float);
-    if (G.groups > 1 && combine > smem) smem = combine;
+    // one size for each kernel; the groups' sums at the end (G.groups x G.dim, where a
+    // thread has one piece: 16 KB at most) fit into it
+    const size_t smem = static_cast<size_t>((mode != kPlain || kNV != 2) && kBiasSlot<kNV> ? 4 : 3) * kNV * 32 * kThreads;
     // several pieces a thread, or ragged ends: one row at a time (kEdges does
     // what kWhole does; the sums' registers bound both)
     constexpr int kP = kNV == 2 ? kPlain : kEdges;
     auto* kernel = mode == kPlain ? backward_kernel<kNV, kP, Act, Res>
                                   : backward_kernel<kNV, kEdges, Act, Res>;
-    if (smem > 32 * 1024 && // beside the static words
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return ZERO_ECUDA;
+    if (!allow_shared(reinterpret_cast<const void*>(kernel), smem)) return ZERO_ECUDA;
     kernel<<<grid, block, smem, stream>>>(G, P, D, dy, du, y, h, dx, dh);
     return cuda_status(cudaGetLastError());
 }

@@ -986,14 +986,13 @@ constexpr int64_t kSmallPartBytes = 43 * 1024, kWidePartBytes = 72 * 1024;
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
 {
-    const size_t smem = static_cast<size_t>(slots) * 16 + static_cast<size_t>(A.top) * 12 +
-                        (kGrad ? (slots * Piece<T>::kElems + 31) / 32 * 4 : 0);
+    auto smem_of = [](int64_t n_slots, int64_t top) {
+        return static_cast<size_t>(n_slots * 16 + top * 12 + (kGrad ? (n_slots * Piece<T>::kElems + 31) / 32 * 4 : 0));
+    };
+    const size_t smem = smem_of(slots, A.top);
     auto* kernel = row_kernel<T, kGrad, kExps, kThreadsOf>;
     const void* k = reinterpret_cast<const void*>(kernel);
-    if (smem > 32 * 1024 &&
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return ZERO_ECUDA;
+    if (smem > 32 * 1024 && !allow_shared(k, smem_of(kMostPartBytes / 16, kMaxTop))) return ZERO_ECUDA;
     const int resident = persistent_blocks(k, kThreadsOf, smem);
     if (resident < 1) return ZERO_ECUDA;
     int64_t clusters = resident / ranks;

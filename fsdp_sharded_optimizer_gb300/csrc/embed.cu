@@ -107,6 +107,10 @@ constexpr int kPlanThreads = kPlanWarps * 32;
 constexpr int kPlanMaxBins = 1024; // rows of the vocabulary a block owns, at most
 constexpr int kPlanBlocks = 152;   // wanted: one block per SM at most
 
+constexpr size_t plan_smem(int64_t bins)
+{
+    return static_cast<size_t>(bins) * (kPlanWarps + 2) * sizeof(uint32_t);
+}
 struct PlanShape {
     int64_t bins, blocks;
     size_t smem;
@@ -117,7 +121,7 @@ PlanShape plan_shape(int64_t vocab)
     s.bins = ((vocab + kPlanBlocks - 1) / kPlanBlocks + 31) / 32 * 32; // whole words of `empty`
     if (s.bins > kPlanMaxBins) s.bins = kPlanMaxBins;
     s.blocks = (vocab + s.bins - 1) / s.bins;
-    s.smem = static_cast<size_t>(s.bins) * (kPlanWarps + 2) * sizeof(uint32_t);
+    s.smem = plan_smem(s.bins);
     return s;
 }
 
@@ -613,9 +617,7 @@ extern "C" int zero_embed_backward(const void* dout, int32_t dout_type, const vo
     const void* plan = id_type == ZERO_TYPE_I64
                            ? reinterpret_cast<const void*>(plan_kernel<int64_t>)
                            : reinterpret_cast<const void*>(plan_kernel<int32_t>);
-    if (p.smem > 32 * 1024 && // beside the static words
-        cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(p.smem)) != cudaSuccess)
+    if (p.smem > 32 * 1024 && !allow_shared(plan, plan_smem(kPlanMaxBins))) // beside the static words
         return ZERO_ECUDA;
     const unsigned blocks = static_cast<unsigned>(p.blocks);
     const int bins = static_cast<int>(p.bins);

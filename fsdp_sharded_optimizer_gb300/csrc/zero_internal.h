@@ -38,6 +38,16 @@ struct StepScalars {
 };
 StepScalars make_scalars(const zero_hparams_t* hp, int32_t n_ranks);
 
+// Lets launches of a kernel ask for up to `most` bytes of dynamic shared memory.
+// The limit is state of the kernel that all host threads share, so it has to be
+// the same in every call: the largest that any launch of this kernel may ask for,
+// not what the coming one does.
+inline bool allow_shared(const void* kernel, size_t most)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(most)) == cudaSuccess;
+}
+
 // Persistent-grid size for a kernel on the current device: the SM count
 // times the resident blocks per SM (computed once per device and kernel).
 int persistent_blocks(const void* kernel, int block_threads, size_t dyn_smem);
