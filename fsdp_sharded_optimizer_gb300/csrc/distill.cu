@@ -30,6 +30,7 @@
 // every block of a row can form the sum about it before it knows the row's maximum m,
 // and neither so - s_ik nor m - so is negative, so that nothing cancels, however far
 // below m the logits of a block's own part lie.  One block alone takes so = m.
+#include "exchange.cuh"
 #include "typed.cuh"
 #include "zero_internal.h"
 
@@ -37,6 +38,7 @@ namespace zero {
 namespace {
 
 using dev::Bf16;
+using dev::kMaxRanks;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -253,7 +255,6 @@ distill_kernel(const Args A)
 // for all rows and is the only one that reads or fills them, so it asks for
 // the next row's piece (cp.async) as soon as it has used this row's for the
 // last time, and no barrier stands between a row's loads and the one before.
-constexpr int kMaxRanks = 8;
 constexpr int kMaxRowWarps = 16;
 
 // How many exponentials a logit takes.
@@ -396,45 +397,8 @@ __device__ __forceinline__ void fetch_ends(uint4* part, const Part<T>& p, int64_
 struct RowShared {
     float most[2][kMaxRowWarps]; // maxima of the block's warps: logits, teacher
     float sum[4][kMaxRowWarps];  // sums of the block's warps
-    float4 ranks[2][kMaxRanks];  // by row parity: every rank's maximum and sums
-    uint64_t arrived[2];         // mbarriers: all ranks' words of that parity are here
+    dev::Words words;            // every rank's maximum and sums
 };
-
-// The ranks of a cluster hand one another three words a row.  They do it by
-// st.async, which counts its bytes on the receiver's mbarrier: a cluster barrier
-// would have every thread wait for its own stores of the gradient first
-// (measured, 2000 x 131072 bf16 on 4 ranks: 294 us).
-__device__ __forceinline__ uint32_t shared_at(const void* p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void send_words(uint32_t words, uint32_t barrier, int to_rank, float a,
-                                           float b, float c)
-{
-    uint32_t there, there_barrier;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(words), "r"(to_rank));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there_barrier) : "r"(barrier), "r"(to_rank));
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
-                 ::"r"(there), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)),
-                 "r"(__float_as_uint(c)), "r"(0u), "r"(there_barrier)
-                 : "memory");
-}
-// Waits for the phase of a parity, a microsecond at a time; false after about a
-// quarter of a second.
-__device__ __forceinline__ bool wait_phase(uint32_t barrier, uint32_t phase)
-{
-    for (int i = 0; i < (1 << 18); ++i) {
-        uint32_t done;
-        asm volatile("{\n.reg .pred p;\n"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-                     "selp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done)
-                     : "r"(barrier), "r"(phase), "r"(1000u)
-                     : "memory");
-        if (done) return true;
-    }
-    return false;
-}
 
 // 2^(x c - m c) for a thread's maximum m so far.  The reference m c is rounded once
 // and the product inside the fma is not, so the terms agree to rounding; what the
@@ -598,15 +562,9 @@ row_kernel(const Args A, int ranks, int slots)
         sh.most[0][tid] = sh.most[1][tid] = -INFINITY;
         for (int i = 0; i < 4; ++i) sh.sum[i][tid] = 0.0f;
     }
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_at(&sh.arrived[i])) : "memory");
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    if (tid == 0) dev::init_words(sh.words);
     __syncthreads();
-    if (ranks > 1) // every block has begun before another writes to its shared memory
-        asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                     "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (ranks > 1) dev::cluster_barrier(); // every block has begun before another writes to its shared memory
     int64_t row = blockIdx.x / ranks;
     if (row >= A.rows) row = A.rows;
     float w = weight(row), w_next = weight(row + clusters);
@@ -618,8 +576,7 @@ row_kernel(const Args A, int ranks, int slots)
     if (w == 0.0f) here.n = here.from = here.to = 0;
     fetch_from(here, tid);
     here = part_of(row < A.rows ? row : 0);
-    int parity = 0;
-    uint32_t phase = 0; // bit p: the phase that the mbarrier of parity p is in
+    dev::Turns turns;
     while (row < A.rows) {
         const int64_t next = row + clusters;
         const int64_t this_row = row, this_label = label;
@@ -804,32 +761,22 @@ row_kernel(const Args A, int ranks, int slots)
         float row_m = block_m, zs1 = v[0], zs2 = v[1], cross = v[3];
         const float zt = v[2];
         if (ranks > 1) { // the cluster's
-            const uint32_t barrier = shared_at(&sh.arrived[parity]);
-            if (tid == 0)
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(barrier),
-                             "r"(16 * ranks)
-                             : "memory");
-            if (tid < ranks)
-                send_words(shared_at(&sh.ranks[parity][rank]), barrier, tid, block_m, v[0], v[1]);
-            // a rank that does not answer leaves NaN for the row's results
-            const bool here_all = wait_phase(barrier, phase >> parity & 1);
-            phase ^= 1u << parity;
-            for (int r = 0; r < ranks; ++r) row_m = fmaxf(row_m, sh.ranks[parity][r].x);
+            const float4* words = turns.take(sh.words, rank, ranks, block_m, v[0], v[1]);
+            for (int r = 0; r < ranks; ++r) row_m = fmaxf(row_m, words[r].x);
             const RowScale to1(row_m, kLog2e), to2(row_m, c2);
             zs1 = zs2 = 0.0f;
             for (int r = 0; r < ranks; ++r) {
-                const float rm = sh.ranks[parity][r].x;
+                const float rm = words[r].x;
                 // a part without anything above -inf holds 0, or NaN
                 const float f2 = rm == -INFINITY ? 1.0f : RowScale(rm, c2).to(to2);
                 const float f1 = kExps != kTwo     ? power_of<kExps>(f2)
                                  : rm != -INFINITY ? RowScale(rm, kLog2e).to(to1)
                                                    : 1.0f;
-                zs1 = fmaf(sh.ranks[parity][r].y, f1, zs1);
-                zs2 = fmaf(sh.ranks[parity][r].z, f2, zs2);
+                zs1 = fmaf(words[r].y, f1, zs1);
+                zs2 = fmaf(words[r].z, f2, zs2);
             }
-            if (!here_all) zs1 = zs2 = __int_as_float(0x7FC00000);
+            if (turns.lost) zs1 = zs2 = __int_as_float(0x7FC00000);
             if (row_m > -INFINITY) cross = fmaf(zt, (row_m - sbase) * inv_tau, cross);
-            parity ^= 1;
         }
         if (kExps == kOne) zs1 = zs2;
         const RowScale r1(row_m, kLog2e), r2(row_m, c2);
@@ -965,9 +912,7 @@ row_kernel(const Args A, int ranks, int slots)
         }
     }
     // no block ends while another may still write to its shared memory
-    if (ranks > 1)
-        asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                     "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (ranks > 1) dev::cluster_barrier();
 }
 
 // Bytes of a row that a block should hold, and may hold: the larger the parts,
