@@ -938,11 +938,9 @@ int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)
     auto* kernel = row_kernel<T, kGrad, kExps, kThreadsOf>;
     const void* k = reinterpret_cast<const void*>(kernel);
     if (smem > 32 * 1024 && !allow_shared(k, smem_of(kMostPartBytes / 16, kMaxTop))) return ZERO_ECUDA;
-    const int resident = persistent_blocks(k, kThreadsOf, smem);
+    const int resident = persistent_clusters(k, kThreadsOf, smem, ranks);
     if (resident < 1) return ZERO_ECUDA;
-    int64_t clusters = resident / ranks;
-    if (clusters < 1) clusters = 1;
-    if (clusters > A.rows) clusters = A.rows;
+    const int64_t clusters = resident < A.rows ? resident : A.rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
     cfg.blockDim = dim3(kThreadsOf);

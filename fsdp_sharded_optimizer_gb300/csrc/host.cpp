@@ -50,6 +50,17 @@ struct GeomEntry {
 std::mutex g_geom_mu;
 GeomEntry g_geom[256];
 int g_geom_n = 0;
+
+struct ClusterEntry {
+    int device;
+    const void* kernel;
+    size_t smem;
+    int block, ranks, clusters;
+};
+constexpr int kClusterEntries = 32;
+std::mutex g_cluster_mu;
+ClusterEntry g_cluster[kClusterEntries];
+int g_cluster_next = 0;
 } // namespace
 
 int persistent_blocks(const void* kernel, int block_threads, size_t dyn_smem)
@@ -74,6 +85,36 @@ int persistent_blocks(const void* kernel, int block_threads, size_t dyn_smem)
     std::lock_guard<std::mutex> lk(g_geom_mu);
     if (g_geom_n < 256) g_geom[g_geom_n++] = {dev, kernel, block_threads, dyn_smem, blocks};
     return blocks;
+}
+
+int persistent_clusters(const void* kernel, int block_threads, size_t dyn_smem, int ranks)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    {
+        std::lock_guard<std::mutex> lk(g_cluster_mu);
+        for (const ClusterEntry& e : g_cluster)
+            if (e.kernel == kernel && e.smem == dyn_smem && e.ranks == ranks &&
+                e.block == block_threads && e.device == dev)
+                return e.clusters;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+    cfg.blockDim = dim3(static_cast<unsigned>(block_threads));
+    cfg.dynamicSmemBytes = dyn_smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) return -1;
+    if (clusters < 1) return -1;
+    std::lock_guard<std::mutex> lk(g_cluster_mu);
+    g_cluster[g_cluster_next] = {dev, kernel, dyn_smem, block_threads, ranks, clusters};
+    g_cluster_next = (g_cluster_next + 1) % kClusterEntries;
+    return clusters;
 }
 
 } // namespace zero

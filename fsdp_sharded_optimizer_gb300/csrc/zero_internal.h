@@ -52,6 +52,11 @@ inline bool allow_shared(const void* kernel, size_t most)
 // times the resident blocks per SM (computed once per device and kernel).
 int persistent_blocks(const void* kernel, int block_threads, size_t dyn_smem);
 
+// The clusters of `ranks` blocks of a kernel that are resident at once on the
+// current device.  For kernels whose shared memory goes by the call's sizes: the
+// answers of the last few sizes are kept, apart from persistent_blocks' own.
+int persistent_clusters(const void* kernel, int block_threads, size_t dyn_smem, int ranks);
+
 // Splits a grid stride (in vectors) into whole shards and a remainder so
 // that a grid-stride loop can advance (owner, position) without dividing.
 struct StrideSplit {
