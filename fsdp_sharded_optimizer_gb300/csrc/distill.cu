@@ -25,7 +25,7 @@
 // phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
 // 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
 // no cluster holds) took 255, 553 and 212 us for the first, third and last.
-//   kl = tau^2 * ( sum_k p_k ((t_k - tm) - (s_ik - so)) / tau + (m - so) / tau + log Z - log Zt )
+//   kl = tau * ( m - so + tau * ( sum_k p_k ((t_k - tm) - (s_ik - so)) / tau + log Z - log Zt ) )
 // with Zt the teacher's sum and so the student's largest logit at a counted entry:
 // every block of a row can form the sum about it before it knows the row's maximum m,
 // and neither so - s_ik nor m - so is negative, so that nothing cancels, however far
@@ -430,7 +430,10 @@ struct Scale {
 
 // The same for the maximum of a block's part or of the row.  Where |m c| is above
 // 2^23 (far) the terms are 2^((x - m) c), x - m exact wherever that is not 0: an
-// operation more, and outside the loops that all rows go through.
+// operation more, in loops of their own, as in those that all rows go through it costs
+// registers (5 x 50257 fp32 loss 5.80 us, so 5.65; 8192 x 32000 at temperature 1.5 220
+// and 214).  A row without any logit that is not masked takes longer for it (8192 x
+// 32000 bf16 279 us for 179, its loss 186 for 99); one with a masked part does not.
 struct RowScale {
     float m, c, ref;
     bool far;
@@ -462,27 +465,45 @@ struct RowScale {
     }
 };
 
-// Columns [from, to) of a row with a far maximum m, read again: its sums, and its
-// gradient a1 2^((x - m) c1) + a2 2^((x - m) c2).
+// The sums of a part of a row with a far maximum m, read again (from the L2, mostly):
+// without a gradient, its place on the chip has been given to the next row.
 template <typename T>
-__device__ __noinline__ float2 far_sums(const T* s, int64_t from, int64_t to, float m, float c1, float c2)
+__device__ __noinline__ float2 far_sums(const Part<T> p, int64_t vocab, float m, float c1, float c2)
 {
+    constexpr int kE = Piece<T>::kElems, kBatch = 4;
+    const T* at = p.row + p.lo;
+    const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
     float2 z = make_float2(0.0f, 0.0f);
-    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x) {
-        const float d = dev::load1(s + i) - m;
-        z.x += exp2_approx(d * c1);
-        z.y += exp2_approx(d * c2);
+    auto add = [&](float x) {
+        z.x += exp2_approx((x - m) * c1);
+        z.y += exp2_approx((x - m) * c2);
+    };
+    for (int j = p.from + tid; j < p.to; j += kBatch * threads) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            raw[u] = j + u * threads < p.to
+                         ? *reinterpret_cast<const uint4*>(at + static_cast<int64_t>(j + u * threads) * kE)
+                         : lowest_piece(T());
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            float2 x[Piece<T>::kPairs];
+            unpack_piece(raw[u], x, T());
+#pragma unroll
+            for (int e = 0; e < Piece<T>::kPairs; ++e) {
+                add(x[e].x);
+                add(x[e].y);
+            }
+        }
+    }
+    // what lies in the pieces at the row's ends: one before `from`, one from `to`
+    const int whole = p.to > p.from ? p.to : p.from;
+    for (int i = tid; i < 2 * kE; i += threads) {
+        const int64_t col = p.lo + (i < kE ? i : static_cast<int64_t>(whole) * kE + i - kE);
+        const bool here = i < kE ? p.from == 1 && p.n > 0 && col >= 0 : whole < p.n;
+        if (here && col < vocab) add(dev::load1(p.row + col));
     }
     return z;
-}
-template <typename T>
-__device__ __noinline__ void far_gradient(const T* s, T* ds, int64_t from, int64_t to, float m, float c1,
-                                          float c2, float a1, float a2)
-{
-    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x) {
-        const float d = dev::load1(s + i) - m;
-        dev::store1(ds + i, fmaf(a1, exp2_approx(d * c1), a2 * exp2_approx(d * c2)));
-    }
 }
 
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
@@ -720,25 +741,44 @@ row_kernel(const Args A, int ranks, int slots)
         tm = warp_max(sh.most[1][lane % kMaxRowWarps]);
         const RowScale b1(block_m, kLog2e), b2(block_m, c2);
         float sbase = block_m;
+        const bool far_part = b2.far || (kExps == kTwo && b1.far);
+        bool nothing = false; // a masked part of a row that has a logit far above it
         if (ranks > 1) {
             sbase = -INFINITY;
             for (int k = lane; k < A.top; k += 32) sbase = fmaxf(sbase, top_s[k]);
             sbase = warp_max(sbase);
+            nothing = far_part && (sbase - block_m) * (kExps == kTwo ? fminf(kLog2e, c2) : c2) > 512.0f;
         }
         if (sbase == -INFINITY) sbase = 0.0f;
         const float tbase = tm == -INFINITY ? 0.0f : tm;
         // its sums
         float v[4] = {z1.x + z1.y, z2.x + z2.y, 0.0f, 0.0f};
-        if (b2.far || (kExps == kTwo && b1.far)) {
-            const float2 z = far_sums(s, lo < 0 ? 0 : lo, hi < vocab ? hi : vocab, b2.m, kLog2e, c2);
+        if (far_part && !nothing) {
+            float2 z = make_float2(0.0f, 0.0f);
+            if (kGrad) {
+                for (int j = tid; j < n; j += kThreadsOf) {
+                    float2 x[kP];
+                    unpack_piece(part[j], x, T());
+#pragma unroll
+                    for (int e = 0; e < kP; ++e) {
+                        const float2 d = dev::add2(x[e], dev::pair(-b2.m));
+                        const float2 e1 = exp2_pair(dev::mul2(d, dev::pair(kLog2e)));
+                        const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
+                        z.x += e1.x + e1.y;
+                        z.y += e2.x + e2.y;
+                    }
+                }
+            } else {
+                z = far_sums(now, vocab, b2.m, kLog2e, c2);
+            }
             v[0] = kExps == kTwo ? z.x * exp2_approx(b1.off()) : z.x;
             v[1] = z.y * exp2_approx(b2.off());
         } else { // a thread without anything above -inf has 0, or NaN
-            const float f2 = Scale(m, c2).to(b2.ref);
+            const float f2 = nothing ? 0.0f : Scale(m, c2).to(b2.ref);
             v[1] *= f2;
-            v[0] *= kExps == kOne   ? 0.0f
-                    : kExps == kTwo ? Scale(m, kLog2e).to(b1.ref)
-                                    : power_of<kExps>(f2);
+            v[0] *= kExps == kOne || nothing ? 0.0f
+                    : kExps == kTwo          ? Scale(m, kLog2e).to(b1.ref)
+                                             : power_of<kExps>(f2);
         }
         for (int k = tid; k < A.top; k += kThreadsOf) {
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
@@ -758,8 +798,8 @@ row_kernel(const Args A, int ranks, int slots)
         for (int off = 4; off > 0; off >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, off);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, all, 8 * i);
-        float row_m = block_m, zs1 = v[0], zs2 = v[1], cross = v[3];
-        const float zt = v[2];
+        float row_m = block_m, zs1 = v[0], zs2 = v[1];
+        const float zt = v[2], cross = v[3];
         if (ranks > 1) { // the cluster's
             const float4* words = turns.take(sh.words, rank, ranks, block_m, v[0], v[1]);
             for (int r = 0; r < ranks; ++r) row_m = fmaxf(row_m, words[r].x);
@@ -776,7 +816,6 @@ row_kernel(const Args A, int ranks, int slots)
                 zs2 = fmaf(words[r].z, f2, zs2);
             }
             if (turns.lost) zs1 = zs2 = __int_as_float(0x7FC00000);
-            if (row_m > -INFINITY) cross = fmaf(zt, (row_m - sbase) * inv_tau, cross);
         }
         if (kExps == kOne) zs1 = zs2;
         const RowScale r1(row_m, kLog2e), r2(row_m, c2);
@@ -789,8 +828,8 @@ row_kernel(const Args A, int ranks, int slots)
             const float from = row_m == -INFINITY ? 0.0f : row_m;
             const float log1 = kExps == kTwo ? r1.log_of(zs1) : r2.log_of(zs1, 1 << kExps);
             A.ce[this_row] = has_label ? log1 - (s_label - from) : 0.0f;
-            A.kl[this_row] = has_top ? A.tau * A.tau * (cross / zt + (r2.log_of(zs2) - logf(zt)))
-                                     : 0.0f;
+            A.kl[this_row] =
+                has_top ? A.tau * fmaf(A.tau, cross / zt + (r2.log_of(zs2) - logf(zt)), from - sbase) : 0.0f;
         }
         if constexpr (kGrad) {
             for (int k = tid; k < A.top; k += kThreadsOf) { // the marks are read: clear them
@@ -846,15 +885,30 @@ row_kernel(const Args A, int ranks, int slots)
                     fetch_whole(part_at, then, j);
                 }
             }
-            const int end = far ? 0 : n;
-            if (far && has_any)
-                far_gradient(s, ds, lo < 0 ? 0 : lo, hi < vocab ? hi : vocab, r2.m, kLog2e, c2,
-                             kExps == kOne ? 0.0f : kExps == kTwo ? a1 * exp2_approx(r1.off()) : a1,
-                             a2 * exp2_approx(r2.off()));
+            if (far) {
+                const float f1 = kExps == kOne   ? 0.0f
+                                 : kExps == kTwo ? a1 * exp2_approx(r1.off())
+                                                 : a1;
+                const float f2 = a2 * exp2_approx(r2.off());
+                for (; j < n; j += kThreadsOf) {
+                    float2 x[kP];
+                    unpack_piece(part[j], x, T());
+#pragma unroll
+                    for (int e = 0; e < kP; ++e) {
+                        const float2 d = dev::add2(x[e], dev::pair(-r2.m));
+                        const float2 e1 = exp2_pair(dev::mul2(d, dev::pair(kLog2e)));
+                        const float2 e2 = exp2_pair(dev::mul2(d, dev::pair(c2)));
+                        x[e] = dev::fma2(e1, dev::pair(f1), dev::mul2(e2, dev::pair(f2)));
+                    }
+                    write(j, x);
+                    at_slot(j);
+                    fetch_whole(part_at, then, j);
+                }
+            }
             // whole batches: nothing of them at the ends, of this row or the next
             const int first = now.from > then.from ? now.from : then.from;
             int batches = wide_to < then.to || then.to == 0 ? wide_to : then.to;
-            if (!alike || far) batches = 0;
+            if (!alike) batches = 0;
             for (; j + kStep - kThreadsOf < batches; j += kStep) {
                 at_slot(j);
                 uint4 raw[kBatch];
@@ -877,7 +931,7 @@ row_kernel(const Args A, int ranks, int slots)
                     }
                 }
             }
-            for (; j < end; j += kThreadsOf) {
+            for (; j < n; j += kThreadsOf) {
                 float2 x[kP];
                 unpack_piece(part[j], x, T());
 #pragma unroll

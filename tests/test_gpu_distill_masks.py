@@ -29,7 +29,8 @@ def log_q(monkeypatch):
             a = (t[r][on] - t[r][on].max()) / tau
             p = np.exp(a) / np.exp(a).sum()
             terms = a - np.log(np.exp(a).sum()) - d[ids[r][on]] + np.log(np.exp(d).sum())
-            kl[r] = tau ** 2 * (p[p > 0] * terms[p > 0]).sum()
+            with np.errstate(over="ignore"):  # infinite where fp32, the output's type, cannot hold it
+                kl[r] = np.float32(tau ** 2 * (p[p > 0] * terms[p > 0]).sum())
         return (ce, kl, *rest)
 
     monkeypatch.setattr(test_gpu_distill, "reference", reference)
@@ -97,4 +98,21 @@ def test_differences_of_large_logits(log_q, exponent, tau):
         k = torch.randint(0, 24, (R, V), generator=gen, device="cuda").double()
         sign = 1.0 if exponent % 2 else -1.0
         c["s"].copy_((sign * (2.0 ** exponent + step * 32) + k * step).float())
+        check(c, tau)
+
+
+@pytest.mark.parametrize("value", [-1e9, 1e9, None], ids=["-1e9", "1e9", "lowest"])
+@pytest.mark.parametrize("ranks,logits,V", [(2, "f32", 5003), (4, "bf16", 8192), (8, "f32", 9001)])
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0])
+def test_parts_without_live_entries(log_q, ranks, logits, V, value, tau):
+    """The teacher's entries all in the masked part, or none; one live column in the
+    part whose other columns are masked; a part far above the others."""
+    part = -(-V // ranks)
+    for r in {0, ranks // 2, ranks - 1}:
+        lo, hi = max(0, r * part - 50), min(V, (r + 1) * part + 50)
+        c = masked(ROWS[ranks], V, 4, logits, value, lo, hi)
+        c["ids"][::3] = -1
+        c["ids"][1::3] = torch.arange(lo, lo + 4, device="cuda")
+        c["labels"][2::3] = lo + 1
+        c["s"][2, (lo + hi) // 2] = 1.0
         check(c, tau)
