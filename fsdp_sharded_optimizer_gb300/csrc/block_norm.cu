@@ -29,9 +29,13 @@
 // Measured (device time, one GB300): forward 16384 x 4096 bf16 91 us, 5.9 TB/s, of
 // 345 us with one row's loads, weights and exchanges after another; backward
 // 16384 x 2048 with an fp32 residual 105 us, 5.8 TB/s (288 at first), 16384 x 4096
-// bf16 160 us; 8191 x 768 LayerNorm with biases 32 us, of which 11 are the two
+// bf16 159 us (a gate row for each token 390: 268 MB more, and a row at a time);
+// 8191 x 768 LayerNorm with biases 32 us, of which 11 are the two
 // launches, their first loads and the sums over blocks, and the rest is bound by
-// instructions (three exchanges a row); a single row 3.7 us forward.
+// instructions (three exchanges a row); a single row 3.7 us forward.  dim above 4096
+// backward (one row at a time) and above 8192 at all does not fit the registers:
+// 8192 x 8192 RMS forward 93 us, backward 328 (240 to 480 bytes of stack a thread; LayerNorm
+// 132 and 576, up to 856 bytes), 8192 x 16384 968 and 3353 us (1.0 to 2.4 KB).
 //
 // Rows whose length is no multiple of 8 start at every alignment.  A thread
 // then takes the 8 columns of an aligned 16-byte (bf16) or 32-byte (fp32)

@@ -19,12 +19,14 @@
 // costs about ten instructions, an exponential per pass among them.
 //
 // Measured (device time, one GB300): 4096 x 32000 fp32, soft targets only, 164 us,
-// 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 175 us, 6.0 TB/s, at 1.5 with
+// 6.4 TB/s; 8192 x 32000 bf16 at temperature 1 177 us, 5.9 TB/s, at 1.5 with
 // labels 213 us (two exponentials a logit and pass); 8191 x 50257 bf16 at
-// temperature 2 307 us, 5.4 TB/s (100 KB a row: two blocks to an SM, whose
-// phases do not hide one another fully); the loss alone of 8192 x 32000 bf16
-// 91-94 us, 5.7 TB/s.  Reading the row twice instead (distill_kernel, for rows that
-// no cluster holds) took 255, 553 and 212 us for the first, third and last.
+// temperature 2 308 us, 5.4 TB/s (100 KB a row: two blocks to an SM, whose
+// phases do not hide one another fully); 2000 x 131072 bf16 193 us, 5.4 TB/s; the loss
+// alone of 8192 x 32000 bf16 95-96 us, 5.5 TB/s.  Reading the row twice instead
+// (distill_kernel, for rows that no cluster holds) took 255, 553 and 212 us for the
+// first, third and last of the four that a block or two hold; 200 x 800003 takes 304 us.
+//
 //   kl = tau * ( m - so + tau * ( sum_k p_k ((t_k - tm) - (s_ik - so)) / tau + log Z - log Zt ) )
 // with Zt the teacher's sum and so the student's largest logit at a counted entry:
 // every block of a row can form the sum about it before it knows the row's maximum m,
@@ -969,10 +971,14 @@ row_kernel(const Args A, int ranks, int slots)
     if (ranks > 1) dev::cluster_barrier();
 }
 
-// Bytes of a row that a block should hold, and may hold: the larger the parts,
-// the fewer sums are handed round (4096 x 32000 fp32 on 2 and 4 ranks 164 and 340
-// us, 2000 x 50257 fp32 on 2 and 3 ranks 141 and 193).  The number of ranks is a
-// power of two: 2000 x 131072 bf16 takes 340 us on 3 ranks, 267 on 4.
+// Bytes of a row that a block should hold, and may hold.  Larger parts leave one block
+// to an SM, smaller ones hand round more sums: 4096 x 32000 fp32 takes 206, 166, 167, 174
+// and 261 us on 1, 2, 3, 4 and 8 ranks, its loss alone 108, 91 and 101 on 1, 2 and 4;
+// 8191 x 50257 bf16 308 and 337 on 1 and 2; 2000 x 50257 fp32 141, 146, 144 and 166 on
+// 2, 3, 4 and 8; 2000 x 131072 bf16 263, 229, 194 and 224.  The number of ranks is a
+// power of two; another is better by up to a tenth where the parts come to 74 KB (2000 x
+// 151936 bf16 on 3, 4, 5 and 8 ranks 256, 265, 241 and 250; 1000 x 256000 on 4, 5, 6 and
+// 8 273, 213, 238 and 214).
 constexpr int64_t kPartBytes = 104 * 1024, kMostPartBytes = 192 * 1024;
 
 // Five blocks with parts up to the first of these fit an SM, three up to the second,
@@ -980,7 +986,8 @@ constexpr int64_t kPartBytes = 104 * 1024, kMostPartBytes = 192 * 1024;
 // logits at temperature 2 with 128, 160 and 256 threads 120, 128 and 153 us; 32000 at
 // temperature 1 with 128, 160 and 256 187, 175 and 179, at 1.5 223, 213 and 228; with
 // 256, 320 and 384 threads 38000 at 2 262, 248 and 264, 48000 at 1 273, 267 and 281,
-// 24000 fp32 245, 237 and 248.
+// 24000 fp32 245, 237 and 248.  The loss alone of 32000 at 1 with 128, 160 and 320: 101,
+// 96 and 114, of 2000 x 131072 on 4 ranks 115, 112 and 142.
 constexpr int64_t kSmallPartBytes = 43 * 1024, kWidePartBytes = 72 * 1024;
 template <typename T, bool kGrad, int kExps, int kThreadsOf>
 int launch_rows(const Args& A, int ranks, int64_t slots, cudaStream_t stream)

@@ -26,10 +26,12 @@
 //   join_kernel  the frequent rows' sums over their chunks.
 //
 // Read and written: T ids, T*D of dout, V*D of dtable (each row once), and
-// 8*D bytes of partial sums per chunk at most.  HBM-bound, by writes above all:
-// 16384 x 4096 into 32000 rows takes 80 us for 396 MB, 262 MB of them written
-// (a fill of this GPU's memory reaches 4.0 TB/s, a copy 3.4 each way); 8192 x
-// 768 into 50257 rows 29 us.
+// 8*D bytes of partial sums per chunk at most.  16384 x 4096 into 32000 rows takes
+// 80 us for 396 MB, 262 MB of them written (4.9 TB/s): the plan 15 us, in which memory
+// idles, the sums and zeros 62.  8192 x 768 into 50257 rows takes 29 us for 90 MB: the
+// plan 11 us, the sums and zeros 18.5, whose 96-thread blocks of short rows wait for
+// their loads at a third of the warps.  (Writes alone do not bound it: a fill of 262 MB
+// takes 66 us, but the lookup, which reads as well, writes at 4.5 TB/s.)
 #include "typed.cuh"
 #include "zero_internal.h"
 

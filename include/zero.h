@@ -798,7 +798,9 @@ const char* zero_strerror(int code);
  *    only (ZERO_EALIGN otherwise); wide loads are used where addresses allow.
  *  - All arithmetic and all sums are fp32; an output of bf16 is rounded once,
  *    to nearest even.  Sums have a fixed order: the same call on the same
- *    inputs, at the same alignment to 16 bytes, gives the same bits.
+ *    inputs, at the same alignment to 16 bytes, gives the same bits.  The
+ *    order goes by the call's sizes and by that alignment, so one row, token
+ *    or gate in a call of other sizes may differ in the last bits.
  *  - Scratch is the caller's, 16-byte aligned, of the size the *_scratch_bytes
  *    call gives; calls that share it must be ordered.  Its contents need not
  *    be kept from one call to the next.
@@ -849,7 +851,8 @@ int zero_embed_backward(const void* dout, int32_t dout_type, const void* ids, in
 
 /* The norms around a block.  kind: ZERO_NORM_RMS, norm(v) = v * r * w + c with
  * r = 1/sqrt(mean(v^2) + eps), or ZERO_NORM_LAYER, the same of v - mean(v).
- * An absent (null) weight is 1, an absent bias 0. */
+ * An absent (null) weight is 1, an absent bias 0.  The mean squares are fp32:
+ * a row whose squares sum to more than 3.4e38 has r = 0. */
 typedef struct {
     int64_t n_rows, dim;     /* dim up to 16384 */
     int64_t rows_per_gate;   /* >= 1: row i uses row i / rows_per_gate of the gate */
@@ -936,7 +939,12 @@ typedef struct {
  * an id that occurs twice counts with both probabilities.  kl is 0 where no
  * entry counts (or all that count are -inf), ce where the label lies outside
  * [0, vocab) or labels is null, both where every logit is -inf or row_weight
- * is 0 (such rows are not read).
+ * is 0 (such rows are not read).  Masked logits may have any finite value;
+ * where all that a row has are masked, they are a distribution like others.
+ * A row's sums are split over 1, 2, 4 or 8 blocks by vocab and, below 77 rows,
+ * by n_rows, and over threads by where the row starts between two multiples of
+ * 16 bytes: a row alone and in a batch, or rows of an odd vocab at another
+ * place, may differ in the last bits.
  *   logits          [n_rows, vocab], rows logits_stride apart
  *   teacher_logits  [n_rows, top]
  *   teacher_ids     [n_rows, top]
