@@ -27,7 +27,7 @@
 // (distill_kernel, for rows that no cluster holds) took 255, 553 and 212 us for the
 // first, third and last of the four that a block or two hold; 200 x 800003 takes 304 us.
 //
-//   kl = tau * ( m - so + tau * ( sum_k p_k ((t_k - tm) - (s_ik - so)) / tau + log Z - log Zt ) )
+//   kl = tau * ( sum_k p_k ((t_k - tm) - (s_ik - so)) + m - so ) + tau^2 * (log Z - log Zt)
 // with Zt the teacher's sum and so the student's largest logit at a counted entry:
 // every block of a row can form the sum about it before it knows the row's maximum m,
 // and neither so - s_ik nor m - so is negative, so that nothing cancels, however far
@@ -53,6 +53,15 @@ __device__ __forceinline__ float exp2_approx(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// kl of a row from the sum of e_k ((t_k - tm) - (s_ik - so)), in units that keep kMaxTop
+// terms of any finite size in range, the teacher's sum zt, m - so and log Z.  Nothing is
+// divided by the temperature: a masked logit of the type's lowest value would overflow.
+constexpr float kCrossUnit = 1.0f / kMaxTop;
+__device__ __forceinline__ float kl_of(float tau, float cross, float zt, float above, float log_z)
+{
+    return fmaf(cross / zt, tau / kCrossUnit, fmaf(tau * tau, log_z - logf(zt), tau * above));
 }
 
 struct Args {
@@ -183,8 +192,7 @@ distill_kernel(const Args A)
         for (int k = tid; k < A.top; k += kThreads) {
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
             zt += e;
-            if (e != 0.0f)
-                cross = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - base)) * inv_tau, cross);
+            if (e != 0.0f) cross = fmaf(e * kCrossUnit, (top_p[k] - tbase) - (top_s[k] - base), cross);
             top_p[k] = e;
         }
         zt = block_sum(zt, red);
@@ -196,8 +204,7 @@ distill_kernel(const Args A)
         const bool has_label = labelled && !empty;
         if (tid == 0) {
             A.ce[row] = has_label ? logf(z1) - (s_label - base) : 0.0f;
-            A.kl[row] =
-                has_top ? A.tau * A.tau * (cross / zt + (logf(z2) - logf(zt))) : 0.0f;
+            A.kl[row] = has_top ? kl_of(A.tau, cross, zt, 0.0f, logf(z2)) : 0.0f;
         }
         if constexpr (kGrad) {
             const float a1 = has_label ? w * A.ce_weight / z1 : 0.0f;
@@ -785,8 +792,7 @@ row_kernel(const Args A, int ranks, int slots)
         for (int k = tid; k < A.top; k += kThreadsOf) {
             const float e = exp2_approx((top_p[k] - tbase) * c2); // 0 where not counted
             v[2] += e;
-            if (e != 0.0f)
-                v[3] = fmaf(e, ((top_p[k] - tbase) - (top_s[k] - sbase)) * inv_tau, v[3]);
+            if (e != 0.0f) v[3] = fmaf(e * kCrossUnit, (top_p[k] - tbase) - (top_s[k] - sbase), v[3]);
             top_p[k] = e;
         }
         const bool marked = kGrad && labelled && this_label >= lo && this_label < hi &&
@@ -830,8 +836,7 @@ row_kernel(const Args A, int ranks, int slots)
             const float from = row_m == -INFINITY ? 0.0f : row_m;
             const float log1 = kExps == kTwo ? r1.log_of(zs1) : r2.log_of(zs1, 1 << kExps);
             A.ce[this_row] = has_label ? log1 - (s_label - from) : 0.0f;
-            A.kl[this_row] =
-                has_top ? A.tau * fmaf(A.tau, cross / zt + (r2.log_of(zs2) - logf(zt)), from - sbase) : 0.0f;
+            A.kl[this_row] = has_top ? kl_of(A.tau, cross, zt, from - sbase, r2.log_of(zs2)) : 0.0f;
         }
         if constexpr (kGrad) {
             for (int k = tid; k < A.top; k += kThreadsOf) { // the marks are read: clear them

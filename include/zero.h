@@ -936,15 +936,15 @@ typedef struct {
  *   kl[row] = temperature^2 * sum_k p_k (log p_k - log q[teacher_ids_k])
  *   ce[row] = -log softmax(logits)[label]
  * An entry whose id lies outside [0, vocab) is not counted (shorter lists);
- * an id that occurs twice counts with both probabilities.  kl is 0 where no
- * entry counts (or all that count are -inf), ce where the label lies outside
- * [0, vocab) or labels is null, both where every logit is -inf or row_weight
- * is 0 (such rows are not read).  Masked logits may have any finite value;
- * where all that a row has are masked, they are a distribution like others.
- * A row's sums are split over 1, 2, 4 or 8 blocks by vocab and, below 77 rows,
- * by n_rows, and over threads by where the row starts between two multiples of
- * 16 bytes: a row alone and in a batch, or rows of an odd vocab at another
- * place, may differ in the last bits.
+ * an id that occurs twice counts with both probabilities; a probability below
+ * fp32's range is 0.  kl is 0 where no entry counts (or all that count are
+ * -inf), ce where the label lies outside [0, vocab) or labels is null, both
+ * where every logit is -inf or row_weight is 0 (such rows are not read).
+ * Masked logits may have any finite value; a row in which all are masked is a
+ * distribution like others.  A row's sums are split over 1, 2, 4 or 8 blocks by
+ * vocab and, below 77 rows, by n_rows, and over threads by where the row starts
+ * between two multiples of 16 bytes: a row alone and in a batch, or rows of an
+ * odd vocab at another place, may differ in the last bits.
  *   logits          [n_rows, vocab], rows logits_stride apart
  *   teacher_logits  [n_rows, top]
  *   teacher_ids     [n_rows, top]

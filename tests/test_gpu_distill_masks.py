@@ -116,3 +116,23 @@ def test_parts_without_live_entries(log_q, ranks, logits, V, value, tau):
         c["labels"][2::3] = lo + 1
         c["s"][2, (lo + hi) // 2] = 1.0
         check(c, tau)
+
+
+@pytest.mark.parametrize("tau", [0.9, 0.5, 0.1, 1e-3])
+@pytest.mark.parametrize("R,V,logits", [(12, 5003, "f32"), (100, 4097, "bf16"), (2, 400003, "f32")])
+def test_lowest_value_at_the_teachers_entries(log_q, R, V, logits, tau):
+    """A loss near the end of fp32's range: the lowest value at all of the teacher's
+    entries, at one, and at an entry without a probability to speak of."""
+    c = make(R, V, 8, logits=logits)
+    c["weight"].fill_(1.0)
+    low = torch.finfo(c["s"].dtype).min
+    for r in range(R):
+        c["ids"][r] = torch.arange(V - 8, V)
+        at = {0: slice(V - 8, V), 1: slice(V - 8, V - 7)}.get(r % 3, slice(V - 1, V))
+        c["s"][r, at] = low
+        c["t"][r] = torch.linspace(0.0, -0.7 * tau, 8, device="cuda")
+        if r % 3 == 2:
+            c["t"][r, 7] = -1e4 * tau
+        if c["labels"][r] >= V - 8:
+            c["labels"][r] = 0
+    check(c, tau)
