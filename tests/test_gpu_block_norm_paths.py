@@ -39,3 +39,21 @@ def test_many_rows(spec):
     for name, (_, t) in bufs.items():
         close(t, *want[name], t.dtype, name)
         assert torch.equal(t, again[name][1]), name
+
+
+@pytest.mark.parametrize("spec", [
+    dict(rows=3000, dim=256, span=3), dict(rows=3000, dim=100, act="f32", res="f32"),
+    dict(rows=1000, dim=1001, span=1, **BIASED), dict(rows=700, dim=520, span=100, offset=1),
+    dict(rows=611, dim=4096), dict(rows=400, dim=5000, **BIASED), dict(rows=400, dim=8200)],
+    ids=lambda c: "-".join("%s%s" % (k[:4], v) for k, v in c.items()))
+def test_gradients_in_place(spec):
+    """dx in dy's place and dbranch in du's: the same bits as apart."""
+    c = Case(**spec)
+    want = {k: t for k, (_, t) in run_backward(c, torch.float32, backward64(c)).items()}
+    scratch = torch.empty(B.zero_block_norm_scratch_bytes(c.rows, c.dim, c.span), dtype=torch.uint8,
+                          device="cuda")
+    sums = {k: torch.empty_like(t) for k, t in want.items() if k not in ("dx", "dbranch")}
+    B.zero_block_norm_backward(c.x, scratch, dy=c.dy, du=c.du, dx=c.dy, dbranch=c.du, **c.common(), **sums)
+    assert torch.equal(c.dy, want["dx"]) and torch.equal(c.du, want["dbranch"])
+    for k, t in sums.items():
+        assert torch.equal(t, want[k]), k
