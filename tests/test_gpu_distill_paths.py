@@ -106,3 +106,9 @@ def test_rows_that_no_cluster_holds(V, logits, tau):
     inside = run(c, tau, out=c["s"])
     assert torch.equal(inside[2], first[2]) and torch.equal(inside[1], first[1])
     c["s"].copy_(keep)
+
+
+@pytest.mark.parametrize("V,logits", [(785001, "bf16"), (392001, "f32")])
+def test_the_largest_rows_of_a_cluster(V, logits):
+    """Parts of almost 192 KB on 8 blocks, with as many entries as there may be."""
+    check(lively(2, V, 1024, logits=logits), 1.5)
