@@ -7,9 +7,11 @@ weights (the all-gather).  ZeRO-3 adds the per-unit gather and the per-unit
 reduce-scatter, scheduled with next-unit prefetch on a side stream
 (``zero3_step``, natively or as a CUDA graph).
 
-``zero_embed_*``, ``zero_block_norm_*`` and ``zero_distill_*`` are operators of
-the model that is trained: the embedding, the norms around a block and the
-distillation loss, each with its gradient.
+``zero_embed_*``, ``zero_block_norm_*``, ``zero_group_norm_*``, ``zero_relpos_*`` and
+``zero_distill_*`` are operators of the model that is trained: the embedding, the
+norms around a block, the group norm with its activation, the relative position
+bias and the distillation loss, each with its gradient.  ``zero_tensors_*`` take
+the global norm over many gradient tensors, and clip and copy them.
 
 The public calls carry the C ABI's names (include/zero.h) and live in
 ``_binding``.  They are loaded on first use, so that ``build`` can be imported
@@ -37,7 +39,11 @@ _PUBLIC = ("ZERO_DEFAULT_ALIGN", "ZERO_CHUNK_ELEMS", "ZERO_EALIGN", "ZERO_ECUDA"
            "zero_block_norm_forward", "zero_block_norm_backward",
            "zero_block_norm_scratch_bytes", "zero_distill_forward",
            "zero_distill_forward_backward", "zero_block_norm_t", "zero_block_norm_grads_t",
-           "zero_distill_t")
+           "zero_distill_t", "zero_tensor_list", "TensorList", "zero_tensors_sqnorm",
+           "zero_tensors_scale", "zero_tensors_clip", "zero_tensor_t",
+           "zero_group_norm_forward", "zero_group_norm_backward",
+           "zero_group_norm_scratch_bytes", "zero_group_norm_t", "zero_relpos_forward",
+           "zero_relpos_backward", "zero_relpos_scratch_bytes", "zero_relpos_t")
 
 __all__ = list(_PUBLIC)
 

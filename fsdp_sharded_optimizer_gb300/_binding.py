@@ -79,6 +79,7 @@ class zero_clip_t(C.Structure):
 
 ZERO_TYPE_BF16, ZERO_TYPE_F32, ZERO_TYPE_I32, ZERO_TYPE_I64 = 1, 2, 3, 4
 ZERO_NORM_RMS, ZERO_NORM_LAYER = 0, 1
+ZERO_ACT_NONE, ZERO_ACT_SILU, ZERO_ACT_GELU = 0, 1, 2
 
 
 class zero_block_norm_t(C.Structure):
@@ -100,6 +101,25 @@ class zero_distill_t(C.Structure):
                 ("top", C.c_int32), ("logits_type", C.c_int32), ("teacher_type", C.c_int32),
                 ("id_type", C.c_int32), ("label_type", C.c_int32), ("temperature", C.c_double),
                 ("ce_weight", C.c_double), ("kl_weight", C.c_double)]
+
+
+class zero_tensor_t(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_int64),
+                ("src_type", C.c_int32), ("dst_type", C.c_int32)]
+
+
+class zero_group_norm_t(C.Structure):
+    _fields_ = [("samples", C.c_int64), ("positions", C.c_int64), ("channels", C.c_int64),
+                ("x_stride", C.c_int64), ("y_stride", C.c_int64), ("groups", C.c_int32),
+                ("type", C.c_int32), ("param_type", C.c_int32), ("grad_type", C.c_int32),
+                ("act", C.c_int32), ("eps", C.c_double)]
+
+
+class zero_relpos_t(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("heads", C.c_int64), ("q_len", C.c_int64),
+                ("k_len", C.c_int64), ("start", C.c_int64), ("max_distance", C.c_int64),
+                ("buckets", C.c_int32), ("bidirectional", C.c_int32), ("causal", C.c_int32),
+                ("table_type", C.c_int32), ("type", C.c_int32)]
 
 
 def clip_args(max_norm, scratch, norm_coef, grad_shard=None):
@@ -197,6 +217,22 @@ SIGNATURES = {
     "zero_distill_forward": (C.c_int, [_P] * 9),
     # ..., ce, kl, dlogits, dlogits stride, stream
     "zero_distill_forward_backward": (C.c_int, [_P] * 9 + [_I64, _P]),
+    # tensors, n_tensors, accumulate, scratch, scratch bytes, stream
+    "zero_tensors_sqnorm": (C.c_int, [_P, _I64, _I32, _P, _I64, _P]),
+    # tensors, n_tensors, scale, norm_coef, stream
+    "zero_tensors_scale": (C.c_int, [_P, _I64, _F64, _P, _P]),
+    # tensors, n_tensors, max_norm, norm_coef, scratch, scratch bytes, stream
+    "zero_tensors_clip": (C.c_int, [_P, _I64, _F64, _P, _P, _I64, _P]),
+    "zero_group_norm_scratch_bytes": (_I64, [_I64, _I64, _I64, _I32]),
+    # norm, x, weight, bias, lengths, y, stats, scratch, scratch bytes, stream
+    "zero_group_norm_forward": (C.c_int, [_P] * 8 + [_I64, _P]),
+    # norm, x, dy, weight, bias, lengths, stats, dx, dweight, dbias, scratch, bytes, stream
+    "zero_group_norm_backward": (C.c_int, [_P] * 11 + [_I64, _P]),
+    # relpos, table, starts, q lengths, k lengths, scores, stride, out, stride, stream
+    "zero_relpos_forward": (C.c_int, [_P] * 6 + [_I64, _P, _I64, _P]),
+    "zero_relpos_scratch_bytes": (_I64, [_I64, _I64, _I64, _I64, _I32]),
+    # relpos, starts, q lengths, k lengths, dout, stride, dtable, accumulate, scratch, bytes, stream
+    "zero_relpos_backward": (C.c_int, [_P] * 5 + [_I64, _P, _I32, _P, _I64, _P]),
     "zero_stream_wait": (C.c_int, [_P, _I64]),
     "zero_strerror": (C.c_char_p, [C.c_int]),
 }
@@ -966,3 +1002,250 @@ def zero_distill_forward_backward(logits, teacher_logits, teacher_ids, ce, kl, d
         raise ValueError("logits and dlogits must have one type")
     _check("zero_distill_forward_backward", lib.zero_distill_forward_backward(
         *args, ptr, stride, _raw_stream(stream)))
+
+
+# ---------------------------------------------- gradients in many tensors
+class TensorList:
+    """Tensors and where they go, for the zero_tensors_* calls (zero_tensor_list).  It
+    keeps the tensors alive and holds their addresses: make it anew when they move."""
+
+    def __init__(self, array, n, keep):
+        self.array, self.n, self._keep = array, n, keep
+
+
+def zero_tensor_list(src, dst=None):
+    """A list of contiguous bf16 or fp32 tensors of any sizes for the zero_tensors_*
+    calls, each with its destination of as many elements (dst[i]; the tensor itself
+    by default or where dst[i] is src[i]), e.g. its place in a flat gradient buffer.
+    A destination must not overlap any other tensor of the list."""
+    src = list(src)
+    dst = src if dst is None else list(dst)
+    if len(src) != len(dst):
+        raise ValueError("zero_tensor_list: %d tensors and %d destinations" % (len(src), len(dst)))
+    array = (zero_tensor_t * len(src))()
+    spans = []  # (first byte, end, whether it is written)
+    for i, (a, b) in enumerate(zip(src, dst)):
+        what = "tensor %d" % i
+        if a.numel() != b.numel():
+            raise ValueError("%s: %d elements, and %d at its destination" % (
+                what, a.numel(), b.numel()))
+        e = array[i]
+        e.src, e.dst, e.n = _at(a, what), _at(b, "the destination of " + what), a.numel()
+        e.src_type, e.dst_type = _type(a, what), _type(b, "the destination of " + what)
+        if e.n:
+            if e.src == e.dst and e.src_type != e.dst_type:
+                raise ValueError("%s: another type in its own place" % what)
+            if e.src != e.dst:
+                spans.append((e.src, e.src + a.nbytes, False))
+            spans.append((e.dst, e.dst + b.nbytes, True))
+    any_end = written_end = 0
+    for first, end, written in sorted(spans):
+        if first < (any_end if written else written_end):
+            raise ValueError("zero_tensor_list: a destination overlaps another tensor")
+        any_end = max(any_end, end)
+        if written:
+            written_end = max(written_end, end)
+    return TensorList(array, len(src), (src, dst))
+
+
+def _tensor_list(tensors):
+    return tensors if isinstance(tensors, TensorList) else zero_tensor_list(tensors)
+
+
+def _coef(norm_coef):
+    if norm_coef.dtype != torch.float32 or norm_coef.numel() < 2:
+        raise ValueError("norm_coef must hold two fp32 values")
+    return _at(norm_coef, "norm_coef")
+
+
+def zero_tensors_sqnorm(tensors, scratch, accumulate=False, stream=None):
+    """Add the squared norm of all tensors (a zero_tensor_list, or tensors) into the
+    partials of zero_grad_sqnorm in `scratch`; zero_clip_coef gives the norm."""
+    t = _tensor_list(tensors)
+    _check("zero_tensors_sqnorm", lib.zero_tensors_sqnorm(
+        t.array, t.n, 1 if accumulate else 0, _at(scratch, "scratch"), scratch.nbytes,
+        _raw_stream(stream)))
+
+
+def zero_tensors_scale(tensors, scale=1.0, norm_coef=None, stream=None):
+    """dst = scale * coef * src for every tensor of a zero_tensor_list (or for tensors,
+    in place); coef is the second of norm_coef (zero_clip_coef), 1 without it."""
+    t = _tensor_list(tensors)
+    _check("zero_tensors_scale", lib.zero_tensors_scale(
+        t.array, t.n, scale, None if norm_coef is None else _coef(norm_coef),
+        _raw_stream(stream)))
+
+
+def zero_tensors_clip(tensors, max_norm, norm_coef, scratch, stream=None):
+    """dst = coef * src for every tensor of a zero_tensor_list (or for tensors, in
+    place), coef = min(1, max_norm / (norm + 1e-6)) of the norm over all of them;
+    norm_coef (2 fp32): norm and coef, written.  scratch: a device tensor of
+    zero_clip_scratch_bytes() bytes."""
+    t = _tensor_list(tensors)
+    _check("zero_tensors_clip", lib.zero_tensors_clip(
+        t.array, t.n, max_norm, _coef(norm_coef), _at(scratch, "scratch"), scratch.nbytes,
+        _raw_stream(stream)))
+
+
+# ------------------------------------------------------------- group norm
+_ACTS = {None: ZERO_ACT_NONE, "none": ZERO_ACT_NONE, "silu": ZERO_ACT_SILU, "gelu": ZERO_ACT_GELU}
+
+
+def _strided_rows(t, what, shape=None):
+    """Address of a tensor whose last dimension is contiguous, and the elements between
+    its rows, which have to be evenly apart."""
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if not _addressable(t):
+        raise ValueError("%s must be CUDA or pinned host memory" % what)
+    sizes, strides = t.shape, t.stride()
+    cols = sizes[-1]
+    if t.numel() == 0:
+        return t.data_ptr(), max(1, cols)
+    if cols > 1 and strides[-1] != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % what)
+    row = span = None
+    for size, stride in zip(sizes[-2::-1], strides[-2::-1]):
+        if size == 1:
+            continue
+        if row is None:
+            row = stride
+        elif stride != span:
+            raise ValueError("%s must have rows that are evenly apart" % what)
+        span = stride * size
+    return t.data_ptr(), max(1, cols) if row is None else row
+
+
+def _lengths(t, n, what):
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise ValueError("%s must be int32, got %s" % (what, t.dtype))
+    return _at(t, what, (n,))
+
+
+def _group_norm_call(x, stats, groups, act):
+    if x.dim() < 2:
+        raise ValueError("x must have two dimensions or more: samples, positions, channels")
+    if act not in _ACTS:
+        raise ValueError("act must be 'none', 'silu' or 'gelu'")
+    if stats is None and groups is None:
+        raise ValueError("groups must be given where stats are not")
+    N, C = x.shape[0], x.shape[-1]
+    P = 1
+    for n in x.shape[1:-1]:
+        P *= n
+    G = int(groups) if groups is not None else stats.shape[1]
+    if stats is not None:
+        if stats.dtype != torch.float32:
+            raise ValueError("stats must be fp32")
+        stats = _at(stats, "stats", (N, G, 2))
+    return N, P, C, G, stats
+
+
+def zero_group_norm_scratch_bytes(samples, positions, channels, groups):
+    return _bytes("zero_group_norm_scratch_bytes", lib.zero_group_norm_scratch_bytes(
+        int(samples), int(positions), int(channels), int(groups)))
+
+
+def zero_group_norm_forward(x, y, stats, scratch, weight=None, bias=None, lengths=None,
+                            groups=None, act="silu", eps=1e-5, stream=None):
+    """y = act(group norm of x), channels last.  x, y (samples x ... x channels): bf16 or
+    fp32, channels contiguous, positions evenly apart; y may be x.  stats (samples x
+    groups x 2, fp32): mean and 1/sqrt(variance + eps), written; may be None, with
+    groups given.  lengths (samples, int32): the positions that count; the others are
+    neither read nor written.  scratch: a device tensor of
+    zero_group_norm_scratch_bytes(samples, positions, channels, groups) bytes."""
+    N, P, C_, G, stats = _group_norm_call(x, stats, groups, act)
+    xp, xs = _strided_rows(x, "x")
+    yp, ys = _strided_rows(y, "y", x.shape)
+    par = _Alike((C_,), "weight and bias")
+    w, b = par(weight, "weight"), par(bias, "bias")
+    type = _type(x, "x")
+    if _type(y, "y") != type:
+        raise ValueError("x and y must have one type")
+    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, par.type or ZERO_TYPE_BF16,
+                             ZERO_TYPE_BF16, _ACTS[act], eps)
+    _check("zero_group_norm_forward", lib.zero_group_norm_forward(
+        C.byref(spec), xp, w, b, _lengths(lengths, N, "lengths"), yp, stats,
+        _at(scratch, "scratch"), scratch.nbytes, _raw_stream(stream)))
+
+
+def zero_group_norm_backward(x, dy, stats, dx, scratch, weight=None, bias=None, lengths=None,
+                             dweight=None, dbias=None, act="silu", stream=None):
+    """The gradient of zero_group_norm_forward from x and the stats it wrote: dx (None:
+    not wanted; may be dy), dweight and dbias (each may be None), which may lie in a
+    rank's gradient buffer."""
+    N, P, C_, G, stats = _group_norm_call(x, stats, None, act)
+    xp, xs = _strided_rows(x, "x")
+    dyp, ys = _strided_rows(dy, "dy", x.shape)
+    dxp = None
+    if dx is not None:
+        dxp, dxs = _strided_rows(dx, "dx", x.shape)
+        if dxs != xs:
+            raise ValueError("dx must have x's stride between positions")
+    par = _Alike((C_,), "weight and bias")
+    w, b = par(weight, "weight"), par(bias, "bias")
+    sums = _Alike((C_,), "dweight and dbias")
+    dw, db = sums(dweight, "dweight"), sums(dbias, "dbias")
+    type = _type(x, "x")
+    if _type(dy, "dy") != type or (dx is not None and _type(dx, "dx") != type):
+        raise ValueError("x, dy and dx must have one type")
+    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, par.type or ZERO_TYPE_BF16,
+                             sums.type or ZERO_TYPE_BF16, _ACTS[act], 1.0)
+    _check("zero_group_norm_backward", lib.zero_group_norm_backward(
+        C.byref(spec), xp, dyp, w, b, _lengths(lengths, N, "lengths"), stats, dxp, dw, db,
+        _at(scratch, "scratch"), scratch.nbytes, _raw_stream(stream)))
+
+
+# ------------------------------------------------- relative position bias
+def _relpos_call(scores, what, table, starts, q_lengths, k_lengths, start, max_distance,
+                 bidirectional, causal):
+    if scores.dim() != 4:
+        raise ValueError("%s must have four dimensions: batch, heads, queries, keys" % what)
+    if table.dim() != 2 or table.shape[1] != scores.shape[1]:
+        raise ValueError("the table must be buckets x heads")
+    B, H, Q, K = scores.shape
+    spec = zero_relpos_t(B, H, Q, K, start, max_distance, table.shape[0],
+                         1 if bidirectional else 0, 1 if causal else 0, _type(table, "the table"),
+                         _type(scores, what))
+    return spec, (_lengths(starts, B, "starts"), _lengths(q_lengths, B, "q_lengths"),
+                  _lengths(k_lengths, B, "k_lengths"))
+
+
+def zero_relpos_forward(table, out, scores=None, start=0, starts=None, q_lengths=None,
+                        k_lengths=None, max_distance=128, bidirectional=True, causal=False,
+                        stream=None):
+    """out[b, h, i, j] = scores[b, h, i, j] + table[bucket(j - i - start), h]; -inf for
+    later keys where causal and for keys from k_lengths[b] on; rows from q_lengths[b] on
+    are left as they are.  table (buckets x heads); out and scores (batch x heads x
+    queries x keys): bf16 or fp32, keys contiguous, rows evenly apart; scores may be None
+    (0) or out.  start: the position of query 0 among the keys; starts, q_lengths,
+    k_lengths (batch): int32."""
+    spec, of_batch = _relpos_call(out, "out", table, starts, q_lengths, k_lengths, start,
+                                  max_distance, bidirectional, causal)
+    at, stride = _strided_rows(out, "out")
+    sp, ss = (None, 0) if scores is None else _strided_rows(scores, "scores", out.shape)
+    if scores is not None and _type(scores, "scores") != spec.type:
+        raise ValueError("scores and out must have one type")
+    _check("zero_relpos_forward", lib.zero_relpos_forward(
+        C.byref(spec), _at(table, "table"), *of_batch, sp, ss, at, stride, _raw_stream(stream)))
+
+
+def zero_relpos_scratch_bytes(batch, heads, q_len, k_len, buckets):
+    return _bytes("zero_relpos_scratch_bytes", lib.zero_relpos_scratch_bytes(
+        int(batch), int(heads), int(q_len), int(k_len), int(buckets)))
+
+
+def zero_relpos_backward(dout, dtable, scratch, start=0, starts=None, q_lengths=None,
+                         k_lengths=None, max_distance=128, bidirectional=True, causal=False,
+                         accumulate=False, stream=None):
+    """dtable[v, h] = (dtable[v, h] if accumulate else 0) + the sum of dout over the places
+    with bucket v that are neither masked nor behind a length.  scratch: a device tensor
+    of zero_relpos_scratch_bytes(batch, heads, queries, keys, buckets) bytes."""
+    spec, of_batch = _relpos_call(dout, "dout", dtable, starts, q_lengths, k_lengths, start,
+                                  max_distance, bidirectional, causal)
+    at, stride = _strided_rows(dout, "dout")
+    _check("zero_relpos_backward", lib.zero_relpos_backward(
+        C.byref(spec), *of_batch, at, stride, _at(dtable, "dtable"), 1 if accumulate else 0,
+        _at(scratch, "scratch"), scratch.nbytes, _raw_stream(stream)))

@@ -972,6 +972,164 @@ int zero_distill_forward_backward(const zero_distill_t* d, const void* logits,
                                   float* kl, void* dlogits, int64_t dlogits_stride,
                                   cudaStream_t stream);
 
+/* One of many tensors: n elements at src, and where they go.  dst may be src
+ * (then with src's type); otherwise no dst may overlap any src or other dst. */
+typedef struct {
+    const void* src;
+    void* dst;        /* not looked at by zero_tensors_sqnorm */
+    int64_t n;        /* 0 .. 2^40; the addresses may be null with 0 */
+    int32_t src_type; /* ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+    int32_t dst_type;
+} zero_tensor_t;
+
+/* zero_tensors_sqnorm -- adds the sum of the squares of all tensors' elements to
+ * the per-block partials of zero_grad_sqnorm, for gradients that lie in many
+ * tensors and not in ranks' flat buffers: gradients of one replica, or disjoint
+ * shards of the averaged one.  zero_clip_coef then gives the norm and the
+ * coefficient; both calls' partials may be added up in one scratch.
+ *   tensors        host array; it may be freed when the call returns
+ *   n_tensors      any number, 0 included (1000 to a launch)
+ *   accumulate     0: the partials are set, 1: added to
+ *   scratch        zero_clip_scratch_bytes() bytes
+ * A tensor listed twice counts twice.  Squares are summed in fp32 within a
+ * thread's 64 elements and in fp64 beyond, or in fp64 alone where fp32 would
+ * overflow or underflow.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_tensors_sqnorm(const zero_tensor_t* tensors, int64_t n_tensors, int32_t accumulate,
+                        double* scratch, int64_t scratch_bytes, cudaStream_t stream);
+
+/* zero_tensors_scale -- dst = round(scale * coef * src) for every tensor, e.g.
+ * gradients into their places in a rank's flat gradient buffer.
+ *   norm_coef  device float[2] as zero_clip_coef writes it (coef is its second), or
+ *              null (1).  The factor scale * coef is rounded to fp32 first.
+ * Where dst is src and the factor is 1 nothing is read or written.
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_tensors_scale(const zero_tensor_t* tensors, int64_t n_tensors, double scale,
+                       const float* norm_coef, cudaStream_t stream);
+
+/* zero_tensors_clip -- the global norm of all tensors and the clip by it:
+ *   norm = sqrt(sum of squares), coef = min(1, max_norm / (norm + 1e-6)),
+ *   dst  = round(coef * src)
+ * the same bits as zero_tensors_sqnorm, zero_clip_coef and zero_tensors_scale in
+ * turn, in two launches (for up to 1000 tensors).  A NaN or an infinity anywhere
+ * makes norm NaN or infinite and coef NaN or 0, as zero_clip_coef.
+ *   norm_coef  device float[2], 16-byte aligned: written, norm and coef
+ *   scratch    zero_clip_scratch_bytes() bytes
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_tensors_clip(const zero_tensor_t* tensors, int64_t n_tensors, double max_norm,
+                      float* norm_coef, double* scratch, int64_t scratch_bytes,
+                      cudaStream_t stream);
+
+#define ZERO_ACT_NONE 0
+#define ZERO_ACT_SILU 1 /* z / (1 + exp(-z)) */
+#define ZERO_ACT_GELU 2 /* z * (1 + erf(z / sqrt(2))) / 2 */
+
+/* Group norm with an activation, channels last: [samples, positions, channels],
+ * the channels of a position next to one another. */
+typedef struct {
+    int64_t samples, positions; /* up to 2^30 each */
+    int64_t channels;           /* up to 16384, a multiple of groups */
+    int64_t x_stride, y_stride; /* elements between positions, of x and dx and of y and dy:
+                                   >= channels; samples are positions * stride apart */
+    int32_t groups;
+    int32_t type;               /* x, y, dy, dx: ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+    int32_t param_type;         /* weight, bias */
+    int32_t grad_type;          /* dweight, dbias */
+    int32_t act;                /* ZERO_ACT_* */
+    double eps;                 /* > 0 */
+} zero_group_norm_t;
+
+/* Bytes of scratch of either call; ZERO_EINVAL for sizes they refuse. */
+int64_t zero_group_norm_scratch_bytes(int64_t samples, int64_t positions, int64_t channels,
+                                      int32_t groups);
+
+/* zero_group_norm_forward -- for each sample and group of channels / groups
+ * neighbouring channels, over all its counted positions:
+ *   z = (x - mean) / sqrt(variance + eps) * weight + bias,  y = act(z)
+ * A sample counts its first lengths[sample] positions (all without lengths; a
+ * length is held within [0, positions]); the others are neither read nor
+ * written.
+ *   weight, bias  [channels] of param_type, or null (1, 0)
+ *   lengths       [samples] int32, or null
+ *   y             as x; may be x (then with the same stride)
+ *   stats         [samples, groups, 2] fp32, or null: mean and 1/sqrt(variance +
+ *                 eps), written (0 and 1/sqrt(eps) for a length of 0)
+ * The variance is summed about means of parts of the group: no digits are lost
+ * to a mean that is large beside it.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_group_norm_forward(const zero_group_norm_t* norm, const void* x, const void* weight,
+                            const void* bias, const int32_t* lengths, void* y, float* stats,
+                            void* scratch, int64_t scratch_bytes, cudaStream_t stream);
+
+/* zero_group_norm_backward -- the gradient of zero_group_norm_forward, from x
+ * and the stats that the forward call wrote:
+ *   h = (x - mean) * rstd, d = dy * act'(h * weight + bias)
+ *   dx = rstd * (d * weight - mean of (d * weight) - h * mean of (d * weight * h))
+ *   dweight = sum of d * h, dbias = sum of d     over samples and positions
+ *   dy       as x, positions y_stride apart
+ *   dx       as x, or null (not wanted); may be dy (then with one stride); places
+ *            behind a sample's length are left as they are
+ *   dweight, dbias  [channels] of grad_type, each or null; written, not added
+ *            (+0 without samples)
+ * eps is not used.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_group_norm_backward(const zero_group_norm_t* norm, const void* x, const void* dy,
+                             const void* weight, const void* bias, const int32_t* lengths,
+                             const float* stats, void* dx, void* dweight, void* dbias,
+                             void* scratch, int64_t scratch_bytes, cudaStream_t stream);
+
+/* The learned relative position bias by buckets.  Key j stands j - i - start
+ * places ahead of query i.  With n = the distance behind (0 for later keys) and
+ * N = buckets, or n = the distance either way and N = buckets / 2 where
+ * bidirectional, and half = N / 2 (rounded down):
+ *   bucket = n for n < half, else the lower of N - 1 and
+ *            half + floor(log(n / half) / log(max_distance / half) * (N - half))
+ *   (in whole numbers: a distance on a border belongs to the bucket it begins)
+ * plus N for later keys where bidirectional. */
+typedef struct {
+    int64_t batch, heads;   /* heads up to 65535, batch * heads up to 2^30 */
+    int64_t q_len, k_len;   /* up to 2^24 */
+    int64_t start;          /* position of query 0 among the keys, within 2^40 */
+    int64_t max_distance;   /* above half, up to 8192 */
+    int32_t buckets;        /* 2 .. 512; even and 4 or more where bidirectional */
+    int32_t bidirectional;
+    int32_t causal;         /* 1: later keys are masked */
+    int32_t table_type;     /* table, dtable: ZERO_TYPE_BF16 or ZERO_TYPE_F32 */
+    int32_t type;           /* scores, out, dout */
+} zero_relpos_t;
+
+/* zero_relpos_forward -- the bias, alone or added to attention scores:
+ *   out[b, h, i, j] = scores[b, h, i, j] + table[bucket(j - i - start), h]
+ * -inf where the key is masked: a later one where causal, or j >= k_lengths[b].
+ * Masked scores do not matter, whatever they hold.  Rows i >= q_lengths[b] and
+ * what lies between k_len and the stride are left as they are.
+ *   table      [buckets, heads] of table_type
+ *   starts     [batch] int32 in start's place, or null
+ *   q_lengths, k_lengths  [batch] int32, held within [0, q_len] and [0, k_len], or null
+ *   scores     [batch, heads, q_len, k_len], rows scores_stride apart, or null (0)
+ *   out        the same shape, rows out_stride apart; may be scores (then with one
+ *              stride).  Heads are q_len * stride apart.
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_relpos_forward(const zero_relpos_t* relpos, const void* table, const int32_t* starts,
+                        const int32_t* q_lengths, const int32_t* k_lengths, const void* scores,
+                        int64_t scores_stride, void* out, int64_t out_stride, cudaStream_t stream);
+
+/* Bytes of scratch of zero_relpos_backward; ZERO_EINVAL for sizes it refuses. */
+int64_t zero_relpos_scratch_bytes(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len,
+                                  int32_t buckets);
+
+/* zero_relpos_backward -- the gradient of zero_relpos_forward in its table:
+ *   dtable[v, h] = (accumulate ? dtable[v, h] : 0)
+ *                  + sum of dout[b, h, i, j] over the places with bucket v
+ * Masked places and rows behind q_lengths do not count, whatever they hold.  (The
+ * gradient in the scores is dout itself.)
+ *   dout        [batch, heads, q_len, k_len], rows dout_stride apart, heads q_len *
+ *               dout_stride apart
+ *   dtable      [buckets, heads] of table_type
+ *   accumulate  1: added to what is there (a table that several layers share)
+ * ZERO_EINVAL / ZERO_EALIGN / ZERO_ECUDA. */
+int zero_relpos_backward(const zero_relpos_t* relpos, const int32_t* starts,
+                         const int32_t* q_lengths, const int32_t* k_lengths, const void* dout,
+                         int64_t dout_stride, void* dtable, int32_t accumulate, void* scratch,
+                         int64_t scratch_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
