@@ -83,23 +83,43 @@ __device__ __forceinline__ int bucket_of(const Borders& B, int distance)
 // ------------------------------------------------------------------ forward
 constexpr int kThreads = 256;
 
-// The bias by distance in shared memory, d from -last to last (to 0 where later
-// keys share bucket 0): a word of padding every eight, so that threads that read
-// eight places each, eight apart, meet different banks.
-__host__ __device__ __forceinline__ int padded(int i) { return i + (i >> 3); }
+// The bias by distance in shared memory: place k stands for the distance k - 8 - last,
+// held within [-last, last] (or [-last, 0] where later keys share bucket 0), so that a
+// vector anywhere reads eight places in a row, far ones the end values.  kCopies = 4:
+// copy a begins at place a, so eight places from any k on are two aligned 16-byte
+// reads of copy k mod 4 (against eight words of one copy, four of which meet in a
+// bank).  Lines of more than kMostCopied distances have one copy.
+constexpr int kMostCopied = 2048;
+__host__ __device__ __forceinline__ int line_places(int span) { return (span + 20) / 4 * 4; }
 
 __device__ __forceinline__ int clamped(int64_t x, int lo, int hi)
 {
     return x < lo ? lo : x > hi ? hi : static_cast<int>(x);
 }
 
-template <typename T>
+template <int kCopies>
+__device__ __forceinline__ void read_line(const float* line, int places, int k, float (&x)[8])
+{
+    if constexpr (kCopies == 4) {
+        const int copy = k & 3;
+        const auto* p = reinterpret_cast<const float4*>(line + copy * places + (k - copy));
+        const float4 a = p[0], b = p[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = line[k + e];
+    }
+}
+
+template <typename T, bool kScores, int kCopies>
 __global__ void __launch_bounds__(kThreads)
 forward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borders B,
                const void* __restrict__ table, int32_t table_type, const T* scores, T* out,
                int lanes_log2, int rows_per_block, int tiles, int same_lead)
 {
-    extern __shared__ float line[];
+    extern __shared__ __align__(16) float line[];
+    constexpr int kAhead = kScores ? 4 : 1; // vectors of a thread in flight
     const int64_t plane = blockIdx.x / tiles;
     const int h = static_cast<int>(plane % G.heads), b = static_cast<int>(plane / G.heads);
     const int rows = length_of(G.q_lengths, b, G.q_len);
@@ -110,70 +130,71 @@ forward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borde
     const int64_t start = start_of(G, b);
     const int last = B.at[B.n - 1];
     const int span = B.both ? 2 * last : last;
-    for (int i = threadIdx.x; i <= span; i += kThreads) {
-        const int d = i - last;
+    const int places = line_places(span);
+    for (int k = threadIdx.x; k < places; k += kThreads) {
+        const int d = min(max(k - 8, 0), span) - last;
         const int bucket = bucket_of(B, d < 0 ? -d : d) + (d > 0 ? B.n : 0);
         float x[1];
         dev::load_any<1>(table, table_type, static_cast<int64_t>(bucket) * G.heads + h, x);
-        line[padded(i)] = x[0];
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+            if (k >= c) line[c * places + k - c] = x[0];
     }
     __syncthreads();
-    const float first_value = line[0], last_value = line[padded(span)];
 
     const int lanes = 1 << lanes_log2;
     const int lane = threadIdx.x & (lanes - 1);
     for (int i = row0 + (threadIdx.x >> lanes_log2); i < row1; i += kThreads >> lanes_log2) {
         T* o = out + plane * G.out_plane + i * G.out_stride;
-        const T* s = scores ? scores + plane * G.in_plane + i * G.in_stride : nullptr;
+        const T* s = kScores ? scores + plane * G.in_plane + i * G.in_stride : nullptr;
         const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(o) & 15u) / sizeof(T));
         const int64_t at = start + i; // the query's position
-        // columns from `end` on are masked; columns up to `near` are at distance -last or
-        // beyond, those from `far` on at last or beyond (any later key where they share a bucket)
-        const int end = G.causal ? clamped(at + 1, 0, keys) : keys;
-        const int near = clamped(at - last, -8, G.k_len);
-        const int far = clamped(B.both ? at + last : at, -8, G.k_len);
-        for (int j0 = lane * 8 - lead; j0 < G.k_len; j0 += 8 * lanes) {
-            const bool whole = j0 >= 0 && j0 + 8 <= G.k_len;
-            float x[8];
-            if (j0 >= end) {
+        const int end = G.causal ? clamped(at + 1, 0, keys) : keys; // masked from here on
+        const int place = clamped(8 + last - at, -(1 << 29), 1 << 29); // of column 0
+        for (int c = lane * 8 - lead; c < G.k_len; c += kAhead * 8 * lanes) {
+            Raw8<T> raw[kAhead];
+            if (kScores && same_lead) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = -INFINITY;
-            } else {
-                if (j0 + 7 <= near || j0 >= far) {
-                    const float v = j0 >= far ? last_value : first_value;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = v;
-                } else {
-                    const int d = clamped(j0 - at + last, -8, span + 1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = line[padded(min(max(d + e, 0), span))];
-                }
-                if (s) {
-                    if (whole && same_lead && j0 + 8 <= end) {
-                        Raw8<T> r;
-                        dev::stream_raw8(s + j0, r);
-                        float y[8];
-                        dev::unpack8(r, y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] += y[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (j0 + e >= 0 && j0 + e < end) x[e] += dev::load1(s + j0 + e);
-                    }
-                }
-                if (j0 + 8 > end) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (j0 + e >= end) x[e] = -INFINITY;
+                for (int k = 0; k < kAhead; ++k) {
+                    const int j0 = c + k * 8 * lanes;
+                    if (j0 >= 0 && j0 + 8 <= end) dev::stream_raw8(s + j0, raw[k]);
                 }
             }
-            if (whole) {
-                dev::store8_stream(o + j0, x);
-            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (j0 + e >= 0 && j0 + e < G.k_len) dev::store1(o + j0 + e, x[e]);
+            for (int k = 0; k < kAhead; ++k) {
+                const int j0 = c + k * 8 * lanes;
+                if (j0 >= G.k_len) break;
+                float x[8];
+                if (j0 >= end) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = -INFINITY;
+                } else {
+                    read_line<kCopies>(line, places, min(max(j0 + place, 0), span + 9), x);
+                    if (kScores) {
+                        if (same_lead && j0 >= 0 && j0 + 8 <= end) {
+                            float y[8];
+                            dev::unpack8(raw[k], y);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] += y[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (j0 + e >= 0 && j0 + e < end) x[e] += dev::load1(s + j0 + e);
+                        }
+                    }
+                    if (j0 + 8 > end) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (j0 + e >= end) x[e] = -INFINITY;
+                    }
+                }
+                if (j0 >= 0 && j0 + 8 <= G.k_len) {
+                    dev::store8_stream(o + j0, x);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (j0 + e >= 0 && j0 + e < G.k_len) dev::store1(o + j0 + e, x[e]);
+                }
             }
         }
     }
@@ -204,10 +225,51 @@ __device__ __forceinline__ void add_diagonals(const float (&x)[8], float (&acc)[
     for (int e = 0; e < 8; ++e) acc[e - kPhase + 7] += x[e];
 }
 
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* p)
+{
+    return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+// Elements f .. l - 1 of a vector, +0 in the place of the others.
+__device__ __forceinline__ uint32_t keep_pair(uint32_t w, int e, int f, int l)
+{
+    return w & ((e >= f && e < l ? 0xFFFFu : 0u) | (e + 1 >= f && e + 1 < l ? 0xFFFF0000u : 0u));
+}
+__device__ __forceinline__ void keep_inside(Raw8<Bf16>& r, int f, int l)
+{
+    r.a = make_uint4(keep_pair(r.a.x, 0, f, l), keep_pair(r.a.y, 2, f, l), keep_pair(r.a.z, 4, f, l),
+                     keep_pair(r.a.w, 6, f, l));
+}
+__device__ __forceinline__ void keep_inside(Raw8<float>& r, int f, int l)
+{
+    auto keep = [&](float x, int e) { return e >= f && e < l ? x : 0.0f; };
+    r.a = make_float4(keep(r.a.x, 0), keep(r.a.y, 1), keep(r.a.z, 2), keep(r.a.w, 3));
+    r.b = make_float4(keep(r.b.x, 4), keep(r.b.y, 5), keep(r.b.z, 6), keep(r.b.w, 7));
+}
+// The elements of a vector at column j0 that lie in columns 0 .. keys - 1, one by one.
+__device__ __forceinline__ void load_inside(const Bf16* at, int j0, int keys, Raw8<Bf16>& r)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t b = j0 + e >= 0 && j0 + e < keys ? at[e].bits : 0u;
+        w[e / 2] = e % 2 ? w[e / 2] | b << 16 : b;
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load_inside(const float* at, int j0, int keys, Raw8<float>& r)
+{
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = j0 + e >= 0 && j0 + e < keys ? at[e] : 0.0f;
+    r.a = make_float4(x[0], x[1], x[2], x[3]);
+    r.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+
 // kAligned: every row starts at a 16-byte boundary, so that a row's place in its
 // group is its phase.
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 3 : 2)
 backward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borders B,
                 const __grid_constant__ Split S, const T* __restrict__ dout,
                 const T* __restrict__ dout_end, float* __restrict__ partial)
@@ -231,7 +293,8 @@ backward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Bord
 #pragma unroll
     for (int k = 0; k < kSums; ++k) acc[k] = 0.0f;
 
-    // the sums of the diagonals to the sums of their buckets
+    // the sums of the diagonals to the sums of their buckets: a thread takes a bucket of a
+    // few diagonals, a warp one of many
     auto flush = [&](int64_t octets_before) {
         float* mine = diag[warp];
         if (lane < 7) mine[lane] = 0.0f;
@@ -254,7 +317,7 @@ backward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Bord
         }
         __syncthreads();
         constexpr int64_t kFar = int64_t(1) << 60;
-        for (int q = warp; q < S.buckets; q += kWarps) {
+        auto interval = [&](int q, int& t0, int& t1) {
             int64_t from, to; // the bucket's diagonals
             if (q < B.n) {
                 from = q + 1 < B.n ? 1 - static_cast<int64_t>(B.at[q + 1]) : -kFar;
@@ -263,13 +326,29 @@ backward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Bord
                 from = B.at[q - B.n] > 1 ? B.at[q - B.n] : 1;
                 to = q - B.n + 1 < B.n ? B.at[q - B.n + 1] : kFar;
             }
-            const int t0 = clamped(from - d0, 0, kBand), t1 = clamped(to - d0, 0, kBand);
-            if (t0 >= t1) continue;
-            float x = 0.0f;
-            for (int t = t0 + lane; t < t1; t += 32) x += total[t];
+            t0 = clamped(from - d0, 0, kBand);
+            t1 = clamped(to - d0, 0, kBand);
+        };
+        // buckets q0 .. q0 + 31 are this warp's, lane by lane
+        for (int q0 = 32 * warp; q0 < S.buckets; q0 += 32 * kWarps) {
+            int t0 = 0, t1 = 0;
+            if (q0 + lane < S.buckets) interval(q0 + lane, t0, t1);
+            if (t1 - t0 <= 16) {
+                float x = 0.0f;
+                for (int t = t0; t < t1; ++t) x += total[t];
+                if (t0 < t1) sums[q0 + lane] += x;
+            }
+            unsigned many = __ballot_sync(0xFFFFFFFFu, t1 - t0 > 16);
+            while (many) {
+                const int l = __ffs(many) - 1;
+                many &= many - 1;
+                const int from = __shfl_sync(0xFFFFFFFFu, t0, l), to = __shfl_sync(0xFFFFFFFFu, t1, l);
+                float x = 0.0f;
+                for (int t = from + lane; t < to; t += 32) x += total[t];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-            if (lane == 0) sums[q] += x;
+                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+                if (lane == 0) sums[q0 + l] += x;
+            }
         }
     };
 
@@ -290,61 +369,63 @@ backward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Bord
         g1 = min(g1, g0 + S.groups_per_part);
         for (int g = g0 + warp; g < g1; g += kWarps) {
             const int i0 = 8 * g - r;
-            Raw8<T> raw[8] = {};
-            int lead[8];
-            unsigned edge = 0; // bit k: not all of vector k counts; bit 8 + k: not loaded
+            const T* first = plane + i0 * G.in_stride; // row i0, where there is one
+            Raw8<T> raw[8];
+            int place[8]; // of a row: its lead and its place in the group, phase and carry
+            // All eight rows' vectors whole in all lanes: no checks.  A row's lead may
+            // move its vectors by one.
+            const int u0 = low + g, u1 = u0 + 31 + (kAligned ? 0 : 1);
+            const bool inner = i0 >= 0 && i0 + 8 <= rows && u0 >= (kAligned ? 0 : 1) &&
+                               8 * u1 + 8 <= keys && (!G.causal || low + 31 <= octets_before);
+            if (inner) {
+                const T* at = first + 8 * (slot + g);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = i0 + k;
-                const T* row = plane + i * G.in_stride;
-                lead[k] = kAligned ? 0
-                                   : static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) /
-                                                      sizeof(T));
-                const int u = slot + (8 * g + k + lead[k]) / 8;
-                const int j0 = 8 * u - lead[k];
-                if (counted && i >= 0 && i < rows && u >= 0 && j0 < keys) {
-                    if (j0 < 0 || j0 + 8 > keys) edge |= 1u << k;
-                    if (row + j0 >= dout && row + j0 + 8 <= dout_end)
-                        dev::stream_raw8(row + j0, raw[k]);
-                    else
-                        edge |= 256u << k; // not all of it is the tensor's
+                for (int k = 0; k < 8; ++k, at += G.in_stride) {
+                    const int lead = kAligned ? 0 : lead_of(at);
+                    place[k] = k + lead;
+                    dev::stream_raw8(kAligned ? at : at - lead + (place[k] & 8), raw[k]);
+                }
+            } else {
+                unsigned edge = 0; // bit k: not all of vector k counts
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const T* row = first + k * G.in_stride;
+                    const int lead = kAligned ? 0 : lead_of(row);
+                    place[k] = k + lead;
+                    const int u = slot + g + (place[k] >> 3);
+                    const int j0 = 8 * u - lead;
+                    raw[k] = Raw8<T>{};
+                    if (counted && i0 + k >= 0 && i0 + k < rows && u >= 0 && j0 < keys) {
+                        if (j0 < 0 || j0 + 8 > keys) edge |= 1u << k;
+                        const T* at = row + j0;
+                        if (at >= dout && at + 8 <= dout_end)
+                            dev::stream_raw8(at, raw[k]);
+                        else // not all of it is the tensor's
+                            load_inside(at, j0, keys, raw[k]);
+                    }
+                }
+                if (__any_sync(0xFFFFFFFFu, edge)) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (edge & (1u << k)) {
+                            const int j0 = 8 * (slot + g + (place[k] >> 3)) - (place[k] - k);
+                            keep_inside(raw[k], -j0, keys - j0);
+                        }
                 }
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 float x[8];
                 dev::unpack8(raw[k], x);
-                if (edge & (257u << k)) {
-                    const T* row = plane + (i0 + k) * G.in_stride;
-                    const int j0 = 8 * (slot + (8 * g + k + lead[k]) / 8) - lead[k];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const bool in = j0 + e >= 0 && j0 + e < keys;
-                        x[e] = !in ? 0.0f : edge & (256u << k) ? dev::load1(row + j0 + e) : x[e];
-                    }
-                }
-                if constexpr (kAligned) {
-                    switch (k) { // known at compile time
-                    case 0: add_diagonals<0>(x, acc); break;
-                    case 1: add_diagonals<1>(x, acc); break;
-                    case 2: add_diagonals<2>(x, acc); break;
-                    case 3: add_diagonals<3>(x, acc); break;
-                    case 4: add_diagonals<4>(x, acc); break;
-                    case 5: add_diagonals<5>(x, acc); break;
-                    case 6: add_diagonals<6>(x, acc); break;
-                    default: add_diagonals<7>(x, acc);
-                    }
-                } else {
-                    switch ((k + lead[k]) & 7) { // the same in all lanes
-                    case 0: add_diagonals<0>(x, acc); break;
-                    case 1: add_diagonals<1>(x, acc); break;
-                    case 2: add_diagonals<2>(x, acc); break;
-                    case 3: add_diagonals<3>(x, acc); break;
-                    case 4: add_diagonals<4>(x, acc); break;
-                    case 5: add_diagonals<5>(x, acc); break;
-                    case 6: add_diagonals<6>(x, acc); break;
-                    default: add_diagonals<7>(x, acc);
-                    }
+                switch (kAligned ? k : place[k] & 7) { // the same in all lanes
+                case 0: add_diagonals<0>(x, acc); break;
+                case 1: add_diagonals<1>(x, acc); break;
+                case 2: add_diagonals<2>(x, acc); break;
+                case 3: add_diagonals<3>(x, acc); break;
+                case 4: add_diagonals<4>(x, acc); break;
+                case 5: add_diagonals<5>(x, acc); break;
+                case 6: add_diagonals<6>(x, acc); break;
+                default: add_diagonals<7>(x, acc);
                 }
             }
         }
@@ -494,20 +575,25 @@ int launch_forward(const Geometry& G, const Borders& B, const void* table, int32
     const int64_t tiles = (G.q_len + rows - 1) / rows;
     const int64_t blocks = tiles * G.batch * G.heads;
     if (blocks > 0x7FFFFFFF) return ZERO_EINVAL;
-    const int same = ((reinterpret_cast<uintptr_t>(scores) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
+    const int same = scores && ((reinterpret_cast<uintptr_t>(scores) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
                      (G.in_stride - G.out_stride) % kUnit == 0 &&
                      (G.in_plane - G.out_plane) % kUnit == 0;
     const int last = B.at[B.n - 1];
-    auto bytes_of = [](int64_t span) { return static_cast<size_t>(padded(static_cast<int>(span)) + 1) * 4; };
-    if (!allow_shared(reinterpret_cast<const void*>(forward_kernel<T>), bytes_of(2 * kMaxDistance)))
-        return ZERO_ECUDA;
-    forward_kernel<T><<<static_cast<unsigned>(blocks), kThreads, bytes_of(B.both ? 2 * last : last), stream>>>(
-        G, B, table, table_type, static_cast<const T*>(scores), static_cast<T*>(out), log2,
-        static_cast<int>(rows), static_cast<int>(tiles), same);
-    return cuda_status(cudaGetLastError());
+    const int span = B.both ? 2 * last : last;
+    const int copies = span <= kMostCopied ? 4 : 1;
+    auto start = [&](auto kernel) {
+        const size_t most = 4 * static_cast<size_t>(line_places(copies == 4 ? kMostCopied : 2 * kMaxDistance)) * copies;
+        if (!allow_shared(reinterpret_cast<const void*>(kernel), most)) return ZERO_ECUDA;
+        kernel<<<static_cast<unsigned>(blocks), kThreads, 4 * static_cast<size_t>(line_places(span)) * copies,
+                 stream>>>(G, B, table, table_type, static_cast<const T*>(scores), static_cast<T*>(out),
+                           log2, static_cast<int>(rows), static_cast<int>(tiles), same);
+        return cuda_status(cudaGetLastError());
+    };
+    if (scores) return copies == 4 ? start(forward_kernel<T, true, 4>) : start(forward_kernel<T, true, 1>);
+    return copies == 4 ? start(forward_kernel<T, false, 4>) : start(forward_kernel<T, false, 1>);
 }
 
-constexpr int64_t kWanted = 152 * 3 * 4; // blocks: four rounds of those that are resident
+constexpr int64_t kResident = 152 * 3; // blocks at once
 
 // The split of a call's work: by its sizes alone (with a causal mask also by start).
 Split split(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len, int32_t buckets,
@@ -527,13 +613,12 @@ Split split(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len, int32_t 
     // groups that meet one band
     const int64_t meet = std::min<int64_t>(S.groups, vectors + 32);
     const int64_t planes = heads * S.bands * batch;
-    int64_t parts = planes >= kWanted ? 1 : (kWanted + planes - 1) / planes;
-    if (parts > (meet + 2 * kWarps - 1) / (2 * kWarps)) parts = (meet + 2 * kWarps - 1) / (2 * kWarps);
+    // at least two rounds of blocks where that leaves a warp four groups, and 16 at most
+    int64_t parts = (2 * kResident + planes - 1) / planes;
+    parts = std::max<int64_t>(1, std::min<int64_t>(parts, meet / (4 * kWarps)));
     S.groups_per_part = static_cast<int32_t>((meet + parts - 1) / parts);
     S.group_parts = static_cast<int32_t>((meet + S.groups_per_part - 1) / S.groups_per_part);
-    int64_t per = planes / kWanted;
-    if (per < 1) per = 1;
-    if (per > batch) per = batch;
+    const int64_t per = std::min<int64_t>(batch, std::max<int64_t>(1, planes / (8 * kResident)));
     S.batch_per_part = static_cast<int32_t>(per);
     S.batch_parts = static_cast<int32_t>((batch + per - 1) / per);
     S.parts = S.bands * S.group_parts * S.batch_parts;
@@ -541,13 +626,14 @@ Split split(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len, int32_t 
 }
 
 // The most parts of a head that split() gives for these sizes.  With p = heads * bands *
-// batch below kWanted they are bands * batch * ceil(kWanted / p) at most, so less than
-// kWanted / heads + bands * batch, and bands * batch is less than kWanted / heads; from
-// kWanted on they are bands * ceil(batch / floor(p / kWanted)), which is less than
-// 2 * kWanted / heads + bands.  A causal mask leaves fewer bands.
+// batch below 2 * kResident they are bands * batch * ceil(2 * kResident / p) at most, less
+// than 4 * kResident / heads; up to 16 * kResident they are bands * batch; beyond, bands *
+// ceil(batch / floor(p / (8 * kResident))), less than 16 * kResident / heads + bands.  A
+// causal mask leaves fewer bands.
 int64_t most_parts(int64_t batch, int64_t heads, int64_t q_len, int64_t k_len, int32_t buckets)
 {
-    return 2 * ((kWanted + heads - 1) / heads) + split(batch, heads, q_len, k_len, buckets, false, 0).bands + 2;
+    return (16 * kResident + heads - 1) / heads +
+           split(batch, heads, q_len, k_len, buckets, false, 0).bands + 1;
 }
 
 template <typename T>
