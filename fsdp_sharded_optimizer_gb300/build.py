@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_lib", "obj")
 LIB = os.path.join(PKG, "_lib", "libzero.so")
 
 CUDA_SOURCES = ["fused_step.cu", "gather.cu", "gen.cu", "clip.cu", "noalloc.cu", "reshard.cu",
-                "embed.cu", "block_norm.cu", "distill.cu", "tensors.cu", "group_norm.cu", "relpos.cu"]
+                "embed.cu", "block_norm.cu", "distill.cu", "tensors.cu", "group_norm.cu", "group_norm_passes.cu",
+                "group_norm_single.cu", "relpos.cu"]
 HOST_SOURCES = ["host.cpp", "zero3_sched.cpp", "graph.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
