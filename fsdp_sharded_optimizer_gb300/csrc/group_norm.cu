@@ -149,7 +149,8 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
     words += channel_words(H);
     const Segments S = segments_at(H, 2, words);
     float2* group_stats = reinterpret_cast<float2*>(words + segment_words(H, 2));
-    float2* group_means = group_stats + H.slab_groups;
+    float2* next_stats = group_stats + H.slab_groups; // they change places
+    float2* group_means = next_stats + H.slab_groups;
     float* weights = reinterpret_cast<float*>(group_means + H.slab_groups);
     float* biases = weights + H.width;
 
@@ -167,7 +168,7 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
     };
     auto copy_stats = [&](int sample) {
         const float2* of = stats + static_cast<int64_t>(sample) * H.groups + slab * H.slab_groups;
-        for (int g = threadIdx.x; g < H.slab_groups; g += kThreads) group_stats[g] = __ldg(of + g);
+        for (int g = threadIdx.x; g < H.slab_groups; g += kThreads) next_stats[g] = __ldg(of + g);
     };
     int n = blockIdx.x / H.slabs; // less than samples
     Here next = here_of<kFlat>(H, n, x, rg, lane, 0);
@@ -179,11 +180,14 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
     bool first = true;
     for (; n < H.samples; n += step) {
         const Here h = next;
-        float2 minus_mean[4], rstd[4], w[4];
+        float2* const old = group_stats;
+        group_stats = next_stats;
+        next_stats = old;
+        float2 minus_mean[4], a[4];
         copies_here();
         if (rg < H.row_groups) {
             float2 b[4], s[4], q[4];
-            backward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, rstd, w, b);
+            forward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, a, b);
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i] = q[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 2
@@ -195,7 +199,7 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
                 read_slot(place, rd);
                 dev::unpack8(rx, v);
                 dev::unpack8(rd, d);
-                form_d<kAct>(v, d, minus_mean, rstd, w, b);
+                form_d<kAct>(v, d, minus_mean, a, b);
                 if (kFlat && !whole<kFlat>(H, h, k))
                     outside(H, h, k, [&](int e) { of_pair(v, e) = of_pair(d, e) = 0.0f; });
                 place[0] = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
@@ -206,8 +210,8 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
                     q[i] = dev::fma2(d[i], v[i], q[i]);
                 }
             }
+            put_weighed<kFlat>(H, h, lane, weights, group_stats, s, q, S);
             add_channels(H, C, rg, lane, kFlat || first, s, q);
-            put_weighed<kFlat>(H, h, lane, s, q, w, S);
         }
         first = false;
         __syncthreads();
@@ -223,8 +227,8 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
         const int rows2 = more ? next.rows : 0;
         if (more) copy_stats(n + step);
         if (dx && rg < H.row_groups) {
-            float2 wr[4], s1[4], s2[4];
-            result_factors<kFlat>(H, h, lane, group_means, rstd, w, wr, s1, s2);
+            float2 rstd[4], s1[4], s2[4];
+            result_factors<kFlat>(H, h, lane, group_stats, group_means, rstd, s1, s2);
 #pragma unroll 2
             for (int k = 0; k < h.rows; ++k) {
                 Raw8<T> raw;
@@ -238,7 +242,7 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     v[i] = dev::fma2(dev::mul2(dev::add2(v[i], minus_mean[i]), rstd[i]), s2[i],
-                                     dev::fma2(d[i], wr[i], s1[i]));
+                                     dev::fma2(d[i], a[i], s1[i]));
                 store_row<kFlat>(H, h, k, out, H.x_sample, H.x_stride, v);
                 if (k < rows2) copy(next, k);
             }
@@ -266,7 +270,7 @@ sum_blocks_kernel(const __grid_constant__ Layout H, const float2* __restrict__ b
 int64_t held_words(const Layout& H, bool backward)
 {
     return (backward ? channel_words(H) : 0) + segment_words(H, backward ? 2 : 3) + 2 * H.width +
-           2 * H.slab_groups * (backward ? 2 : 1);
+           2 * H.slab_groups * (backward ? 3 : 1);
 }
 int64_t slot_bytes(int32_t type, bool backward)
 {
@@ -496,7 +500,7 @@ extern "C" int zero_group_norm_backward(const zero_group_norm_t* norm, const voi
         const int status = norm->type == ZERO_TYPE_BF16 ? gn::backward_by_act<gn::Bf16>(c, p)
                                                         : gn::backward_by_act<float>(c, p);
         if (status != ZERO_OK || (!dweight && !dbias)) return status;
-        return gn::launch(true, gn::sum_blocks_kernel, (norm->channels + 31) / 32, 0, stream, p.H, static_cast<const float2*>(scratch),
+        return gn::launch(true, gn::sum_blocks_kernel, (norm->channels + gn::kSumChannels - 1) / gn::kSumChannels, 0, stream, p.H, static_cast<const float2*>(scratch),
                           static_cast<int>(p.grid / p.H.slabs), dweight, dbias, norm->grad_type);
     }
     return any && gn::passes_take(c) ? gn::passes_backward(c) : gn::single_backward(c);

@@ -54,17 +54,32 @@ __device__ __forceinline__ float2 sigmoid2(float2 z)
     const float2 d = dev::add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), dev::pair(1.0f));
     return make_float2(reciprocal_fast(d.x), reciprocal_fast(d.y));
 }
-__device__ __forceinline__ float2 normal_cdf2(float2 z)
+// The normal distribution's density and cumulative probability: Abramowitz and Stegun, 26.2.17
+// (absolute error below 7.5e-8), which needs one exponential for both.
+__device__ __forceinline__ void normal2(float2 z, float2& density, float2& cdf)
 {
-    const float2 t = dev::mul2(z, dev::pair(0.70710678f));
-    return dev::fma2(make_float2(erff(t.x), erff(t.y)), dev::pair(0.5f), dev::pair(0.5f));
+    const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+    const float2 r = dev::fma2(a, dev::pair(0.2316419f), dev::pair(1.0f));
+    const float2 t = make_float2(reciprocal_fast(r.x), reciprocal_fast(r.y));
+    const float2 e = dev::mul2(dev::mul2(z, z), dev::pair(-0.5f * kLog2e));
+    density = dev::mul2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), dev::pair(0.39894228f));
+    float2 p = dev::fma2(t, dev::pair(1.330274429f), dev::pair(-1.821255978f));
+    p = dev::fma2(p, t, dev::pair(1.781477937f));
+    p = dev::fma2(p, t, dev::pair(-0.356563782f));
+    p = dev::mul2(dev::fma2(p, t, dev::pair(0.319381530f)), t);
+    const float2 tail = dev::mul2(p, density);
+    cdf = make_float2(z.x > 0.0f ? 1.0f - tail.x : tail.x, z.y > 0.0f ? 1.0f - tail.y : tail.y);
 }
 
 template <int kAct>
 __device__ __forceinline__ float2 activated2(float2 z)
 {
     if constexpr (kAct == ZERO_ACT_SILU) return dev::mul2(z, sigmoid2(z));
-    if constexpr (kAct == ZERO_ACT_GELU) return dev::mul2(z, normal_cdf2(z));
+    if constexpr (kAct == ZERO_ACT_GELU) {
+        float2 density, cdf;
+        normal2(z, density, cdf);
+        return dev::mul2(z, cdf);
+    }
     return z;
 }
 template <int kAct>
@@ -75,9 +90,9 @@ __device__ __forceinline__ float2 slope2(float2 z)
         return dev::mul2(p, dev::fma2(z, dev::fma2(p, dev::pair(-1.0f), dev::pair(1.0f)), dev::pair(1.0f)));
     }
     if constexpr (kAct == ZERO_ACT_GELU) {
-        const float2 t = dev::mul2(dev::mul2(z, z), dev::pair(-0.5f * kLog2e));
-        const float2 density = dev::mul2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), dev::pair(0.39894228f));
-        return dev::fma2(z, density, normal_cdf2(z));
+        float2 density, cdf;
+        normal2(z, density, cdf);
+        return dev::fma2(z, density, cdf);
     }
     return dev::pair(1.0f);
 }
@@ -352,36 +367,44 @@ __device__ __forceinline__ void sum_rows(const Layout& H, const Here& h, int rg,
     float2 shift[4], s[4], q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) shift[i] = s[i] = q[i] = make_float2(0.0f, 0.0f);
-    for (int k = 0; k < h.rows; k += kAhead) {
+    auto add = [&](int k, const Raw8<T>& raw) {
+        float2 v[4];
+        dev::unpack8(raw, v);
+        if (kFlat && !whole<kFlat>(H, h, k)) outside(H, h, k, [&](int e) { of_pair(v, e) = of_pair(shift, e); });
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 d = dev::fma2(shift[j], dev::pair(-1.0f), v[j]);
+            s[j] = dev::add2(s[j], d);
+            q[j] = dev::fma2(d, d, q[j]);
+        }
+    };
+    int k = 0;
+    if (h.rows > 0) {
+        Raw8<T> raw;
+        fetch(0, raw);
+        dev::unpack8(raw, shift);
+        if (kFlat && !whole<kFlat>(H, h, 0)) { // in the place of what is not the sample's: the next row's
+            float2 next[4] = {};
+            if (h.rows > 1) {
+                Raw8<T> second = {};
+                fetch(1, second);
+                dev::unpack8(second, next);
+            }
+            const int b = value_of(H, h, 1);
+            outside(H, h, 0, [&](int e) { of_pair(shift, e) = h.rows > 1 && b + e < h.total ? of_pair(next, e) : 0.0f; });
+        }
+    }
+    for (; k + kAhead <= h.rows; k += kAhead) {
         Raw8<T> raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (k + i < h.rows) fetch(k + i, raw[i]);
-        if (k == 0) {
-            dev::unpack8(raw[0], shift);
-            if (kFlat && !whole<kFlat>(H, h, 0)) { // in the place of what is not the sample's: the next row's
-                float2 next[4];
-                dev::unpack8(raw[kAhead > 1 ? 1 : 0], next);
-                const int b = value_of(H, h, 1);
-                outside(H, h, 0, [&](int e) {
-                    of_pair(shift, e) = kAhead > 1 && h.rows > 1 && b + e < h.total ? of_pair(next, e) : 0.0f;
-                });
-            }
-        }
+        for (int i = 0; i < kAhead; ++i) fetch(k + i, raw[i]);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k + i >= h.rows) break;
-            float2 v[4];
-            dev::unpack8(raw[i], v);
-            if (kFlat && !whole<kFlat>(H, h, k + i))
-                outside(H, h, k + i, [&](int e) { of_pair(v, e) = of_pair(shift, e); });
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 d = dev::fma2(shift[j], dev::pair(-1.0f), v[j]);
-                s[j] = dev::add2(s[j], d);
-                q[j] = dev::fma2(d, d, q[j]);
-            }
-        }
+        for (int i = 0; i < kAhead; ++i) add(k + i, raw[i]);
+    }
+    for (; k < h.rows; ++k) {
+        Raw8<T> raw;
+        fetch(k, raw);
+        add(k, raw);
     }
     if (rg >= H.row_groups) return;
     const float count = static_cast<float>(h.rows), inv = h.rows > 0 ? 1.0f / count : 0.0f;
@@ -485,87 +508,62 @@ __device__ __forceinline__ void forward_factors(const Layout& H, const Here& h, 
         of_pair(b, e) = biases[at.c];
     }
 }
-template <bool kFlat>
-__device__ __forceinline__ void backward_factors(const Layout& H, const Here& h, int lane, const float* weights,
-                                                 const float* biases, const float2* stats, float2 (&minus_mean)[4],
-                                                 float2 (&rstd)[4], float2 (&w)[4], float2 (&b)[4])
-{
-    GroupWalk<kFlat> at(H, h, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e, at.next(H)) {
-        const float2 st = stats[at.g];
-        of_pair(minus_mean, e) = -st.x;
-        of_pair(rstd, e) = st.y;
-        of_pair(w, e) = weights[at.c];
-        of_pair(b, e) = biases[at.c];
-    }
-}
-
-// h = (x - mean) * rstd in v's place, d = dy * slope in d's.
+// The same for the gradient's sums; a = weight * rstd.
 template <int kAct>
 __device__ __forceinline__ void form_d(float2 (&v)[4], float2 (&d)[4], const float2 (&minus_mean)[4],
-                                       const float2 (&rstd)[4], const float2 (&w)[4], const float2 (&b)[4])
+                                       const float2 (&a)[4], const float2 (&b)[4])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = dev::mul2(dev::add2(v[i], minus_mean[i]), rstd[i]);
-        if (kAct) d[i] = dev::mul2(d[i], slope2<kAct>(dev::fma2(v[i], w[i], b[i])));
+    for (int i = 0; i < 4; ++i) { // x - mean in v's place, d in dy's
+        v[i] = dev::add2(v[i], minus_mean[i]);
+        if (kAct) d[i] = dev::mul2(d[i], slope2<kAct>(dev::fma2(v[i], a[i], b[i])));
     }
 }
 
-// The factors of dx = rstd (d w - s1 - h s2) = d (rstd w) - rstd s1 - h (rstd s2).
+// The factors of dx = rstd (d w - s1 - h s2) = d a - rstd s1 - ((x - mean) rstd) (rstd s2).
 template <bool kFlat>
-__device__ __forceinline__ void result_factors(const Layout& H, const Here& h, int lane, const float2* means,
-                                               const float2 (&rstd)[4], const float2 (&w)[4], float2 (&wr)[4],
-                                               float2 (&s1)[4], float2 (&s2)[4])
+__device__ __forceinline__ void result_factors(const Layout& H, const Here& h, int lane, const float2* stats,
+                                               const float2* means, float2 (&rstd)[4], float2 (&s1)[4], float2 (&s2)[4])
 {
     GroupWalk<kFlat> at(H, h, lane);
 #pragma unroll
     for (int e = 0; e < 8; ++e, at.next(H)) {
+        const float r = stats[at.g].y;
         const float2 m = means[at.g];
-        of_pair(s1, e) = -m.x;
-        of_pair(s2, e) = -m.y;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        wr[i] = dev::mul2(w[i], rstd[i]);
-        s1[i] = dev::mul2(s1[i], rstd[i]);
-        s2[i] = dev::mul2(s2[i], rstd[i]);
+        of_pair(rstd, e) = r;
+        of_pair(s1, e) = -m.x * r;
+        of_pair(s2, e) = -m.y * r;
     }
 }
 
-// A thread's sums of d (s) and d * h (q), weighed, as the sums (a, b) of its segments.
+// A thread's sums of d (s) and d * (x - mean) (q): the latter to those of d * h, and both,
+// weighed, as the sums (a, b) of its segments.
 template <bool kFlat>
-__device__ __forceinline__ void put_weighed(const Layout& H, const Here& h, int lane, float2 (&s)[4], float2 (&q)[4],
-                                            const float2 (&w)[4], const Segments& S)
+__device__ __forceinline__ void put_weighed(const Layout& H, const Here& h, int lane, const float* weights,
+                                            const float2* stats, float2 (&s)[4], float2 (&q)[4], const Segments& S)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s[i] = dev::mul2(s[i], w[i]);
-        q[i] = dev::mul2(q[i], w[i]);
-    }
     const int t = threadIdx.x;
-    if (H.per < 8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            S.a[e * kThreads + t] = of_pair(s, e);
-            S.b[e * kThreads + t] = of_pair(q, e);
-        }
-        return;
-    }
     GroupWalk<kFlat> at(H, h, lane);
     const int g = at.g;
     float s0 = 0.0f, s1 = 0.0f, q0 = 0.0f, q1 = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e, at.next(H)) {
-        if (at.g != g) {
-            s1 += of_pair(s, e);
-            q1 += of_pair(q, e);
+        const float w = weights[at.c];
+        float& along = of_pair(q, e);
+        along *= stats[at.g].y;
+        const float ws = of_pair(s, e) * w, wq = along * w;
+        if (H.per < 8) {
+            S.a[e * kThreads + t] = ws;
+            S.b[e * kThreads + t] = wq;
+        } else if (at.g != g) {
+            s1 += ws;
+            q1 += wq;
         } else {
-            s0 += of_pair(s, e);
-            q0 += of_pair(q, e);
+            s0 += ws;
+            q0 += wq;
         }
     }
+    if (H.per < 8) return;
     S.a[t] = s0, S.b[t] = q0;
     S.a[kThreads + t] = s1, S.b[kThreads + t] = q1;
     S.firsts[t] = g;
@@ -654,20 +652,21 @@ __device__ __forceinline__ void join_channels(const Layout& H, const ChannelSums
     }
 }
 
-// By a block: dweight and dbias of 32 channels from blocks' sums of their slab's channels; block
-// j of a slab has the index j * slabs + slab.
+// By a block: dweight and dbias of kSumChannels channels from blocks' sums of their slab's
+// channels; block j of a slab has the index j * slabs + slab.
+constexpr int kSumChannels = 8, kSumSlices = kThreads / kSumChannels;
 __device__ __forceinline__ void sum_blocks_of(const Layout& H, int part, const float2* block_sums, int blocks,
                                               void* dweight, void* dbias, int32_t grad_type)
 {
-    __shared__ float2 slices[kWarps][32];
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int c = part * 32 + lane;
+    __shared__ float2 slices[kSumSlices][kSumChannels];
+    const int lane = threadIdx.x % kSumChannels, slice = threadIdx.x / kSumChannels;
+    const int c = part * kSumChannels + lane;
     float s = 0.0f, q = 0.0f;
     if (c < H.channels) {
         const int slab = c / H.width;
         const float2* from = block_sums + static_cast<int64_t>(slab) * H.width + (c - slab * H.width);
-#pragma unroll 8
-        for (int j = slice; j < blocks; j += kWarps) {
+#pragma unroll 10
+        for (int j = slice; j < blocks; j += kSumSlices) {
             const float2 v = from[static_cast<int64_t>(j) * H.slabs * H.width];
             s += v.x;
             q += v.y;
@@ -677,8 +676,8 @@ __device__ __forceinline__ void sum_blocks_of(const Layout& H, int part, const f
     __syncthreads();
     if (slice == 0 && c < H.channels) {
         float a[1] = {0.0f}, b[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+#pragma unroll 8
+        for (int k = 0; k < kSumSlices; ++k) {
             a[0] += slices[k][lane].x;
             b[0] += slices[k][lane].y;
         }

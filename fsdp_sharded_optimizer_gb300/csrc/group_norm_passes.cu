@@ -8,7 +8,7 @@ namespace gn {
 namespace {
 
 constexpr int kResident = 152 * 2; // blocks at once, two an SM
-constexpr int kMostSlots = 32;     // rows of a thread in a run
+constexpr int kMostSlots = 64;     // rows of a thread in a run
 
 struct Run { // a block's work
     int n, slab, chunk;
@@ -22,6 +22,29 @@ __device__ __forceinline__ Run run_of(const Layout& H, int64_t i)
     r.n = static_cast<int>(i / H.slabs);
     return r;
 }
+
+// Rows 0 .. rows - 1, kAhead loaded before any is used; without a branch between them.
+template <int kAhead, typename R, typename Fetch, typename Use>
+__device__ __forceinline__ void over_rows(int rows, Fetch fetch, Use use)
+{
+    int k = 0;
+    for (; k + kAhead <= rows; k += kAhead) {
+        R r[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(k + i, r[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) use(k + i, r[i]);
+    }
+    for (; k < rows; ++k) {
+        R r;
+        fetch(k, r);
+        use(k, r);
+    }
+}
+template <typename T>
+struct Pair { // a row of x and of dy
+    Raw8<T> x, d;
+};
 
 // Mean, squares about it and size of each group in each run.
 template <typename T, bool kFlat>
@@ -87,7 +110,7 @@ __device__ __forceinline__ void load_groups(const Layout& H, const Run& run, con
 }
 
 template <typename T, int kAct, bool kFlat>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 apply_kernel(const __grid_constant__ Layout H, const T* x, const void* __restrict__ weight,
              const void* __restrict__ bias, int32_t param_type, const float2* stats, T* y)
 {
@@ -108,23 +131,17 @@ apply_kernel(const __grid_constant__ Layout H, const T* x, const void* __restric
     forward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, a, b);
     const T* xp = x + (row0 + rg) * H.x_stride + run.slab * H.width + lane * 8;
     T* yp = y + (row0 + rg) * H.y_stride + run.slab * H.width + lane * 8;
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
-    for (int k = 0; k < h.rows; k += kAhead) {
-        Raw8<T> raw[kAhead];
+    auto put = [&](int k, const Raw8<T>& raw) {
+        float2 v[4];
+        dev::unpack8(raw, v);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (k + i < h.rows) load_row<kFlat, true>(H, h, k + i, xp, H.x_sample, H.x_stride, raw[i]);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k + i >= h.rows) break;
-            float2 v[4];
-            dev::unpack8(raw[i], v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = activated2<kAct>(dev::fma2(dev::add2(v[j], minus_mean[j]), a[j], b[j]));
-            store_row<kFlat>(H, h, k + i, yp, H.y_sample, H.y_stride, v);
-        }
-    }
+        for (int j = 0; j < 4; ++j)
+            v[j] = activated2<kAct>(dev::fma2(dev::add2(v[j], minus_mean[j]), a[j], b[j]));
+        store_row<kFlat>(H, h, k, yp, H.y_sample, H.y_stride, v);
+    };
+    over_rows<sizeof(T) == 2 ? 4 : 2, Raw8<T>>(h.rows, [&](int k, Raw8<T>& raw) {
+        load_row<kFlat, true>(H, h, k, xp, H.x_sample, H.x_stride, raw);
+    }, put);
 }
 
 // ------------------------------------------------------------------ backward
@@ -153,7 +170,7 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
     load_params(H, run.slab * H.width, weight, bias, param_type, weights, biases);
     for (int c = threadIdx.x; c < H.width; c += kThreads) C.sums[c] = make_float2(0.0f, 0.0f);
 
-    float2 minus_mean[4], rstd[4], w[4], b[4];
+    float2 minus_mean[4], a[4], b[4];
     Here h;
     bool first = true;
     int last_n = -1, lead = 0;
@@ -171,7 +188,7 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
             load_groups(H, run, stats, group_stats);
             __syncthreads();
             if (rg < H.row_groups)
-                backward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, rstd, w, b);
+                forward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, a, b);
             last_n = run.n;
             lead = h.lead;
         }
@@ -181,33 +198,24 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
             float2 s[4], q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = q[j] = make_float2(0.0f, 0.0f);
-            constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
-            for (int k = 0; k < h.rows; k += kAhead) {
-                Raw8<T> rx[kAhead], rd[kAhead];
+            over_rows<sizeof(T) == 2 ? 4 : 2, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
+                load_row<kFlat, false>(H, h, k, xp, H.x_sample, H.x_stride, r.x);
+                load_row<kFlat, false>(H, h, k, dp, H.y_sample, H.y_stride, r.d);
+            }, [&](int k, const Pair<T>& r) {
+                float2 v[4], d[4];
+                dev::unpack8(r.x, v);
+                dev::unpack8(r.d, d);
+                form_d<kAct>(v, d, minus_mean, a, b);
+                if (kFlat && !whole<kFlat>(H, h, k))
+                    outside(H, h, k, [&](int e) { of_pair(v, e) = of_pair(d, e) = 0.0f; });
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (k + j < h.rows) {
-                        load_row<kFlat, false>(H, h, k + j, xp, H.x_sample, H.x_stride, rx[j]);
-                        load_row<kFlat, false>(H, h, k + j, dp, H.y_sample, H.y_stride, rd[j]);
-                    }
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    if (k + j >= h.rows) break;
-                    float2 v[4], d[4];
-                    dev::unpack8(rx[j], v);
-                    dev::unpack8(rd[j], d);
-                    form_d<kAct>(v, d, minus_mean, rstd, w, b);
-                    if (kFlat && !whole<kFlat>(H, h, k + j))
-                        outside(H, h, k + j, [&](int e) { of_pair(v, e) = of_pair(d, e) = 0.0f; });
-#pragma unroll
-                    for (int l = 0; l < 4; ++l) {
-                        s[l] = dev::add2(s[l], d[l]);
-                        q[l] = dev::fma2(d[l], v[l], q[l]);
-                    }
+                for (int l = 0; l < 4; ++l) {
+                    s[l] = dev::add2(s[l], d[l]);
+                    q[l] = dev::fma2(d[l], v[l], q[l]);
                 }
-            }
+            });
+            put_weighed<kFlat>(H, h, lane, weights, group_stats, s, q, S);
             add_channels(H, C, rg, lane, first, s, q);
-            put_weighed<kFlat>(H, h, lane, s, q, w, S);
         }
         first = false;
         __syncthreads();
@@ -224,7 +232,7 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
 }
 
 // Blocks below group_blocks: a warp for each group of each sample, its means of d * weight and
-// d * weight * h; the others dweight and dbias of 32 channels each.
+// d * weight * h; the others dweight and dbias of kSumChannels channels each.
 __global__ void __launch_bounds__(kThreads)
 join_sums_kernel(const __grid_constant__ Layout H, const float2* __restrict__ partial, int64_t group_blocks,
                  float2* __restrict__ means, const float2* __restrict__ block_sums, int blocks_of_slab, void* dweight,
@@ -278,38 +286,29 @@ apply_gradient_kernel(const __grid_constant__ Layout H, const T* __restrict__ x,
     load_groups(H, run, means, group_means);
     __syncthreads();
     if (h.rows == 0) return;
-    float2 minus_mean[4], rstd[4], w[4], b[4], wr[4], s1[4], s2[4];
-    backward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, rstd, w, b);
-    result_factors<kFlat>(H, h, lane, group_means, rstd, w, wr, s1, s2);
+    float2 minus_mean[4], a[4], b[4], rstd[4], s1[4], s2[4];
+    forward_factors<kFlat>(H, h, lane, weights, biases, group_stats, minus_mean, a, b);
+    result_factors<kFlat>(H, h, lane, group_stats, group_means, rstd, s1, s2);
     const T* xp = x + (row0 + rg) * H.x_stride + run.slab * H.width + lane * 8;
     const T* dp = dy + (row0 + rg) * H.y_stride + run.slab * H.width + lane * 8;
     T* out = dx + (row0 + rg) * H.x_stride + run.slab * H.width + lane * 8;
-    constexpr int kAhead = 2;
-    for (int k = 0; k < h.rows; k += kAhead) {
-        Raw8<T> rx[kAhead], rd[kAhead];
+    over_rows<sizeof(T) == 2 ? 4 : 2, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
+        load_row<kFlat, true>(H, h, k, xp, H.x_sample, H.x_stride, r.x);
+        load_row<kFlat, true>(H, h, k, dp, H.y_sample, H.y_stride, r.d);
+    }, [&](int k, const Pair<T>& r) {
+        float2 v[4], d[4];
+        dev::unpack8(r.x, v);
+        dev::unpack8(r.d, d);
+        form_d<kAct>(v, d, minus_mean, a, b);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (k + i < h.rows) {
-                load_row<kFlat, true>(H, h, k + i, xp, H.x_sample, H.x_stride, rx[i]);
-                load_row<kFlat, true>(H, h, k + i, dp, H.y_sample, H.y_stride, rd[i]);
-            }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (k + i >= h.rows) break;
-            float2 v[4], d[4];
-            dev::unpack8(rx[i], v);
-            dev::unpack8(rd[i], d);
-            form_d<kAct>(v, d, minus_mean, rstd, w, b);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = dev::fma2(v[j], s2[j], dev::fma2(d[j], wr[j], s1[j]));
-            store_row<kFlat>(H, h, k + i, out, H.x_sample, H.x_stride, v);
-        }
-    }
+        for (int j = 0; j < 4; ++j) v[j] = dev::fma2(dev::mul2(v[j], rstd[j]), s2[j], dev::fma2(d[j], a[j], s1[j]));
+        store_row<kFlat>(H, h, k, out, H.x_sample, H.x_stride, v);
+    });
 }
 
 // --------------------------------------------------------------------- host
 // false: a slab of these channels is not possible.
-bool make_layout(const zero_group_norm_t& n, bool flat, Layout* out)
+bool make_layout(const zero_group_norm_t& n, bool flat, bool backward, Layout* out)
 {
     if (n.positions * n.channels >= (int64_t(1) << 30) && flat) return false;
     Layout H = {};
@@ -343,18 +342,27 @@ bool make_layout(const zero_group_norm_t& n, bool flat, Layout* out)
     H.row_groups = kThreads / H.lanes;
     const int64_t rows = flat ? (n.positions * n.channels + 7 + 8 * H.lanes - 1) / (8 * H.lanes) : n.positions;
     const int64_t steps = (rows + H.row_groups - 1) / H.row_groups; // rows of a thread in a sample
-    int64_t slots = n.samples * H.slabs * steps / (kResident * 4);
+    // As many rows to a run as leave a few rounds of blocks (backward one: a block takes several
+    // runs then), and then as leave the last round full.
+    const int64_t all = n.samples * H.slabs;
+    int64_t slots = all * steps / (kResident * (backward ? 1 : 4));
     slots = slots < 4 ? 4 : slots > kMostSlots ? kMostSlots : slots;
+    double best = 0;
+    for (int64_t t = slots; t > slots / 2; --t) {
+        const int64_t runs = all * ((steps + t - 1) / t);
+        const double use = static_cast<double>(runs) / static_cast<double>((runs + kResident - 1) / kResident * kResident);
+        if (use > best + 0.02) best = use, slots = t;
+    }
     H.slots = static_cast<int32_t>(slots);
     H.chunks = static_cast<int32_t>((steps + slots - 1) / slots);
     *out = H;
     return true;
 }
 
-Layout layout_of(const Call& c, bool flat)
+Layout layout_of(const Call& c, bool flat, bool backward)
 {
     Layout H;
-    make_layout(*c.norm, flat, &H);
+    make_layout(*c.norm, flat, backward, &H);
     H.lengths = c.lengths;
     H.x_sample = c.norm->positions * c.norm->x_stride;
     H.y_sample = c.norm->positions * c.norm->y_stride;
@@ -388,7 +396,7 @@ Scratch scratch_of(void* base, const Layout& H)
 template <typename T, int kAct, bool kFlat>
 int forward(const Call& c)
 {
-    const Layout H = layout_of(c, kFlat);
+    const Layout H = layout_of(c, kFlat, false);
     const Scratch s = scratch_of(c.scratch, H);
     const int64_t runs = runs_of(H), units = static_cast<int64_t>(H.samples) * (H.groups / H.splits);
     float2* stats = c.stats ? c.stats : s.groups;
@@ -406,22 +414,21 @@ int forward(const Call& c)
 template <typename T, int kAct, bool kFlat>
 int backward(const Call& c)
 {
-    const Layout H = layout_of(c, kFlat);
+    const Layout H = layout_of(c, kFlat, true);
     const Scratch s = scratch_of(c.scratch, H);
     const int64_t runs = runs_of(H), units = static_cast<int64_t>(H.samples) * (H.groups / H.splits);
     const auto* x = static_cast<const T*>(c.x);
     const auto* dy = static_cast<const T*>(c.dy);
     auto* partial = reinterpret_cast<float2*>(s.partial);
-    int64_t blocks = kResident / H.slabs; // of each slab; a slab is wider than half of kWidth, or all channels
+    int64_t blocks = kResident / H.slabs; // of each slab
     if (blocks > runs / H.slabs) blocks = runs / H.slabs;
-    if (blocks < 1) blocks = 1;
     auto* sums = sums_kernel<T, kAct, kFlat>;
     const int64_t words = channel_words(H) + segment_words(H, 2) + 2 * H.slab_groups + 2 * H.width;
     if (!allow_shared(reinterpret_cast<const void*>(sums), 113 * 1024)) return ZERO_ECUDA;
     int rc = launch(false, sums, blocks * H.slabs, static_cast<size_t>(4 * words), c.stream, H, x, dy, c.weight, c.bias,
                     c.norm->param_type, c.stats_in, partial, s.block_sums);
     const int64_t group_blocks = c.dx ? (units + kWarps - 1) / kWarps : 0;
-    const int64_t more = c.dweight || c.dbias ? (H.channels + 31) / 32 : 0;
+    const int64_t more = c.dweight || c.dbias ? (H.channels + kSumChannels - 1) / kSumChannels : 0;
     if (rc == ZERO_OK && group_blocks + more > 0)
         rc = launch(true, join_sums_kernel, group_blocks + more, 0, c.stream, H, partial, group_blocks, s.groups,
                     s.block_sums, static_cast<int>(blocks), c.dweight, c.dbias, c.norm->grad_type);
@@ -456,7 +463,7 @@ bool passes_take(const Call& c)
 {
     Layout H;
     const bool flat = !rows_whole(c);
-    return (!flat || line_whole(c)) && make_layout(*c.norm, flat, &H) && H.slabs <= kResident &&
+    return (!flat || line_whole(c)) && make_layout(*c.norm, flat, false, &H) && H.slabs <= kResident &&
            runs_of(H) <= 0x7FFFFFFF;
 }
 
@@ -464,8 +471,8 @@ int64_t passes_bytes(const zero_group_norm_t& n)
 {
     int64_t most = 0;
     Layout H;
-    for (int flat = 0; flat < 2; ++flat)
-        if (make_layout(n, flat != 0, &H)) {
+    for (int way = 0; way < 4; ++way)
+        if (make_layout(n, way % 2 != 0, way / 2 != 0, &H)) {
             const int64_t bytes = scratch_of(nullptr, H).bytes;
             if (bytes > most) most = bytes;
         }

@@ -210,7 +210,7 @@ single_channels_kernel(const __grid_constant__ Grid G, const float2* __restrict_
 }
 
 // Blocks below group_blocks: a warp for each group of each sample, its means of d * weight and
-// d * weight * h; the others: dweight and dbias of 32 channels over the samples.
+// d * weight * h; the others: dweight and dbias of kSumChannels channels over the samples.
 __global__ void __launch_bounds__(kThreads)
 single_groups_kernel(const __grid_constant__ Grid G, const float2* __restrict__ sums, const void* __restrict__ weight,
                      int32_t param_type, int64_t group_blocks, float2* __restrict__ means, void* dweight, void* dbias,
@@ -362,7 +362,7 @@ int backward(const Call& c)
         rc = launch(blocks > 0, single_channels_kernel, (channels + kThreads - 1) / kThreads, 0, c.stream, G, s.partial,
                     s.sums);
     const int64_t group_blocks = c.dx ? (units + kWarps - 1) / kWarps : 0;
-    const int64_t more = c.dweight || c.dbias ? (G.channels + 31) / 32 : 0;
+    const int64_t more = c.dweight || c.dbias ? (G.channels + kSumChannels - 1) / kSumChannels : 0;
     if (rc == ZERO_OK && group_blocks + more > 0)
         rc = launch(channels > 0, single_groups_kernel, group_blocks + more, 0, c.stream, G, s.sums, c.weight,
                     c.norm->param_type, group_blocks, s.groups, c.dweight, c.dbias, c.norm->grad_type);

@@ -6,7 +6,7 @@
 //   coef = min(1, max_norm / (norm + 1e-6))
 //   dst  = round(factor * src)
 //
-// Every tensor is cut into chunks of kChunk elements at 16-byte boundaries of
+// Every tensor is cut into chunks of kChunk elements (fewer in small lists) at 16-byte boundaries of
 // the tensor that the pass stores (dst) or only reads (src); a block takes the
 // chunks blockIdx, blockIdx + grid, ... of the whole list, so a list of one large
 // and hundreds of small tensors is spread evenly, and one launch does them all.
@@ -30,6 +30,9 @@ using dev::Raw8;
 constexpr int kThreads = 256;
 constexpr int kVecs = 8; // vectors of 8 elements that a thread takes of a chunk
 constexpr int64_t kChunk = int64_t(kThreads) * kVecs * 8;
+// Lists of fewer elements are cut into chunks of one vector a thread: more blocks, each done
+// sooner.
+constexpr int64_t kSmallList = int64_t(kNormBlocks) * kThreads * 8;
 // A list of up to kFew tensors fits the 4 KB of parameters that every launch
 // carries; longer ones take the 32 KB form, and further launches.
 constexpr int kFew = 120, kMany = 1000;
@@ -46,6 +49,7 @@ struct Entry {
 template <int kMost>
 struct List {
     int32_t n, chunks;
+    int64_t chunk; // elements of a chunk
     Entry e[kMost];
 };
 
@@ -101,11 +105,11 @@ __device__ __forceinline__ void add_squares(const Raw8<T>& r, float& sum, double
 
 // The squares of chunk `local` of one tensor.
 template <typename T>
-__device__ __forceinline__ void chunk_squares(const T* src, int64_t n, int64_t local, double& wide)
+__device__ __forceinline__ void chunk_squares(const T* src, int64_t n, int64_t local, int64_t chunk, double& wide)
 {
     const int64_t head = lead(src), end = n + head;
     const T* base = src - head;
-    const int64_t lo = local * kChunk, hi = lo + kChunk < end ? lo + kChunk : end;
+    const int64_t lo = local * chunk, hi = lo + chunk < end ? lo + chunk : end;
     float sum = 0.0f;
     if (lo >= head && hi == lo + kChunk) {
         constexpr int kAhead = sizeof(T) == 2 ? kVecs : kVecs / 2;
@@ -159,9 +163,9 @@ sqnorm_kernel(const __grid_constant__ List<kMost> L, int accumulate, double* __r
     for (int c = blockIdx.x; c < L.chunks; c += gridDim.x) {
         const Entry& e = L.e[entry_of(L, c)];
         if (e.src_type == ZERO_TYPE_BF16)
-            chunk_squares(static_cast<const Bf16*>(e.src), e.n, c - e.first, wide);
+            chunk_squares(static_cast<const Bf16*>(e.src), e.n, c - e.first, L.chunk, wide);
         else
-            chunk_squares(static_cast<const float*>(e.src), e.n, c - e.first, wide);
+            chunk_squares(static_cast<const float*>(e.src), e.n, c - e.first, L.chunk, wide);
     }
     const double b = block_sum(wide);
     if (threadIdx.x == 0) {
@@ -191,13 +195,13 @@ __device__ __forceinline__ void scale_vec(const In* s, Out* d, float factor, boo
 // Chunk `local` of one tensor, cut at 16-byte boundaries of dst.
 template <typename In, typename Out>
 __device__ __forceinline__ void chunk_scale(const In* src, Out* dst, int64_t n, int64_t local,
-                                            float factor)
+                                            int64_t chunk, float factor)
 {
     const int64_t head = lead(dst), end = n + head;
     const In* from = src - head;
     Out* to = dst - head;
     const bool wide_in = (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
-    const int64_t lo = local * kChunk, hi = lo + kChunk < end ? lo + kChunk : end;
+    const int64_t lo = local * chunk, hi = lo + chunk < end ? lo + chunk : end;
     if (wide_in && lo >= head && hi == lo + kChunk) {
         constexpr int kAhead = sizeof(In) == 2 ? kVecs : kVecs / 2;
         const int64_t at = lo + threadIdx.x * 8;
@@ -206,7 +210,7 @@ __device__ __forceinline__ void chunk_scale(const In* src, Out* dst, int64_t n, 
             Raw8<In> r[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                dev::stream_raw8(from + at + (k + i) * kThreads * 8, r[i]);
+                dev::load_raw8(from + at + (k + i) * kThreads * 8, r[i]);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 float x[8];
@@ -268,15 +272,15 @@ scale_kernel(const __grid_constant__ List<kMost> L, float scale,
         if (e.src_type == ZERO_TYPE_BF16) {
             const auto* s = static_cast<const Bf16*>(e.src);
             if (e.dst_type == ZERO_TYPE_BF16)
-                chunk_scale(s, static_cast<Bf16*>(e.dst), e.n, local, factor);
+                chunk_scale(s, static_cast<Bf16*>(e.dst), e.n, local, L.chunk, factor);
             else
-                chunk_scale(s, static_cast<float*>(e.dst), e.n, local, factor);
+                chunk_scale(s, static_cast<float*>(e.dst), e.n, local, L.chunk, factor);
         } else {
             const auto* s = static_cast<const float*>(e.src);
             if (e.dst_type == ZERO_TYPE_BF16)
-                chunk_scale(s, static_cast<Bf16*>(e.dst), e.n, local, factor);
+                chunk_scale(s, static_cast<Bf16*>(e.dst), e.n, local, L.chunk, factor);
             else
-                chunk_scale(s, static_cast<float*>(e.dst), e.n, local, factor);
+                chunk_scale(s, static_cast<float*>(e.dst), e.n, local, L.chunk, factor);
         }
     }
 }
@@ -299,11 +303,19 @@ int check_tensors(const zero_tensor_t* t, int64_t n, bool with_dst)
     return aligned ? ZERO_OK : ZERO_EALIGN;
 }
 
-int64_t chunks_of(const zero_tensor_t& t, bool by_dst)
+int64_t chunks_of(const zero_tensor_t& t, bool by_dst, int64_t chunk)
 {
     const uintptr_t p = reinterpret_cast<uintptr_t>(by_dst ? t.dst : t.src);
     const int64_t head = static_cast<int64_t>(p & 15u) / type_bytes(by_dst ? t.dst_type : t.src_type);
-    return (t.n + head + kChunk - 1) / kChunk;
+    return (t.n + head + chunk - 1) / chunk;
+}
+
+// Elements of a chunk, for a whole list: the order of the sums goes by it.
+int64_t chunk_of(const zero_tensor_t* t, int64_t n)
+{
+    int64_t all = 0;
+    for (int64_t i = 0; i < n && all < kSmallList; ++i) all += t[i].n;
+    return all < kSmallList ? kThreads * 8 : kChunk;
 }
 
 // Fills L from tensor `at` on; returns the first tensor that no longer fits.
@@ -313,7 +325,7 @@ int64_t fill(List<kMost>& L, const zero_tensor_t* t, int64_t n, int64_t at, bool
     L.n = L.chunks = 0;
     for (; at < n && L.n < kMost; ++at) {
         if (t[at].n == 0) continue;
-        const int64_t c = chunks_of(t[at], by_dst);
+        const int64_t c = chunks_of(t[at], by_dst, L.chunk);
         if (L.n > 0 && L.chunks + c > kMaxLaunchChunks) break;
         L.e[L.n++] = {t[at].src, t[at].dst, t[at].n, L.chunks, static_cast<int16_t>(t[at].src_type),
                       static_cast<int16_t>(by_dst ? t[at].dst_type : 0)};
@@ -329,6 +341,7 @@ int launch_sqnorm(const zero_tensor_t* t, int64_t n, int accumulate, double* par
                   cudaStream_t stream, int* used)
 {
     List<kMost> L;
+    L.chunk = chunk_of(t, n);
     int64_t at = 0;
     *used = 0;
     do {
@@ -349,6 +362,7 @@ int launch_scale(const zero_tensor_t* t, int64_t n, float scale, const double* p
                  int n_partials, double max_norm, float* norm_coef, cudaStream_t stream)
 {
     List<kMost> L;
+    L.chunk = chunk_of(t, n);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
