@@ -1094,14 +1094,15 @@ _ACTS = {None: ZERO_ACT_NONE, "none": ZERO_ACT_NONE, "silu": ZERO_ACT_SILU, "gel
 def _strided_rows(t, what, shape=None):
     """Address of a tensor whose last dimension is contiguous, and the elements between
     its rows, which have to be evenly apart."""
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    if not _addressable(t):
+    sizes = t.shape
+    if shape is not None and sizes != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(sizes)))
+    if not t.is_cuda and not _addressable(t):
         raise ValueError("%s must be CUDA or pinned host memory" % what)
-    sizes, strides = t.shape, t.stride()
     cols = sizes[-1]
-    if t.numel() == 0:
-        return t.data_ptr(), max(1, cols)
+    if t.is_contiguous():
+        return t.data_ptr(), cols or 1
+    strides = t.stride()
     if cols > 1 and strides[-1] != 1:
         raise ValueError("%s must be contiguous in its last dimension" % what)
     row = span = None
@@ -1113,34 +1114,50 @@ def _strided_rows(t, what, shape=None):
         elif stride != span:
             raise ValueError("%s must have rows that are evenly apart" % what)
         span = stride * size
-    return t.data_ptr(), max(1, cols) if row is None else row
+    return t.data_ptr(), (cols or 1) if row is None else row
 
 
 def _lengths(t, n, what):
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise ValueError("%s must be int32, got %s" % (what, t.dtype))
     return _at(t, what, (n,))
 
 
+def _two_vectors(a, a_name, b, b_name, shape):
+    """Addresses and type of two tensors of a shape and a type, either of which may be None."""
+    at_a = at_b = None
+    type = ZERO_TYPE_BF16
+    if a is not None:
+        at_a, type = _at(a, a_name, shape), _type(a, a_name)
+    if b is not None:
+        at_b = _at(b, b_name, shape)
+        if a is None:
+            type = _type(b, b_name)
+        elif b.dtype is not a.dtype and _type(b, b_name) != type:
+            raise ValueError("%s and %s must have one type" % (a_name, b_name))
+    return at_a, at_b, type
+
+
 def _group_norm_call(x, stats, groups, act):
-    if x.dim() < 2:
+    sizes = x.shape
+    if len(sizes) < 2:
         raise ValueError("x must have two dimensions or more: samples, positions, channels")
     if act not in _ACTS:
         raise ValueError("act must be 'none', 'silu' or 'gelu'")
-    if stats is None and groups is None:
-        raise ValueError("groups must be given where stats are not")
-    N, C = x.shape[0], x.shape[-1]
+    N, C = sizes[0], sizes[-1]
     P = 1
-    for n in x.shape[1:-1]:
+    for n in sizes[1:-1]:
         P *= n
+    if stats is None:
+        if groups is None:
+            raise ValueError("groups must be given where stats are not")
+        return N, P, C, int(groups), None
     G = int(groups) if groups is not None else stats.shape[1]
-    if stats is not None:
-        if stats.dtype != torch.float32:
-            raise ValueError("stats must be fp32")
-        stats = _at(stats, "stats", (N, G, 2))
-    return N, P, C, G, stats
+    if stats.dtype is not torch.float32:
+        raise ValueError("stats must be fp32")
+    return N, P, C, G, _at(stats, "stats", (N, G, 2))
 
 
 def zero_group_norm_scratch_bytes(samples, positions, channels, groups):
@@ -1159,13 +1176,11 @@ def zero_group_norm_forward(x, y, stats, scratch, weight=None, bias=None, length
     N, P, C_, G, stats = _group_norm_call(x, stats, groups, act)
     xp, xs = _strided_rows(x, "x")
     yp, ys = _strided_rows(y, "y", x.shape)
-    par = _Alike((C_,), "weight and bias")
-    w, b = par(weight, "weight"), par(bias, "bias")
+    w, b, param_type = _two_vectors(weight, "weight", bias, "bias", (C_,))
     type = _type(x, "x")
-    if _type(y, "y") != type:
+    if y.dtype is not x.dtype and _type(y, "y") != type:
         raise ValueError("x and y must have one type")
-    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, par.type or ZERO_TYPE_BF16,
-                             ZERO_TYPE_BF16, _ACTS[act], eps)
+    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, param_type, ZERO_TYPE_BF16, _ACTS[act], eps)
     _check("zero_group_norm_forward", lib.zero_group_norm_forward(
         C.byref(spec), xp, w, b, _lengths(lengths, N, "lengths"), yp, stats,
         _at(scratch, "scratch"), scratch.nbytes, _raw_stream(stream)))
@@ -1184,15 +1199,12 @@ def zero_group_norm_backward(x, dy, stats, dx, scratch, weight=None, bias=None, 
         dxp, dxs = _strided_rows(dx, "dx", x.shape)
         if dxs != xs:
             raise ValueError("dx must have x's stride between positions")
-    par = _Alike((C_,), "weight and bias")
-    w, b = par(weight, "weight"), par(bias, "bias")
-    sums = _Alike((C_,), "dweight and dbias")
-    dw, db = sums(dweight, "dweight"), sums(dbias, "dbias")
+    w, b, param_type = _two_vectors(weight, "weight", bias, "bias", (C_,))
+    dw, db, grad_type = _two_vectors(dweight, "dweight", dbias, "dbias", (C_,))
     type = _type(x, "x")
     if _type(dy, "dy") != type or (dx is not None and _type(dx, "dx") != type):
         raise ValueError("x, dy and dx must have one type")
-    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, par.type or ZERO_TYPE_BF16,
-                             sums.type or ZERO_TYPE_BF16, _ACTS[act], 1.0)
+    spec = zero_group_norm_t(N, P, C_, xs, ys, G, type, param_type, grad_type, _ACTS[act], 1.0)
     _check("zero_group_norm_backward", lib.zero_group_norm_backward(
         C.byref(spec), xp, dyp, w, b, _lengths(lengths, N, "lengths"), stats, dxp, dw, db,
         _at(scratch, "scratch"), scratch.nbytes, _raw_stream(stream)))
@@ -1201,16 +1213,18 @@ def zero_group_norm_backward(x, dy, stats, dx, scratch, weight=None, bias=None, 
 # ------------------------------------------------- relative position bias
 def _relpos_call(scores, what, table, starts, q_lengths, k_lengths, start, max_distance,
                  bidirectional, causal):
-    if scores.dim() != 4:
+    sizes, of_table = scores.shape, table.shape
+    if len(sizes) != 4:
         raise ValueError("%s must have four dimensions: batch, heads, queries, keys" % what)
-    if table.dim() != 2 or table.shape[1] != scores.shape[1]:
+    B, H, Q, K = sizes
+    if len(of_table) != 2 or of_table[1] != H:
         raise ValueError("the table must be buckets x heads")
-    B, H, Q, K = scores.shape
-    spec = zero_relpos_t(B, H, Q, K, start, max_distance, table.shape[0],
+    spec = zero_relpos_t(B, H, Q, K, start, max_distance, of_table[0],
                          1 if bidirectional else 0, 1 if causal else 0, _type(table, "the table"),
                          _type(scores, what))
-    return spec, (_lengths(starts, B, "starts"), _lengths(q_lengths, B, "q_lengths"),
-                  _lengths(k_lengths, B, "k_lengths"))
+    return spec, (None if starts is None else _lengths(starts, B, "starts"),
+                  None if q_lengths is None else _lengths(q_lengths, B, "q_lengths"),
+                  None if k_lengths is None else _lengths(k_lengths, B, "k_lengths"))
 
 
 def zero_relpos_forward(table, out, scores=None, start=0, starts=None, q_lengths=None,
@@ -1226,7 +1240,7 @@ def zero_relpos_forward(table, out, scores=None, start=0, starts=None, q_lengths
                                   max_distance, bidirectional, causal)
     at, stride = _strided_rows(out, "out")
     sp, ss = (None, 0) if scores is None else _strided_rows(scores, "scores", out.shape)
-    if scores is not None and _type(scores, "scores") != spec.type:
+    if scores is not None and scores.dtype is not out.dtype and _type(scores, "scores") != spec.type:
         raise ValueError("scores and out must have one type")
     _check("zero_relpos_forward", lib.zero_relpos_forward(
         C.byref(spec), _at(table, "table"), *of_batch, sp, ss, at, stride, _raw_stream(stream)))

@@ -61,7 +61,7 @@ template <bool kFlat, typename T>
 __device__ __forceinline__ void copy_row(const Layout& H, const Here& h, int k, float4* place, const T* base,
                                          int64_t sample, int64_t stride)
 {
-    if (kFlat) {
+    if (kFlat && !whole<kFlat>(H, h, k)) {
         const int64_t at = h.n * sample + value_of(H, h, k);
         if (at < 0 || H.samples * sample - at < 8) { // not all of the vector is the tensor's
             Raw8<T> r = {};

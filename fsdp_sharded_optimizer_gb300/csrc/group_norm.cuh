@@ -233,7 +233,7 @@ __device__ __forceinline__ void load_row(const Layout& H, const Here& h, int k, 
                                          int64_t stride, Raw8<T>& r)
 {
     const T* from = base + h.n * sample + k * H.row_groups * stride - (kFlat ? h.lead : 0);
-    if (kFlat) {
+    if (kFlat && !whole<kFlat>(H, h, k)) {
         const int64_t at = h.n * sample + value_of(H, h, k), behind = H.samples * sample - at;
         if (at < 0 || behind < 8) {
 #pragma unroll

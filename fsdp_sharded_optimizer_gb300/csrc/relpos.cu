@@ -582,8 +582,10 @@ int launch_forward(const Geometry& G, const Borders& B, const void* table, int32
     const int span = B.both ? 2 * last : last;
     const int copies = span <= kMostCopied ? 4 : 1;
     auto start = [&](auto kernel) {
-        const size_t most = 4 * static_cast<size_t>(line_places(copies == 4 ? kMostCopied : 2 * kMaxDistance)) * copies;
-        if (!allow_shared(reinterpret_cast<const void*>(kernel), most)) return ZERO_ECUDA;
+        // the limit that every block has without asking is 48 KB
+        if (copies == 1 && !allow_shared(reinterpret_cast<const void*>(kernel),
+                                         4 * static_cast<size_t>(line_places(2 * kMaxDistance))))
+            return ZERO_ECUDA;
         kernel<<<static_cast<unsigned>(blocks), kThreads, 4 * static_cast<size_t>(line_places(span)) * copies,
                  stream>>>(G, B, table, table_type, static_cast<const T*>(scores), static_cast<T*>(out),
                            log2, static_cast<int>(rows), static_cast<int>(tiles), same);
