@@ -56,19 +56,17 @@ __device__ __forceinline__ float2 sigmoid2(float2 z)
 }
 // The normal distribution's density and cumulative probability: Abramowitz and Stegun, 26.2.17
 // (absolute error below 7.5e-8), which needs one exponential for both.
-__device__ __forceinline__ void normal2(float2 z, float2& density, float2& cdf)
+__device__ __forceinline__ void normal(float z, float& density, float& cdf)
 {
-    const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
-    const float2 r = dev::fma2(a, dev::pair(0.2316419f), dev::pair(1.0f));
-    const float2 t = make_float2(reciprocal_fast(r.x), reciprocal_fast(r.y));
-    const float2 e = dev::mul2(dev::mul2(z, z), dev::pair(-0.5f * kLog2e));
-    density = dev::mul2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), dev::pair(0.39894228f));
-    float2 p = dev::fma2(t, dev::pair(1.330274429f), dev::pair(-1.821255978f));
-    p = dev::fma2(p, t, dev::pair(1.781477937f));
-    p = dev::fma2(p, t, dev::pair(-0.356563782f));
-    p = dev::mul2(dev::fma2(p, t, dev::pair(0.319381530f)), t);
-    const float2 tail = dev::mul2(p, density);
-    cdf = make_float2(z.x > 0.0f ? 1.0f - tail.x : tail.x, z.y > 0.0f ? 1.0f - tail.y : tail.y);
+    // Single operations: they take constants as they stand, pairs need them in registers.
+    const float t = reciprocal_fast(fmaf(fabsf(z), 0.2316419f, 1.0f));
+    density = exp2_fast(z * z * (-0.5f * kLog2e)) * 0.39894228f;
+    float p = fmaf(t, 1.330274429f, -1.821255978f);
+    p = fmaf(p, t, 1.781477937f);
+    p = fmaf(p, t, -0.356563782f);
+    p = fmaf(p, t, 0.319381530f) * t;
+    const float tail = p * density;
+    cdf = z > 0.0f ? 1.0f - tail : tail;
 }
 
 template <int kAct>
@@ -76,9 +74,10 @@ __device__ __forceinline__ float2 activated2(float2 z)
 {
     if constexpr (kAct == ZERO_ACT_SILU) return dev::mul2(z, sigmoid2(z));
     if constexpr (kAct == ZERO_ACT_GELU) {
-        float2 density, cdf;
-        normal2(z, density, cdf);
-        return dev::mul2(z, cdf);
+        float density, a, b;
+        normal(z.x, density, a);
+        normal(z.y, density, b);
+        return dev::mul2(z, make_float2(a, b));
     }
     return z;
 }
@@ -91,7 +90,8 @@ __device__ __forceinline__ float2 slope2(float2 z)
     }
     if constexpr (kAct == ZERO_ACT_GELU) {
         float2 density, cdf;
-        normal2(z, density, cdf);
+        normal(z.x, density.x, cdf.x);
+        normal(z.y, density.y, cdf.y);
         return dev::fma2(z, density, cdf);
     }
     return dev::pair(1.0f);
