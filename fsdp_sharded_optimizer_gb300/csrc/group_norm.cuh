@@ -10,7 +10,7 @@
 // 8 l + e - lead of it, of channel (8 l + e - lead) mod channels.
 //
 // Statistics: a thread sums each channel's differences from its own first value, and their
-// squares: with at most 32 rows those are at most 2 + 2 * 32 times the squares about the
+// squares: with at most 64 rows those are at most 2 + 2 * 64 times the squares about the
 // mean even where that first value is an outlier, so fp32 keeps the variance.  Threads and
 // blocks are joined by means and sums of squares about them.
 #pragma once

@@ -66,6 +66,21 @@ __device__ __forceinline__ int length_of(const int32_t* lengths, int b, int most
     return n < 0 ? 0 : n < most ? n : most;
 }
 
+// ------------------------------------------------------------------ forward
+constexpr int kThreads = 256;
+
+// The bias by distance in shared memory: place k stands for the distance k - 8 - last,
+// held within [-last, last] (or [-last, 0] where later keys share bucket 0), so that a
+// vector anywhere reads eight places in a row, far ones the end values.  (Four copies, each
+// a place further, for two aligned 16-byte reads in the place of eight words: 8 x 12 x 1024 x
+// 1024 scores 42.6 us, so 43.3.)
+__host__ __device__ __forceinline__ int line_places(int span) { return span + 17; }
+
+__device__ __forceinline__ int clamped(int64_t x, int lo, int hi)
+{
+    return x < lo ? lo : x > hi ? hi : static_cast<int>(x);
+}
+
 // The bucket among one direction's of a distance >= 0.
 __device__ __forceinline__ int bucket_of(const Borders& B, int distance)
 {
@@ -80,45 +95,13 @@ __device__ __forceinline__ int bucket_of(const Borders& B, int distance)
     return lo;
 }
 
-// ------------------------------------------------------------------ forward
-constexpr int kThreads = 256;
-
-// The bias by distance in shared memory: place k stands for the distance k - 8 - last,
-// held within [-last, last] (or [-last, 0] where later keys share bucket 0), so that a
-// vector anywhere reads eight places in a row, far ones the end values.  kCopies = 4:
-// copy a begins at place a, so eight places from any k on are two aligned 16-byte
-// reads of copy k mod 4 (against eight words of one copy, four of which meet in a
-// bank).  Lines of more than kMostCopied distances have one copy.
-constexpr int kMostCopied = 2048;
-__host__ __device__ __forceinline__ int line_places(int span) { return (span + 20) / 4 * 4; }
-
-__device__ __forceinline__ int clamped(int64_t x, int lo, int hi)
-{
-    return x < lo ? lo : x > hi ? hi : static_cast<int>(x);
-}
-
-template <int kCopies>
-__device__ __forceinline__ void read_line(const float* line, int places, int k, float (&x)[8])
-{
-    if constexpr (kCopies == 4) {
-        const int copy = k & 3;
-        const auto* p = reinterpret_cast<const float4*>(line + copy * places + (k - copy));
-        const float4 a = p[0], b = p[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = line[k + e];
-    }
-}
-
-template <typename T, bool kScores, int kCopies>
+template <typename T, bool kScores>
 __global__ void __launch_bounds__(kThreads)
 forward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borders B,
                const void* __restrict__ table, int32_t table_type, const T* scores, T* out,
                int lanes_log2, int rows_per_block, int tiles, int same_lead)
 {
-    extern __shared__ __align__(16) float line[];
+    extern __shared__ float line[];
     constexpr int kAhead = kScores ? 4 : 1; // vectors of a thread in flight
     const int64_t plane = blockIdx.x / tiles;
     const int h = static_cast<int>(plane % G.heads), b = static_cast<int>(plane / G.heads);
@@ -131,14 +114,14 @@ forward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borde
     const int last = B.at[B.n - 1];
     const int span = B.both ? 2 * last : last;
     const int places = line_places(span);
+    // A thread to a place: all loads of the table at once (a warp to a bucket takes one after
+    // another: 32 x 2048 x 2048 41.9 us in the place of 40.6).
     for (int k = threadIdx.x; k < places; k += kThreads) {
         const int d = min(max(k - 8, 0), span) - last;
         const int bucket = bucket_of(B, d < 0 ? -d : d) + (d > 0 ? B.n : 0);
         float x[1];
         dev::load_any<1>(table, table_type, static_cast<int64_t>(bucket) * G.heads + h, x);
-#pragma unroll
-        for (int c = 0; c < kCopies; ++c)
-            if (k >= c) line[c * places + k - c] = x[0];
+        line[k] = x[0];
     }
     __syncthreads();
 
@@ -169,7 +152,9 @@ forward_kernel(const __grid_constant__ Geometry G, const __grid_constant__ Borde
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = -INFINITY;
                 } else {
-                    read_line<kCopies>(line, places, min(max(j0 + place, 0), span + 9), x);
+                    const float* from = line + min(max(j0 + place, 0), span + 9);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = from[e];
                     if (kScores) {
                         if (same_lead && j0 >= 0 && j0 + 8 <= end) {
                             float y[8];
@@ -567,9 +552,13 @@ int launch_forward(const Geometry& G, const Borders& B, const void* table, int32
     const int vecs = (G.k_len + kUnit - 1 + 7) / 8;
     int log2 = 0;
     while (log2 < 5 && (1 << log2) < vecs) ++log2;
-    // blocks of at least 64 K places: the line by distance is laid out once in each
+    // blocks of at least 64 K places, and 16 for each of the line, which is laid out in each
+    // (512 buckets up to 8192, 32 x 2048 x 2048: 185 us, 265 without the latter)
+    const int last = B.at[B.n - 1];
+    const int span = B.both ? 2 * last : last;
     const int per_pass = kThreads >> log2;
-    int64_t rows = (65536 + G.k_len - 1) / G.k_len;
+    const int64_t least = std::max<int64_t>(65536, 16 * line_places(span));
+    int64_t rows = (least + G.k_len - 1) / G.k_len;
     rows = (rows + per_pass - 1) / per_pass * per_pass;
     if (rows > G.q_len) rows = G.q_len;
     const int64_t tiles = (G.q_len + rows - 1) / rows;
@@ -578,21 +567,18 @@ int launch_forward(const Geometry& G, const Borders& B, const void* table, int32
     const int same = scores && ((reinterpret_cast<uintptr_t>(scores) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
                      (G.in_stride - G.out_stride) % kUnit == 0 &&
                      (G.in_plane - G.out_plane) % kUnit == 0;
-    const int last = B.at[B.n - 1];
-    const int span = B.both ? 2 * last : last;
-    const int copies = span <= kMostCopied ? 4 : 1;
+    const size_t bytes = 4 * static_cast<size_t>(line_places(span));
     auto start = [&](auto kernel) {
         // the limit that every block has without asking is 48 KB
-        if (copies == 1 && !allow_shared(reinterpret_cast<const void*>(kernel),
-                                         4 * static_cast<size_t>(line_places(2 * kMaxDistance))))
+        if (bytes > 48 * 1024 && !allow_shared(reinterpret_cast<const void*>(kernel),
+                                               4 * static_cast<size_t>(line_places(2 * kMaxDistance))))
             return ZERO_ECUDA;
-        kernel<<<static_cast<unsigned>(blocks), kThreads, 4 * static_cast<size_t>(line_places(span)) * copies,
-                 stream>>>(G, B, table, table_type, static_cast<const T*>(scores), static_cast<T*>(out),
-                           log2, static_cast<int>(rows), static_cast<int>(tiles), same);
+        kernel<<<static_cast<unsigned>(blocks), kThreads, bytes, stream>>>(
+            G, B, table, table_type, static_cast<const T*>(scores), static_cast<T*>(out), log2,
+            static_cast<int>(rows), static_cast<int>(tiles), same);
         return cuda_status(cudaGetLastError());
     };
-    if (scores) return copies == 4 ? start(forward_kernel<T, true, 4>) : start(forward_kernel<T, true, 1>);
-    return copies == 4 ? start(forward_kernel<T, false, 4>) : start(forward_kernel<T, false, 1>);
+    return scores ? start(forward_kernel<T, true>) : start(forward_kernel<T, false>);
 }
 
 constexpr int64_t kResident = 152 * 3; // blocks at once
@@ -647,8 +633,11 @@ int launch_backward(const Geometry& G, const Borders& B, const Split& S, const v
                    (G.q_len - 1) * G.in_stride + G.k_len;
     constexpr int kUnit = 16 / sizeof(T);
     const dim3 grid(static_cast<unsigned>(S.parts), static_cast<unsigned>(G.heads));
-    if (aligned16(dout) && G.in_stride % kUnit == 0 && G.in_plane % kUnit == 0)
-        backward_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(G, B, S, from, end, partial);
+    // 4 x 32 x 2048 x 2048 bf16: 179 us, by the code for any row 210; fp32 (half the batch) takes
+    // 174 by that and would take 178
+    if (sizeof(T) == 2 && aligned16(dout) && G.in_stride % kUnit == 0 && G.in_plane % kUnit == 0)
+        backward_kernel<Bf16, true><<<grid, 32 * kWarps, 0, stream>>>(
+            G, B, S, reinterpret_cast<const Bf16*>(from), reinterpret_cast<const Bf16*>(end), partial);
     else
         backward_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(G, B, S, from, end, partial);
     return cuda_status(cudaGetLastError());
