@@ -23,13 +23,22 @@ __device__ __forceinline__ Run run_of(const Layout& H, int64_t i)
     return r;
 }
 
-// Rows 0 .. rows - 1 by kAhead, the next ones loaded before the last ones are used; without a
-// branch between rows.
-template <int kAhead, typename R, typename Fetch, typename Use>
+// Rows 0 .. rows - 1 by kAhead, without a branch between those.  kNext: the next ones are
+// loaded before the last ones are used.  On 32 x 4096 x 640 bf16 the gradient's sums take 80 us
+// by four and 95 by two and the next two; its result 110 and 95.
+template <int kAhead, bool kNext, typename R, typename Fetch, typename Use>
 __device__ __forceinline__ void over_rows(int rows, Fetch fetch, Use use)
 {
     int k = 0;
-    if (rows >= kAhead) {
+    if constexpr (!kNext) {
+        for (; k + kAhead <= rows; k += kAhead) {
+            R r[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(k + i, r[i]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) use(k + i, r[i]);
+        }
+    } else if (rows >= kAhead) {
         R a[kAhead], b[kAhead];
         auto load = [&](R(&r)[kAhead], int from) {
             if (from + kAhead > rows) return;
@@ -155,7 +164,7 @@ apply_kernel(const __grid_constant__ Layout H, const T* x, const void* __restric
             v[j] = activated2<kAct>(dev::fma2(dev::add2(v[j], minus_mean[j]), a[j], b[j]));
         store_row<kFlat>(H, h, k, yp, H.y_sample, H.y_stride, v);
     };
-    over_rows<sizeof(T) == 2 ? 2 : 1, Raw8<T>>(h.rows, [&](int k, Raw8<T>& raw) {
+    over_rows<sizeof(T) == 2 ? 2 : 1, true, Raw8<T>>(h.rows, [&](int k, Raw8<T>& raw) {
         load_row<kFlat, true>(H, h, k, xp, H.x_sample, H.x_stride, raw);
     }, put);
 }
@@ -214,7 +223,7 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
             float2 s[4], q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = q[j] = make_float2(0.0f, 0.0f);
-            over_rows<sizeof(T) == 2 ? 2 : 1, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
+            over_rows<sizeof(T) == 2 ? 4 : 2, false, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
                 load_row<kFlat, false>(H, h, k, xp, H.x_sample, H.x_stride, r.x);
                 load_row<kFlat, false>(H, h, k, dp, H.y_sample, H.y_stride, r.d);
             }, [&](int k, const Pair<T>& r) {
@@ -308,7 +317,7 @@ apply_gradient_kernel(const __grid_constant__ Layout H, const T* __restrict__ x,
     const T* xp = x + (row0 + rg) * H.x_stride + run.slab * H.width + lane * 8;
     const T* dp = dy + (row0 + rg) * H.y_stride + run.slab * H.width + lane * 8;
     T* out = dx + (row0 + rg) * H.x_stride + run.slab * H.width + lane * 8;
-    over_rows<sizeof(T) == 2 ? 2 : 1, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
+    over_rows<sizeof(T) == 2 ? 2 : 1, true, Pair<T>>(h.rows, [&](int k, Pair<T>& r) {
         load_row<kFlat, true>(H, h, k, xp, H.x_sample, H.x_stride, r.x);
         load_row<kFlat, true>(H, h, k, dp, H.y_sample, H.y_stride, r.d);
     }, [&](int k, const Pair<T>& r) {
