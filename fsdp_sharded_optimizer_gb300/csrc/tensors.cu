@@ -18,6 +18,13 @@
 // squares of a chunk in fp32 (eight pairwise, then eight such sums) and adds that
 // to an fp64 sum; eight squares whose sum leaves [1e-25, 1e30] are summed in fp64
 // at once, so the norm neither overflows nor loses small gradients.
+//
+// What bounds it: HBM.  The gradients are needed twice, so the least is their bytes once and
+// the result's, and what the L2 does not keep between the passes is read again; the scaling
+// therefore starts at the end of the list, with loads that may hit.  200 tensors of 1.03 G fp32
+// elements to bf16: 1,478 us, 7.0 TB/s of 10.3 GB with both reads (by evict-first loads 1,532);
+// 182 of 124 M bf16: 121 us, 6.1 TB/s of 742 MB; 32 of 128 K fp32: 6.9 us, two launches (9.5
+// with chunks of 16 K elements: fewer blocks, each longer).
 #include "typed.cuh"
 #include "zero_internal.h"
 
@@ -33,8 +40,9 @@ constexpr int64_t kChunk = int64_t(kThreads) * kVecs * 8;
 // Lists of fewer elements are cut into chunks of one vector a thread: more blocks, each done
 // sooner.
 constexpr int64_t kSmallList = int64_t(kNormBlocks) * kThreads * 8;
-// A list of up to kFew tensors fits the 4 KB of parameters that every launch
-// carries; longer ones take the 32 KB form, and further launches.
+// A list of up to kFew tensors fits 4 KB of parameters; longer ones take the 32 KB form, and
+// further launches.  The device takes as long with either; 32 tensors' call takes the host 8.5 us,
+// and 11.9 in the long form.
 constexpr int kFew = 120, kMany = 1000;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxLaunchChunks = int64_t(1) << 30;

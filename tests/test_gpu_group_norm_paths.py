@@ -14,6 +14,8 @@ CASES = [
     dict(N=7, P=6000, C=64, G=8, ragged=True), dict(N=5, P=5000, C=72, G=9, ragged=True, act="gelu"),
     dict(N=2, P=3000, C=640, G=32, pad=16), dict(N=3, P=7000, C=64, G=2, type="f32", ragged=True),
     dict(N=2, P=6000, C=32, G=8, act="none", type="f32"), dict(N=2, P=9000, C=24, G=6, act="gelu"),
+    # as many groups as a slab has channels: the most shared memory
+    dict(N=2, P=3000, C=2048, G=2048), dict(N=1, P=2500, C=2048, G=1024, type="f32", act="none"),
     # along a sample
     dict(N=7, P=5001, C=81, G=3, ragged=True, act="gelu"), dict(N=3, P=9001, C=19, G=1, type="f32", ragged=True),
     dict(N=2, P=8191, C=64, G=8, offset=3), dict(N=3, P=20001, C=5, G=5), dict(N=2, P=7001, C=21, G=3, act="none"),
