@@ -514,8 +514,9 @@ extern "C" int zero_group_norm_backward(const zero_group_norm_t* norm, const voi
         const int status = norm->type == ZERO_TYPE_BF16 ? gn::backward_by_act<gn::Bf16>(c, p)
                                                         : gn::backward_by_act<float>(c, p);
         if (status != ZERO_OK || (!dweight && !dbias)) return status;
-        return gn::launch(true, gn::sum_blocks_kernel, (norm->channels + gn::kSumChannels - 1) / gn::kSumChannels, 0, stream, p.H, static_cast<const float2*>(scratch),
-                          static_cast<int>(p.grid / p.H.slabs), dweight, dbias, norm->grad_type);
+        return gn::launch(true, gn::sum_blocks_kernel, (norm->channels + gn::kSumChannels - 1) / gn::kSumChannels, 0,
+                          stream, p.H, static_cast<const float2*>(scratch), static_cast<int>(p.grid / p.H.slabs),
+                          dweight, dbias, norm->grad_type);
     }
     return any && gn::passes_take(c) ? gn::passes_backward(c) : gn::single_backward(c);
 }
