@@ -1,7 +1,7 @@
 // group_norm_single.cu -- the group norm a channel at a time, for rows that 16-byte accesses
 // cannot reach (channel slices at odd places, tensors unequally far behind a boundary, odd
 // widths above 256).  A thread takes a channel and every row_groups-th row of a run; sums
-// are [samples][chunks][channels], joined by groups in a second kernel.  Loads of 2 or 4 bytes:
+// are [samples][chunks][channels], joined by runs and then by groups.  Loads of 2 or 4 bytes:
 // 32 x 4096 x 640 bf16, which does not come here, would take 289 us, its gradient 361.
 #include "group_norm.cuh"
 
@@ -43,6 +43,18 @@ __device__ __forceinline__ Spot spot_of(const Grid& G)
     return s;
 }
 
+// Mean of `count` parts of `size` values each and the squares about it, from the squares about a
+// value `near` it and from rest, the sum of the parts' means less `near`.  A sum of the means
+// themselves would round by 2^-24 of the mean at every step, and the same way where they are
+// alike; these differences leave nothing large to round.  (Parts of unequal sizes: their
+// differences weighted, count the values of all, size 1.)
+__device__ __forceinline__ float2 corrected(float near, float squares, float rest, float count, float size)
+{
+    const float d = rest / count;
+    const float m2 = fmaf(-size * rest, d, squares);
+    return make_float2(near + d, m2 < 0.0f ? 0.0f : m2); // NaN stays
+}
+
 // Mean and squares about it of each channel in each run.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -72,23 +84,71 @@ single_stats_kernel(const __grid_constant__ Grid G, const T* __restrict__ x, flo
     means[threadIdx.x] = mean;
     squares[threadIdx.x] = square;
     __syncthreads();
-    if (p.rows > 0 && p.rg == 0) { // the row groups joined
-        float sum = 0.0f, m2 = 0.0f;
+    if (p.rows > 0 && p.rg == 0) { // the row groups joined, about this thread's own mean
+        float sum = 0.0f, m2 = 0.0f, rest = 0.0f;
         auto size = [&](int r) { return static_cast<float>((p.rows - r + G.row_groups - 1) / G.row_groups); };
         const int live = min(G.row_groups, p.rows);
-        for (int r = 0; r < live; ++r) sum = fmaf(size(r), means[r * G.lanes + threadIdx.x], sum);
-        const float all = sum / static_cast<float>(p.rows);
+        for (int r = 1; r < live; ++r) sum = fmaf(size(r), means[r * G.lanes + threadIdx.x] - mean, sum);
+        const float count = static_cast<float>(p.rows);
+        mean += sum / count;
         for (int r = 0; r < live; ++r) {
-            const float d = means[r * G.lanes + threadIdx.x] - all;
-            m2 += fmaf(size(r) * d, d, squares[r * G.lanes + threadIdx.x]);
+            const float d = means[r * G.lanes + threadIdx.x] - mean, n = size(r);
+            rest = fmaf(n, d, rest);
+            m2 += fmaf(n * d, d, squares[r * G.lanes + threadIdx.x]);
         }
-        partial[(static_cast<int64_t>(p.n) * G.chunks + p.chunk) * G.channels + p.c] = make_float2(all, m2);
+        partial[(static_cast<int64_t>(p.n) * G.chunks + p.chunk) * G.channels + p.c] = corrected(mean, m2, rest, count, 1.0f);
     }
 }
 
-// A warp joins the channels and runs of one group of one sample.
+// The runs of 32 channels of samples joined, by a warp every kWarps-th run of each.
 __global__ void __launch_bounds__(kThreads)
-single_join_kernel(const __grid_constant__ Grid G, const float2* __restrict__ partial, float eps,
+single_runs_kernel(const __grid_constant__ Grid G, const float2* __restrict__ partial, float2* __restrict__ joined)
+{
+    __shared__ float sums[kWarps][32], squares[kWarps][32], rests[kWarps][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const bool live = at < static_cast<int64_t>(G.samples) * G.channels;
+    const int n = live ? static_cast<int>(at / G.channels) : 0;
+    const int len = live ? length_of(G, n) : 0, chunks = (len + G.rows - 1) / G.rows;
+    const float2* from = partial + static_cast<int64_t>(n) * G.chunks * G.channels + (at - static_cast<int64_t>(n) * G.channels);
+    const float count = static_cast<float>(len), by = len > 0 ? 1.0f / count : 0.0f;
+    const float shift = len > 0 ? from->x : 0.0f;
+    auto over = [&](auto f) { // f(rows of the run, its mean and squares)
+#pragma unroll 4
+        for (int k = warp; k < chunks; k += kWarps)
+            f(static_cast<float>(min(G.rows, len - k * G.rows)), from[static_cast<int64_t>(k) * G.channels]);
+    };
+    float sum = 0.0f, m2 = 0.0f, rest = 0.0f;
+    over([&](float rows, float2 v) { sum = fmaf(rows, v.x - shift, sum); });
+    sums[warp][lane] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sums[w][lane];
+    const float mean = fmaf(sum, by, shift);
+    over([&](float rows, float2 v) {
+        const float d = v.x - mean;
+        rest = fmaf(rows, d, rest);
+        m2 += fmaf(rows * d, d, v.y);
+    });
+    squares[warp][lane] = m2;
+    rests[warp][lane] = rest;
+    __syncthreads();
+    if (warp > 0 || len == 0) return;
+    m2 = rest = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        m2 += squares[w][lane];
+        rest += rests[w][lane];
+    }
+    joined[at] = corrected(mean, m2, rest, count, 1.0f);
+}
+
+// A warp joins the channels of one group of one sample.
+__global__ void __launch_bounds__(kThreads)
+single_join_kernel(const __grid_constant__ Grid G, const float2* __restrict__ channels, float eps,
                    float2* __restrict__ stats)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -97,26 +157,28 @@ single_join_kernel(const __grid_constant__ Grid G, const float2* __restrict__ pa
     const int lane = threadIdx.x & 31;
     if (unit >= static_cast<int64_t>(G.samples) * G.groups) return;
     const int n = static_cast<int>(unit / G.groups), g = static_cast<int>(unit - static_cast<int64_t>(n) * G.groups);
-    const int len = length_of(G, n), chunks = (len + G.rows - 1) / G.rows;
-    const float2* from = partial + static_cast<int64_t>(n) * G.chunks * G.channels + g * G.per;
-    auto over = [&](auto f) { // f(rows of the run, its mean and squares)
-        for (int k = 0; k < chunks; ++k) {
-            const float rows = static_cast<float>(min(G.rows, len - k * G.rows));
-#pragma unroll 4
-            for (int c = lane; c < G.per; c += 32) f(rows, from[static_cast<int64_t>(k) * G.channels + c]);
+    const float len = static_cast<float>(length_of(G, n)), per = static_cast<float>(G.per);
+    float2 all = make_float2(0.0f, 0.0f);
+    if (len > 0.0f) {
+        const float2* from = channels + static_cast<int64_t>(n) * G.channels + g * G.per;
+        const float shift = from->x;
+        float sum = 0.0f, m2 = 0.0f, rest = 0.0f;
+#pragma unroll 8
+        for (int c = lane; c < G.per; c += 32) sum += from[c].x - shift;
+        sum = sum_lanes(sum, 32);
+        const float mean = shift + sum / per;
+#pragma unroll 8
+        for (int c = lane; c < G.per; c += 32) {
+            const float2 v = from[c];
+            const float d = v.x - mean;
+            rest += d;
+            m2 += fmaf(len * d, d, v.y);
         }
-    };
-    const float count = static_cast<float>(len) * static_cast<float>(G.per);
-    float sum = 0.0f, m2 = 0.0f;
-    over([&](float rows, float2 v) { sum = fmaf(rows, v.x, sum); });
-    sum = sum_lanes(sum, 32);
-    const float mean = len > 0 ? sum / count : 0.0f;
-    over([&](float rows, float2 v) {
-        const float d = v.x - mean;
-        m2 += fmaf(rows * d, d, v.y);
-    });
-    m2 = sum_lanes(m2, 32);
-    if (lane == 0) stats[unit] = make_float2(mean, rstd_of(count, m2, eps));
+        m2 = sum_lanes(m2, 32);
+        rest = sum_lanes(rest, 32);
+        all = corrected(mean, m2, rest, per, len);
+    }
+    if (lane == 0) stats[unit] = make_float2(all.x, rstd_of(len * per, all.y, eps));
 }
 
 template <typename T, int kAct>
@@ -336,9 +398,13 @@ int forward(const Call& c)
     const auto* x = static_cast<const T*>(c.x);
     int rc = ZERO_OK;
     if (blocks > 0) rc = launch(false, single_stats_kernel<T>, blocks, 0, c.stream, G, x, s.partial);
+    const bool runs = G.chunks > 1; // else the one run's sums are the channels'
+    if (rc == ZERO_OK && runs)
+        rc = launch(true, single_runs_kernel, (static_cast<int64_t>(G.samples) * G.channels + 31) / 32, 0, c.stream, G,
+                    s.partial, s.sums);
     if (rc == ZERO_OK)
-        rc = launch(blocks > 0, single_join_kernel, (units + kWarps - 1) / kWarps, 0, c.stream, G, s.partial,
-                    static_cast<float>(c.norm->eps), stats);
+        rc = launch(blocks > 0, single_join_kernel, (units + kWarps - 1) / kWarps, 0, c.stream, G,
+                    runs ? s.sums : s.partial, static_cast<float>(c.norm->eps), stats);
     if (rc == ZERO_OK && blocks > 0)
         rc = launch(true, single_apply_kernel<T, kAct>, blocks, 0, c.stream, G, x, c.weight, c.bias,
                     c.norm->param_type, stats, static_cast<T*>(c.y));
