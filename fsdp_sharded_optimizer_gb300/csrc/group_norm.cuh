@@ -343,6 +343,18 @@ __device__ __forceinline__ void over_segments(const Layout& H, int lead, const i
     }
 }
 
+// Mean of `count` parts of `size` values each and the squares about it, from the squares about a
+// value `near` it and from rest, the sum of the parts' means less `near`.  A sum of the means
+// themselves would round by 2^-24 of the mean at every step, and the same way where they are
+// alike; these differences leave nothing large to round.  (Parts of unequal sizes: their
+// differences weighted, count the values of all, size 1.)
+__device__ __forceinline__ float2 corrected(float near, float squares, float rest, float by, float size)
+{
+    const float d = rest * by;
+    const float m2 = fmaf(-size * rest, d, squares);
+    return make_float2(near + d, m2 < 0.0f ? 0.0f : m2); // NaN stays
+}
+
 // In shared memory: words [segments][kThreads] each, and the groups of first channels.
 struct Segments {
     float *a, *b, *c;
@@ -448,20 +460,22 @@ __device__ __forceinline__ void sum_rows(const Layout& H, const Here& h, int rg,
         }
         return;
     }
-    const float m0 = n0 > 0.0f ? sum0 / n0 : 0.0f, m1 = n1 > 0.0f ? sum1 / n1 : 0.0f;
-    float q0 = 0.0f, q1 = 0.0f;
+    const float by0 = n0 > 0.0f ? 1.0f / n0 : 0.0f, by1 = n1 > 0.0f ? 1.0f / n1 : 0.0f;
+    const float m0 = sum0 * by0, m1 = sum1 * by1;
+    float q0 = 0.0f, q1 = 0.0f, rest0 = 0.0f, rest1 = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const bool two = second & (1u << e);
-        const float d = of_pair(s, e) - (two ? m1 : m0);
-        const float add = size[e] > 0.0f ? fmaf(size[e] * d, d, of_pair(q, e)) : 0.0f;
+        const float d = of_pair(s, e) - (two ? m1 : m0), sized = size[e] * d;
+        const float add = size[e] > 0.0f ? fmaf(sized, d, of_pair(q, e)) : 0.0f;
         if (two)
-            q1 += add;
+            q1 += add, rest1 += sized;
         else
-            q0 += add;
+            q0 += add, rest0 += sized;
     }
-    S.a[t] = m0, S.b[t] = q0, S.c[t] = n0;
-    S.a[kThreads + t] = m1, S.b[kThreads + t] = q1, S.c[kThreads + t] = n1;
+    const float2 one = corrected(m0, q0, rest0, by0, 1.0f), other = corrected(m1, q1, rest1, by1, 1.0f);
+    S.a[t] = one.x, S.b[t] = one.y, S.c[t] = n0;
+    S.a[kThreads + t] = other.x, S.b[kThreads + t] = other.y, S.c[kThreads + t] = n1;
     S.firsts[t] = g;
 }
 
@@ -481,14 +495,20 @@ __device__ __forceinline__ void join_groups(const Layout& H, int lead, const Seg
             });
         count = sum_lanes(count, gl);
         sum = sum_lanes(sum, gl);
-        const float mean = count > 0.0f ? sum / count : 0.0f;
+        const float by = count > 0.0f ? 1.0f / count : 0.0f, near = sum * by;
+        float rest = 0.0f;
         if (g < H.slab_groups)
             over_segments<kFlat>(H, lead, S.firsts, g, sub, gl, [&](int i) {
-                const float d = S.a[i] - mean;
-                m2 += S.c[i] > 0.0f ? fmaf(S.c[i] * d, d, S.b[i]) : 0.0f;
+                const float d = S.a[i] - near, sized = S.c[i] * d;
+                rest += sized;
+                m2 += S.c[i] > 0.0f ? fmaf(sized, d, S.b[i]) : 0.0f;
             });
         m2 = sum_lanes(m2, gl);
-        if (sub == 0 && g < H.slab_groups) done(g, count, mean, m2);
+        rest = sum_lanes(rest, gl);
+        if (sub == 0 && g < H.slab_groups) {
+            const float2 all = corrected(near, m2, rest, by, 1.0f);
+            done(g, count, all.x, all.y);
+        }
     }
 }
 

@@ -122,15 +122,19 @@ join_stats_kernel(const __grid_constant__ Layout H, const float4* __restrict__ p
     }
     count = sum_lanes(count, 32);
     sum = sum_lanes(sum, 32);
-    const float mean = count > 0.0f ? sum / count : 0.0f;
+    const float by = count > 0.0f ? 1.0f / count : 0.0f, near = sum * by;
+    float rest = 0.0f;
 #pragma unroll 4
     for (int k = lane; k < entries; k += 32) {
         const float4 v = from[k];
-        const float d = v.x - mean;
-        m2 += v.z > 0.0f ? fmaf(v.z * d, d, v.y) : 0.0f;
+        const float d = v.x - near, sized = v.z * d;
+        rest += sized;
+        m2 += v.z > 0.0f ? fmaf(sized, d, v.y) : 0.0f;
     }
     m2 = sum_lanes(m2, 32);
-    if (lane == 0) stats[unit] = make_float2(mean, rstd_of(count, m2, eps));
+    rest = sum_lanes(rest, 32);
+    const float2 all = corrected(near, m2, rest, by, 1.0f);
+    if (lane == 0) stats[unit] = make_float2(all.x, rstd_of(count, all.y, eps));
 }
 
 // A slab's values by group (of which parts share one where groups are split).

@@ -43,18 +43,6 @@ __device__ __forceinline__ Spot spot_of(const Grid& G)
     return s;
 }
 
-// Mean of `count` parts of `size` values each and the squares about it, from the squares about a
-// value `near` it and from rest, the sum of the parts' means less `near`.  A sum of the means
-// themselves would round by 2^-24 of the mean at every step, and the same way where they are
-// alike; these differences leave nothing large to round.  (Parts of unequal sizes: their
-// differences weighted, count the values of all, size 1.)
-__device__ __forceinline__ float2 corrected(float near, float squares, float rest, float count, float size)
-{
-    const float d = rest / count;
-    const float m2 = fmaf(-size * rest, d, squares);
-    return make_float2(near + d, m2 < 0.0f ? 0.0f : m2); // NaN stays
-}
-
 // Mean and squares about it of each channel in each run.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -89,14 +77,14 @@ single_stats_kernel(const __grid_constant__ Grid G, const T* __restrict__ x, flo
         auto size = [&](int r) { return static_cast<float>((p.rows - r + G.row_groups - 1) / G.row_groups); };
         const int live = min(G.row_groups, p.rows);
         for (int r = 1; r < live; ++r) sum = fmaf(size(r), means[r * G.lanes + threadIdx.x] - mean, sum);
-        const float count = static_cast<float>(p.rows);
-        mean += sum / count;
+        const float by = 1.0f / static_cast<float>(p.rows);
+        mean = fmaf(sum, by, mean);
         for (int r = 0; r < live; ++r) {
             const float d = means[r * G.lanes + threadIdx.x] - mean, n = size(r);
             rest = fmaf(n, d, rest);
             m2 += fmaf(n * d, d, squares[r * G.lanes + threadIdx.x]);
         }
-        partial[(static_cast<int64_t>(p.n) * G.chunks + p.chunk) * G.channels + p.c] = corrected(mean, m2, rest, count, 1.0f);
+        partial[(static_cast<int64_t>(p.n) * G.chunks + p.chunk) * G.channels + p.c] = corrected(mean, m2, rest, by, 1.0f);
     }
 }
 
@@ -113,7 +101,7 @@ single_runs_kernel(const __grid_constant__ Grid G, const float2* __restrict__ pa
     const int n = live ? static_cast<int>(at / G.channels) : 0;
     const int len = live ? length_of(G, n) : 0, chunks = (len + G.rows - 1) / G.rows;
     const float2* from = partial + static_cast<int64_t>(n) * G.chunks * G.channels + (at - static_cast<int64_t>(n) * G.channels);
-    const float count = static_cast<float>(len), by = len > 0 ? 1.0f / count : 0.0f;
+    const float by = len > 0 ? 1.0f / static_cast<float>(len) : 0.0f;
     const float shift = len > 0 ? from->x : 0.0f;
     auto over = [&](auto f) { // f(rows of the run, its mean and squares)
 #pragma unroll 4
@@ -143,7 +131,7 @@ single_runs_kernel(const __grid_constant__ Grid G, const float2* __restrict__ pa
         m2 += squares[w][lane];
         rest += rests[w][lane];
     }
-    joined[at] = corrected(mean, m2, rest, count, 1.0f);
+    joined[at] = corrected(mean, m2, rest, by, 1.0f);
 }
 
 // A warp joins the channels of one group of one sample.
@@ -166,7 +154,7 @@ single_join_kernel(const __grid_constant__ Grid G, const float2* __restrict__ ch
 #pragma unroll 8
         for (int c = lane; c < G.per; c += 32) sum += from[c].x - shift;
         sum = sum_lanes(sum, 32);
-        const float mean = shift + sum / per;
+        const float by = 1.0f / per, mean = fmaf(sum, by, shift);
 #pragma unroll 8
         for (int c = lane; c < G.per; c += 32) {
             const float2 v = from[c];
@@ -176,7 +164,7 @@ single_join_kernel(const __grid_constant__ Grid G, const float2* __restrict__ ch
         }
         m2 = sum_lanes(m2, 32);
         rest = sum_lanes(rest, 32);
-        all = corrected(mean, m2, rest, per, len);
+        all = corrected(mean, m2, rest, by, len);
     }
     if (lane == 0) stats[unit] = make_float2(all.x, rstd_of(len * per, all.y, eps));
 }

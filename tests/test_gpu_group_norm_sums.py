@@ -47,3 +47,34 @@ def test_large_mean_a_channel_at_a_time(case, mean):
     _, y = T.place((c.N, c.P, c.C), c.type, c.pad, c.offset, None)
     Z.zero_group_norm_forward(c.x, y, stats, c.scr(), act="none", groups=c.G, eps=c.eps, lengths=c.lengths)
     check_statistics(c, stats)
+
+
+HELD = [dict(N=2, P=300, C=64, G=8), dict(N=3, P=700, C=45, G=3, ragged=True), dict(N=1, P=200, C=96, G=24),
+        dict(N=5, P=1, C=4096, G=32), dict(N=400, P=9, C=12, G=6), dict(N=1, P=40, C=2048, G=1)]
+PASSES = [dict(N=1, P=300000, C=64, G=1), dict(N=2, P=9000, C=640, G=32), dict(N=7, P=6000, C=72, G=9, ragged=True),
+          dict(N=2, P=6000, C=24, G=6), dict(N=2, P=300, C=4096, G=1)]
+ALONG = [dict(N=1, P=200000, C=33, G=1), dict(N=7, P=5001, C=81, G=3, ragged=True), dict(N=3, P=20001, C=5, G=5),
+         dict(N=2, P=8191, C=64, G=8, offset=3)]
+
+
+@pytest.mark.parametrize("mean", [1000.3, -500.1])
+@pytest.mark.parametrize("case", HELD + PASSES + ALONG, ids=ids(HELD + PASSES + ALONG))
+def test_large_mean(case, mean):
+    test_large_mean_a_channel_at_a_time(case, mean)
+
+
+@pytest.mark.parametrize("value", [1000.3, -0.1, 7e-5])
+@pytest.mark.parametrize("case", SINGLE + HELD + PASSES + ALONG, ids=ids(SINGLE + HELD + PASSES + ALONG))
+def test_groups_of_one_value(case, value):
+    """A mean of parts that all are v is v again: a sum of them comes to v (1 + k u) for a few k,
+    all differences from that are -v k u exactly, their mean the same up to its own rounding, and v
+    is the number next to the corrected one.  Then every x - mean is 0, and y is the bias."""
+    c = T.Case(type="f32", act="none", **case)
+    c.x.fill_(value)
+    stats = torch.empty((c.N, c.G, 2), device="cuda")
+    _, y = T.place((c.N, c.P, c.C), c.type, c.pad, c.offset, None)
+    Z.zero_group_norm_forward(c.x, y, stats, c.scr(), act="none", bias=c.b, eps=c.eps, lengths=c.lengths)
+    for n in range(c.N):
+        if c.len[n]:
+            assert torch.all(stats[n, :, 0] == c.x[n, 0, 0]), "mean"
+            assert torch.all(y[n, :c.len[n]] == c.b.float()), "y"
