@@ -140,7 +140,7 @@ held_forward_kernel(const __grid_constant__ Layout H, const T* x, const void* __
             dev::unpack8(raw, v);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = activated2<kAct>(dev::fma2(dev::add2(v[i], minus_mean[i]), a[i], b[i]));
+                v[i] = activated2<T, kAct>(dev::fma2(dev::add2(v[i], minus_mean[i]), a[i], b[i]));
             store_row<kFlat>(H, h, k, yp, H.y_sample, H.y_stride, v);
             if (k < rows2) copy(next, k);
         }
@@ -213,7 +213,7 @@ held_backward_kernel(const __grid_constant__ Layout H, const T* x, const T* dy, 
                 read_slot(place, rd);
                 dev::unpack8(rx, v);
                 dev::unpack8(rd, d);
-                form_d<kAct>(v, d, minus_mean, a, b);
+                form_d<T, kAct>(v, d, minus_mean, a, b);
                 if (kFlat && !whole<kFlat>(H, h, k))
                     outside(H, h, k, [&](int e) { of_pair(v, e) = of_pair(d, e) = 0.0f; });
                 place[0] = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);

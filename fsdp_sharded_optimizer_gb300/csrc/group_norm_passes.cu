@@ -173,7 +173,7 @@ apply_kernel(const __grid_constant__ Layout H, const T* x, const void* __restric
         dev::unpack8(raw, v);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[j] = activated2<kAct>(dev::fma2(dev::add2(v[j], minus_mean[j]), a[j], b[j]));
+            v[j] = activated2<T, kAct>(dev::fma2(dev::add2(v[j], minus_mean[j]), a[j], b[j]));
         store_row<kFlat>(H, h, k, yp, H.y_sample, H.y_stride, v);
     };
     over_rows<sizeof(T) == 2 ? 2 : 1, true, Raw8<T>>(h.rows, [&](int k, Raw8<T>& raw) {
@@ -242,7 +242,7 @@ sums_kernel(const __grid_constant__ Layout H, const T* __restrict__ x, const T* 
                 float2 v[4], d[4];
                 dev::unpack8(r.x, v);
                 dev::unpack8(r.d, d);
-                form_d<kAct>(v, d, minus_mean, a, b);
+                form_d<T, kAct>(v, d, minus_mean, a, b);
                 if (kFlat && !whole<kFlat>(H, h, k))
                     outside(H, h, k, [&](int e) { of_pair(v, e) = of_pair(d, e) = 0.0f; });
 #pragma unroll
@@ -336,7 +336,7 @@ apply_gradient_kernel(const __grid_constant__ Layout H, const T* __restrict__ x,
         float2 v[4], d[4];
         dev::unpack8(r.x, v);
         dev::unpack8(r.d, d);
-        form_d<kAct>(v, d, minus_mean, a, b);
+        form_d<T, kAct>(v, d, minus_mean, a, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = dev::fma2(dev::mul2(v[j], rstd[j]), s2[j], dev::fma2(d[j], a[j], s1[j]));
         store_row<kFlat>(H, h, k, out, H.x_sample, H.x_stride, v);

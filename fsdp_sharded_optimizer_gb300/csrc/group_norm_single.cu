@@ -194,7 +194,7 @@ single_apply_kernel(const __grid_constant__ Grid G, const T* x, const void* __re
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (r + k * G.row_groups < p.rows)
-                dev::store1(to + k * y_step, activated<kAct>(fmaf(v[k] - st.x, a, b[0])));
+                dev::store1(to + k * y_step, activated<T, kAct>(fmaf(v[k] - st.x, a, b[0])));
         from += kAhead * x_step;
         to += kAhead * y_step;
     }
@@ -223,7 +223,7 @@ single_sums_kernel(const __grid_constant__ Grid G, const T* __restrict__ x, cons
 #pragma unroll 4
         for (int r = p.rg; r < p.rows; r += G.row_groups, xp += x_step, dp += y_step) {
             const float h = (dev::load1(xp) - st.x) * st.y, dy1 = dev::load1(dp);
-            const float d = kAct ? dy1 * slope<kAct>(fmaf(h, w[0], b[0])) : dy1;
+            const float d = kAct ? dy1 * slope<T, kAct>(fmaf(h, w[0], b[0])) : dy1;
             s += d;
             q = fmaf(d, h, q);
         }
@@ -328,7 +328,7 @@ single_gradient_kernel(const __grid_constant__ Grid G, const T* __restrict__ x, 
         for (int k = 0; k < kAhead; ++k)
             if (r + k * G.row_groups < p.rows) {
                 const float h = (v[k] - st.x) * st.y;
-                const float g = kAct ? d[k] * slope<kAct>(fmaf(h, w[0], b[0])) : d[k];
+                const float g = kAct ? d[k] * slope<T, kAct>(fmaf(h, w[0], b[0])) : d[k];
                 dev::store1(to + k * x_step, st.y * fmaf(-h, m.y, fmaf(g, w[0], -m.x)));
             }
         xp += kAhead * x_step;
