@@ -1052,6 +1052,18 @@ def _tensor_list(tensors):
     return tensors if isinstance(tensors, TensorList) else zero_tensor_list(tensors)
 
 
+def _sources(tensors):
+    """A list that is only read: without destinations, so that tensors may overlap."""
+    if isinstance(tensors, TensorList):
+        return tensors
+    src = list(tensors)
+    array = (zero_tensor_t * len(src))()
+    for i, (e, t) in enumerate(zip(array, src)):
+        what = "tensor %d" % i
+        e.src, e.n, e.src_type = _at(t, what), t.numel(), _type(t, what)
+    return TensorList(array, len(src), src)
+
+
 def _coef(norm_coef):
     if norm_coef.dtype != torch.float32 or norm_coef.numel() < 2:
         raise ValueError("norm_coef must hold two fp32 values")
@@ -1059,9 +1071,10 @@ def _coef(norm_coef):
 
 
 def zero_tensors_sqnorm(tensors, scratch, accumulate=False, stream=None):
-    """Add the squared norm of all tensors (a zero_tensor_list, or tensors) into the
-    partials of zero_grad_sqnorm in `scratch`; zero_clip_coef gives the norm."""
-    t = _tensor_list(tensors)
+    """Add the squared norm of all tensors (a zero_tensor_list, or tensors, which may overlap:
+    one that is listed twice counts twice) into the partials of zero_grad_sqnorm in
+    `scratch`; zero_clip_coef gives the norm."""
+    t = _sources(tensors)
     _check("zero_tensors_sqnorm", lib.zero_tensors_sqnorm(
         t.array, t.n, 1 if accumulate else 0, _at(scratch, "scratch"), scratch.nbytes,
         _raw_stream(stream)))
