@@ -1130,6 +1130,13 @@ def _strided_rows(t, what, shape=None):
     return t.data_ptr(), (cols or 1) if row is None else row
 
 
+def _fits(n, bits, what):
+    """A whole number for a field of so many bits, which ctypes would cut to size."""
+    if not -(1 << bits - 1) <= n < 1 << bits - 1:
+        raise ValueError("%s: %d is out of range" % (what, n))
+    return n
+
+
 def _lengths(t, n, what):
     if t is None:
         return None
@@ -1166,8 +1173,10 @@ def _group_norm_call(x, stats, groups, act):
     if stats is None:
         if groups is None:
             raise ValueError("groups must be given where stats are not")
-        return N, P, C, int(groups), None
-    G = int(groups) if groups is not None else stats.shape[1]
+        return N, P, C, _fits(int(groups), 32, "groups"), None
+    if len(stats.shape) != 3:
+        raise ValueError("stats must be samples x groups x 2")
+    G = _fits(int(groups), 32, "groups") if groups is not None else stats.shape[1]
     if stats.dtype is not torch.float32:
         raise ValueError("stats must be fp32")
     return N, P, C, G, _at(stats, "stats", (N, G, 2))
@@ -1175,7 +1184,8 @@ def _group_norm_call(x, stats, groups, act):
 
 def zero_group_norm_scratch_bytes(samples, positions, channels, groups):
     return _bytes("zero_group_norm_scratch_bytes", lib.zero_group_norm_scratch_bytes(
-        int(samples), int(positions), int(channels), int(groups)))
+        *(_fits(int(n), 64, "a size") for n in (samples, positions, channels)),
+        _fits(int(groups), 32, "groups")))
 
 
 def zero_group_norm_forward(x, y, stats, scratch, weight=None, bias=None, lengths=None,
@@ -1232,7 +1242,8 @@ def _relpos_call(scores, what, table, starts, q_lengths, k_lengths, start, max_d
     B, H, Q, K = sizes
     if len(of_table) != 2 or of_table[1] != H:
         raise ValueError("the table must be buckets x heads")
-    spec = zero_relpos_t(B, H, Q, K, start, max_distance, of_table[0],
+    spec = zero_relpos_t(B, H, Q, K, _fits(start, 64, "start"),
+                         _fits(max_distance, 64, "max_distance"), _fits(of_table[0], 32, "buckets"),
                          1 if bidirectional else 0, 1 if causal else 0, _type(table, "the table"),
                          _type(scores, what))
     return spec, (None if starts is None else _lengths(starts, B, "starts"),
@@ -1261,7 +1272,8 @@ def zero_relpos_forward(table, out, scores=None, start=0, starts=None, q_lengths
 
 def zero_relpos_scratch_bytes(batch, heads, q_len, k_len, buckets):
     return _bytes("zero_relpos_scratch_bytes", lib.zero_relpos_scratch_bytes(
-        int(batch), int(heads), int(q_len), int(k_len), int(buckets)))
+        *(_fits(int(n), 64, "a size") for n in (batch, heads, q_len, k_len)),
+        _fits(int(buckets), 32, "buckets")))
 
 
 def zero_relpos_backward(dout, dtable, scratch, start=0, starts=None, q_lengths=None,
