@@ -1130,9 +1130,12 @@ def _strided_rows(t, what, shape=None):
     return t.data_ptr(), (cols or 1) if row is None else row
 
 
-def _fits(n, bits, what):
-    """A whole number for a field of so many bits, which ctypes would cut to size."""
-    if not -(1 << bits - 1) <= n < 1 << bits - 1:
+# ctypes cuts a number to its field's size: what int32 and int64 fields take at most here.
+_MOST32, _MOST64 = 2 ** 31 - 1, 2 ** 63 - 1
+
+
+def _fits(n, most, what):
+    if not -most <= n <= most:
         raise ValueError("%s: %d is out of range" % (what, n))
     return n
 
@@ -1173,10 +1176,14 @@ def _group_norm_call(x, stats, groups, act):
     if stats is None:
         if groups is None:
             raise ValueError("groups must be given where stats are not")
-        return N, P, C, _fits(int(groups), 32, "groups"), None
-    if len(stats.shape) != 3:
-        raise ValueError("stats must be samples x groups x 2")
-    G = _fits(int(groups), 32, "groups") if groups is not None else stats.shape[1]
+        return N, P, C, _fits(int(groups), _MOST32, "groups"), None
+    if groups is not None:
+        G = _fits(int(groups), _MOST32, "groups")
+    else:
+        of_stats = stats.shape
+        if len(of_stats) != 3:
+            raise ValueError("stats must be samples x groups x 2")
+        G = of_stats[1]
     if stats.dtype is not torch.float32:
         raise ValueError("stats must be fp32")
     return N, P, C, G, _at(stats, "stats", (N, G, 2))
@@ -1184,8 +1191,8 @@ def _group_norm_call(x, stats, groups, act):
 
 def zero_group_norm_scratch_bytes(samples, positions, channels, groups):
     return _bytes("zero_group_norm_scratch_bytes", lib.zero_group_norm_scratch_bytes(
-        *(_fits(int(n), 64, "a size") for n in (samples, positions, channels)),
-        _fits(int(groups), 32, "groups")))
+        *(_fits(int(n), _MOST64, "a size") for n in (samples, positions, channels)),
+        _fits(int(groups), _MOST32, "groups")))
 
 
 def zero_group_norm_forward(x, y, stats, scratch, weight=None, bias=None, lengths=None,
@@ -1242,8 +1249,10 @@ def _relpos_call(scores, what, table, starts, q_lengths, k_lengths, start, max_d
     B, H, Q, K = sizes
     if len(of_table) != 2 or of_table[1] != H:
         raise ValueError("the table must be buckets x heads")
-    spec = zero_relpos_t(B, H, Q, K, _fits(start, 64, "start"),
-                         _fits(max_distance, 64, "max_distance"), _fits(of_table[0], 32, "buckets"),
+    if not (-_MOST64 <= start <= _MOST64 and -_MOST64 <= max_distance <= _MOST64
+            and of_table[0] <= _MOST32):
+        raise ValueError("start, max_distance or the table's buckets are out of range")
+    spec = zero_relpos_t(B, H, Q, K, start, max_distance, of_table[0],
                          1 if bidirectional else 0, 1 if causal else 0, _type(table, "the table"),
                          _type(scores, what))
     return spec, (None if starts is None else _lengths(starts, B, "starts"),
@@ -1272,8 +1281,8 @@ def zero_relpos_forward(table, out, scores=None, start=0, starts=None, q_lengths
 
 def zero_relpos_scratch_bytes(batch, heads, q_len, k_len, buckets):
     return _bytes("zero_relpos_scratch_bytes", lib.zero_relpos_scratch_bytes(
-        *(_fits(int(n), 64, "a size") for n in (batch, heads, q_len, k_len)),
-        _fits(int(buckets), 32, "buckets")))
+        *(_fits(int(n), _MOST64, "a size") for n in (batch, heads, q_len, k_len)),
+        _fits(int(buckets), _MOST32, "buckets")))
 
 
 def zero_relpos_backward(dout, dtable, scratch, start=0, starts=None, q_lengths=None,
