@@ -94,8 +94,9 @@ def test_statistics_see_every_row(case, type):
     assert float((em * c.P * c.per).max()) < 8 / 3
     T.close(stats[..., 0], m.expand(c.N, c.G), em.expand(c.N, c.G), "mean")
     rstd = 1 / torch.sqrt(m - m * m + c.eps)
-    # squares have whole sums less products of thread means: 600 u of them, as elsewhere
-    T.close(stats[..., 1], rstd.expand(c.N, c.G), (304 * U * rstd + em ** 2 * rstd ** 3 / 2).expand(c.N, c.G), "rstd")
+    # as in test_gpu_group_norm_sums.py
+    er = 304 * U + em * rstd + em ** 2 * rstd ** 2 / 2
+    T.close(stats[..., 1], rstd.expand(c.N, c.G), (er * rstd).expand(c.N, c.G), "rstd")
     mean, rstd = (stats[..., i].double().repeat_interleave(c.per, 1)[:, None] for i in (0, 1))
     z = (c.x.double() - mean) * rstd
     T.close(y, z, 3 * U * z.abs(), "y")
