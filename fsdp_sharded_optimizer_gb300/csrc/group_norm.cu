@@ -15,12 +15,23 @@
 //
 // Measured, bf16 with SiLU, microseconds (forward, gradient):
 //                       held          passes        single
-//   1 x 64 x 1280       5.9,  7.8     7.2, 11.5     15,   9.1
-//   16 x 256 x 640      7.6, 12       12,  23       26,  22
-//   64 x 256 x 1280     24,  61       52,  75       51,  83
-//   32 x 1024 x 320     14,  32       30,  34       41,  46
-//   32 x 4096 x 640     -             95, 176       289, 361
-//   64 x 8000 x 81      -             106, 144      141, 168  (passes along a sample)
+//   1 x 64 x 1280       5.8,  7.7     7.2, 11       8.3,  9.2
+//   16 x 256 x 640      7.7, 12       12,  23       17,  22
+//   64 x 256 x 1280     24,  61       53,  70       50,  82
+//   32 x 1024 x 320     14,  32       32,  33       29,  46
+//   32 x 4096 x 640     -             95, 176       196, 363
+//   32 x 16384 x 320    -             184, 329      420, 820
+// and where the channels fill no vectors (passes along a sample):
+//   2 x 300000 x 33     -             62,  68       114, 234
+//   1 x 1000000 x 15    -             82,  60       122, 271
+//   32 x 5000 x 255     -             92, 131       98,  186
+//   64 x 8000 x 81      -             106, 138      97,  169
+//   32 x 16000 x 33     -             90,  63       43,  73
+//   16 x 2000 x 201     -             59,  40       26,  40
+//   64 x 1500 x 27      19,  40       37,  40       17,  21
+// Passes are taken for all of those: up to 4.5 times faster over long samples and in most
+// gradients, up to 2.3 times slower over many samples of few thousand rows and groups, where the
+// joins of their runs cost more than the rows.
 // A sample held by a team of blocks that exchange their sums through global memory (a cooperative
 // launch) read every value once and took longer than two passes: 32 x 16384 x 320 216 us against
 // 184, as a turn's exchange takes longer than its streaming.
